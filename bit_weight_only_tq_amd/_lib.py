@@ -16,7 +16,7 @@ LIB_PATH = os.path.join(HERE, "libtq.so")
 STATUS_NAMES = {
     0: "TQ_OK", 1: "TQ_ERR_NULL", 2: "TQ_ERR_SHAPE", 3: "TQ_ERR_ALIGN", 4: "TQ_ERR_DTYPE",
     5: "TQ_ERR_GROUP", 6: "TQ_ERR_NONFINITE", 7: "TQ_ERR_RANGE", 8: "TQ_ERR_BAD_CODE",
-    9: "TQ_ERR_HIP", 10: "TQ_ERR_PATH", 11: "TQ_ERR_SCRATCH",
+    9: "TQ_ERR_HIP", 10: "TQ_ERR_PATH", 11: "TQ_ERR_SCRATCH", 12: "TQ_ERR_VALUE",
 }
 # tq_dtype
 TQ_F16, TQ_BF16 = 0, 1
@@ -46,6 +46,10 @@ SIGNATURES = {
     "w4a16_gemm_asym": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _sz, _vp,
                                _i32]),
     "w4a16_gemm_asym_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, _i64, _i32]),
+    "tq_paged_plan": (_i32, [_vp, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp,
+                             _vp]),
+    "tq_kv_append": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i64, _i64, _i64, _i64, _vp,
+                            _vp, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i32, _vp, _vp]),
     "tq_diag_stream_read": (_i32, [_vp, _sz, _vp, _i64, _vp]),
     "tq_diag_gemv": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32]),
     "tq_select_path": (_i32, [_i32, _i64, _i64, _i64, _i32]),

@@ -28,7 +28,9 @@ SOURCES = {
     "gemv.hip": [],
     "gemm.hip": [],
     "diag.hip": [],
+    "paged.hip": [],
     "api.cpp": ["-x", "hip"],
+    "api_serving.cpp": ["-x", "hip"],
 }
 
 

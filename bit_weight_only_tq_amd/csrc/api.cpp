@@ -134,6 +134,7 @@ const char* tq_status_str(tq_status s) {
         case TQ_ERR_HIP: return "HIP runtime error or kernel launch failure";
         case TQ_ERR_PATH: return "forced kernel path cannot run this shape";
         case TQ_ERR_SCRATCH: return "the call needs more scratch memory than tq_gemm_noalloc holds";
+        case TQ_ERR_VALUE: return "an argument's value is not allowed";
     }
     return "unknown status";
 }

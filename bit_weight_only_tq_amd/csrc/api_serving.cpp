@@ -1,0 +1,102 @@
+// extern "C" entry points of the serving operators: argument checks, then one
+// launcher call.  See include/tq.h for the contract.  Like the rest of the
+// library they work on the caller's current device and stream and keep no
+// state between calls.
+
+#include "tq.h"
+
+#include <hip/hip_runtime.h>
+
+#include "tq_internal.h"
+
+namespace {
+
+constexpr int64_t kInt32Max = 0x7FFFFFFF;
+
+bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+tq_status from_hip(hipError_t e) { return e == hipSuccess ? TQ_OK : TQ_ERR_HIP; }
+
+// log2 of a page size (a power of two from 16 to 1024), or -1.
+int page_shift(int64_t page_size) {
+    for (int s = 4; s <= 10; ++s)
+        if (page_size == (int64_t)1 << s) return s;
+    return -1;
+}
+
+}  // namespace
+
+extern "C" {
+
+tq_status tq_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, int32_t* page_table, int64_t table_stride,
+                        const int32_t* free_pages, const int32_t* free_head, int64_t B, int64_t width, int64_t n_free,
+                        int64_t T, int64_t page_size, int32_t* cu_q, int32_t* kv_lens, int32_t* positions,
+                        int64_t* slots, int32_t* state, hipStream_t stream) {
+    if (!ctx_lens || !new_lens || !page_table || !free_head || !cu_q || !kv_lens || !state) return TQ_ERR_NULL;
+    if (n_free > 0 && !free_pages) return TQ_ERR_NULL;
+    if (T > 0 && (!positions || !slots)) return TQ_ERR_NULL;
+    if (B <= 0 || B > tq::kPlanMaxRequests || width <= 0 || width > kInt32Max || n_free < 0 || n_free > kInt32Max ||
+        T < 0 || T > kInt32Max)
+        return TQ_ERR_SHAPE;
+    const int shift = page_shift(page_size);
+    if (shift < 0 || table_stride < width) return TQ_ERR_VALUE;
+    if (!aligned(ctx_lens, 4) || !aligned(new_lens, 4) || !aligned(page_table, 4) || !aligned(free_pages, 4) ||
+        !aligned(free_head, 4) || !aligned(cu_q, 4) || !aligned(kv_lens, 4) || !aligned(positions, 4) ||
+        !aligned(slots, 8) || !aligned(state, 4))
+        return TQ_ERR_ALIGN;
+    const tq::PlanArgs a{ctx_lens, new_lens, page_table, table_stride, free_pages, free_head, (int)B,     (int)width,
+                         (int)n_free, (int)T, shift,     cu_q,         kv_lens,    positions, slots, state};
+    return from_hip(tq::launch_paged_plan(a, stream));
+}
+
+tq_status tq_kv_append(const void* q, int64_t q_stride, int64_t q_head, const void* k, int64_t k_stride,
+                       int64_t k_head, const void* v, int64_t v_stride, int64_t v_head, tq_dtype dt, int64_t T,
+                       int64_t Hq, int64_t Hkv, int64_t D, void* k_cache, void* v_cache, int64_t pages,
+                       int64_t page_size, int64_t page_stride, const int64_t* slots, const int32_t* positions,
+                       const float* rope, int64_t rope_rows, int64_t rot, int interleaved, void* q_out,
+                       hipStream_t stream) {
+    if (dt != TQ_F16 && dt != TQ_BF16) return TQ_ERR_DTYPE;
+    if (T < 0 || T > kInt32Max || Hq < 0 || Hq > 4096 || Hkv <= 0 || Hkv > 4096 || D <= 0 || D > 4096 || pages <= 0 ||
+        pages > kInt32Max || rot < 0 || rot > D || rot % 2 != 0)
+        return TQ_ERR_SHAPE;
+    const int shift = page_shift(page_size);
+    if (shift < 0 || page_stride < Hkv * page_size * D) return TQ_ERR_VALUE;
+    if (T == 0) return TQ_OK;
+    if (!k || !v || !k_cache || !v_cache || !slots) return TQ_ERR_NULL;
+    if (Hq > 0 && (!q || !q_out)) return TQ_ERR_NULL;
+    if (rot > 0 && (!rope || !positions)) return TQ_ERR_NULL;
+    if (rot > 0 && rope_rows <= 0) return TQ_ERR_SHAPE;
+    if (!aligned(q, 2) || !aligned(k, 2) || !aligned(v, 2) || !aligned(k_cache, 2) || !aligned(v_cache, 2) ||
+        !aligned(q_out, 2) || !aligned(slots, 8) || !aligned(positions, 4) || !aligned(rope, 4))
+        return TQ_ERR_ALIGN;
+    tq::AppendArgs a;
+    a.q = static_cast<const uint16_t*>(q);
+    a.k = static_cast<const uint16_t*>(k);
+    a.v = static_cast<const uint16_t*>(v);
+    a.q_stride = q_stride;
+    a.q_head = q_head;
+    a.k_stride = k_stride;
+    a.k_head = k_head;
+    a.v_stride = v_stride;
+    a.v_head = v_head;
+    a.bf16 = dt == TQ_BF16 ? 1 : 0;
+    a.T = T;
+    a.Hq = (int)Hq;
+    a.Hkv = (int)Hkv;
+    a.D = (int)D;
+    a.k_cache = static_cast<uint16_t*>(k_cache);
+    a.v_cache = static_cast<uint16_t*>(v_cache);
+    a.pages = pages;
+    a.page_stride = page_stride;
+    a.shift = shift;
+    a.slots = slots;
+    a.positions = positions;
+    a.rope = rope;
+    a.rope_rows = rope_rows;
+    a.rot = (int)rot;
+    a.interleaved = interleaved ? 1 : 0;
+    a.q_out = static_cast<uint16_t*>(q_out);
+    return from_hip(tq::launch_kv_append(a, stream));
+}
+
+}  // extern "C"

@@ -147,4 +147,40 @@ size_t w4_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int compute_unit
 bool w4_prefill_ok(const GemmArgs& a, size_t workspace_bytes);
 hipError_t launch_w4_prefill(const GemmArgs& a, void* workspace, size_t workspace_bytes, hipStream_t s);
 
+// ---- serving operators (paged.hip, attention.hip, sample.hip)
+
+// paged.hip: the plan of a step; arguments as tq_paged_plan.
+constexpr int kPlanMaxRequests = 16384;  // prefix sums of the requests stay in LDS
+struct PlanArgs {
+    const int32_t *ctx, *fresh;
+    int32_t* table;
+    int64_t table_stride;
+    const int32_t *free_pages, *free_head;
+    int B, width, n_free, T, shift;  // page size 1 << shift
+    int32_t *cu_q, *kv_lens, *positions;
+    int64_t* slots;
+    int32_t* state;
+};
+hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t s);
+
+// paged.hip: rotary positions and the cache append; arguments as tq_kv_append.
+struct AppendArgs {
+    const uint16_t *q, *k, *v;
+    int64_t q_stride, q_head, k_stride, k_head, v_stride, v_head;  // elements between tokens and between heads
+    int bf16;
+    int64_t T;
+    int Hq, Hkv, D;  // Hq 0: no queries
+    uint16_t *k_cache, *v_cache;
+    int64_t pages, page_stride;
+    int shift;
+    const int64_t* slots;
+    const int32_t* positions;
+    const float* rope;
+    int64_t rope_rows;
+    int rot, interleaved;
+    uint16_t* q_out;
+    int tokens_per_group = 1;  // set by the launcher
+};
+hipError_t launch_kv_append(const AppendArgs& a, hipStream_t s);
+
 }  // namespace tq

@@ -81,7 +81,8 @@ typedef enum tq_status {
     TQ_ERR_BAD_CODE = 8,   /* unpack: a 2-bit field holds the unused 0b11 */
     TQ_ERR_HIP = 9,        /* a HIP runtime call or kernel launch failed */
     TQ_ERR_PATH = 10,      /* a forced kernel path cannot run this shape */
-    TQ_ERR_SCRATCH = 11    /* tq_gemm_noalloc: the schedule needs more than its scratch */
+    TQ_ERR_SCRATCH = 11,   /* tq_gemm_noalloc: the schedule needs more than its scratch */
+    TQ_ERR_VALUE = 12      /* serving calls: an argument's value is not allowed (page size, strides, scale, window) */
 } tq_status;
 
 typedef enum tq_dtype {
@@ -376,6 +377,79 @@ tq_status w4a16_gemm_asym(const void* A, tq_dtype dt, int64_t M, int64_t N, int6
  */
 size_t w4a16_gemm_asym_workspace_bytes(int64_t M, int64_t N, int64_t K, tq_dtype dt, int64_t group_size,
                                        int with_perm);
+
+/* ------------------------------------------------------ serving operators
+ *
+ * What a serving step of a model with these linear layers runs between the
+ * products: the step's plan over a paged KV cache, the append of its keys and
+ * values, attention over the pages, and the sampling of the next tokens.
+ *
+ * The cache.  Keys and values live in pages of page_size tokens: k_cache and
+ * v_cache are [pages][Hkv][page_size][D] in `dt`, contiguous within a page,
+ * with page_stride elements from one page to the next (both caches alike).
+ * page_size is a power of two from 16 to 1024.  A slot is page * page_size +
+ * offset; request b's token i lies in page page_table[b][i / page_size].
+ *
+ * All calls are asynchronous on `stream`, allocate nothing, never synchronize
+ * and can be captured in a graph.  Lengths, tables, slots and positions are
+ * device data that the host does not see: the kernels check them, and no
+ * value in them makes a call read or write outside the buffers it was given.
+ */
+
+/*
+ * tq_paged_plan - the plan of one step, made on the device.
+ *   ctx_lens   [B] tokens each request has in the cache.
+ *   new_lens   [B] tokens this step adds to each (0 for a request that rests).
+ *   page_table [B] rows of `width` page ids, table_stride elements apart; the
+ *              first ceil(ctx / page_size) entries of a row are the pages the
+ *              request holds.  The entries of the pages it needs now are
+ *              written (-1 where the free list or the row's width ends).
+ *   free_pages [n_free] page ids; the step takes them in request order from
+ *   free_head  [1] on (read only: the new head is state[0], so a step that
+ *              is planned again gives the same plan).
+ *   T          entries of positions and slots, at least the sum of new_lens.
+ *   cu_q       [B + 1] offsets of each request's new tokens (written).
+ *   kv_lens    [B] ctx + new (written).
+ *   positions  [T] position of each new token (written).
+ *   slots      [T] its slot, or -1 where it has no page (written).
+ *   state      [2] free_head after the step, and how many of the step's
+ *              tokens have no slot (written).
+ * Tokens of `positions` and `slots` past the sum of new_lens are padding:
+ * position 0, slot -1, not counted; tokens past T are not written and are
+ * counted.  Negative lengths count as 0, sums are held at 2^31 - 1.
+ * 1 <= B <= 16384 (TQ_ERR_SHAPE).
+ */
+tq_status tq_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, int32_t* page_table, int64_t table_stride,
+                        const int32_t* free_pages, const int32_t* free_head, int64_t B, int64_t width,
+                        int64_t n_free, int64_t T, int64_t page_size, int32_t* cu_q, int32_t* kv_lens,
+                        int32_t* positions, int64_t* slots, int32_t* state, hipStream_t stream);
+
+/*
+ * tq_kv_append - rotary positions and the append to the cache.
+ *   q, k, v    [T][Hq][D], [T][Hkv][D], [T][Hkv][D] in `dt`, with the given
+ *              strides (elements) between tokens and between heads, so the
+ *              parts of a fused projection's output go in as they are.  q may
+ *              be NULL with Hq = 0.
+ *   slots      [T] slot of each token; tokens whose slot is negative or past
+ *              the cache are not stored.  Two tokens of a call must not share
+ *              a slot.
+ *   positions  [T] row of `rope` for each token (may be NULL without rope).
+ *   rope       [rope_rows][rot] fp32, rot / 2 cosines then rot / 2 sines, or
+ *              NULL with rot = 0: nothing is rotated.  rot is even, at most D.
+ *   interleaved  0: dimension i turns with i + rot / 2; 1: 2 i with 2 i + 1.
+ *              The dimensions from rot on are copied.
+ *   q_out      [T][Hq][D] rotated queries, contiguous (written).
+ * A pair (x, y) becomes (x cos - y sin, y cos + x sin) in fp32, rounded once.
+ * A position outside [0, rope_rows) gives NaN in the rotated dimensions.
+ * T = 0 does nothing.  Any D up to 4096; vectors of 16 bytes are used where
+ * sizes, strides and pointers are multiples of them, single values elsewhere.
+ */
+tq_status tq_kv_append(const void* q, int64_t q_stride, int64_t q_head, const void* k, int64_t k_stride,
+                       int64_t k_head, const void* v, int64_t v_stride, int64_t v_head, tq_dtype dt, int64_t T,
+                       int64_t Hq, int64_t Hkv, int64_t D, void* k_cache, void* v_cache, int64_t pages,
+                       int64_t page_size, int64_t page_stride, const int64_t* slots, const int32_t* positions,
+                       const float* rope, int64_t rope_rows, int64_t rot, int interleaved, void* q_out,
+                       hipStream_t stream);
 
 /* ----------------------------------------------------------- measurement
  *
