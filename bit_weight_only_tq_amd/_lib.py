@@ -50,6 +50,10 @@ SIGNATURES = {
                              _vp]),
     "tq_kv_append": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i64, _i64, _i64, _i64, _vp,
                             _vp, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i32, _vp, _vp]),
+    "tq_paged_attention": (_i32, [_vp, _i64, _i64, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _vp, _i64,
+                                  _i64, _vp, _vp, _i64, _i64, _i64, ctypes.c_float, _i64, _i64, _vp, _vp, _vp, _sz,
+                                  _vp]),
+    "tq_paged_attention_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64]),
     "tq_diag_stream_read": (_i32, [_vp, _sz, _vp, _i64, _vp]),
     "tq_diag_gemv": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32]),
     "tq_select_path": (_i32, [_i32, _i64, _i64, _i64, _i32]),

@@ -6,6 +6,7 @@
 #include "tq.h"
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 
 #include "tq_internal.h"
 
@@ -97,6 +98,76 @@ tq_status tq_kv_append(const void* q, int64_t q_stride, int64_t q_head, const vo
     a.interleaved = interleaved ? 1 : 0;
     a.q_out = static_cast<uint16_t*>(q_out);
     return from_hip(tq::launch_kv_append(a, stream));
+}
+
+static bool attention_sizes_ok(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q, int64_t max_kv) {
+    return T >= 0 && T <= kInt32Max && Hkv > 0 && Hkv <= 4096 && Hq > 0 && Hq <= 65536 && Hq % Hkv == 0 &&
+           (D == 64 || D == 128) && B > 0 && B <= kInt32Max && max_q > 0 && max_q <= kInt32Max && max_kv >= 0 &&
+           max_kv <= kInt32Max;
+}
+
+size_t tq_paged_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q,
+                                          int64_t max_kv, int64_t window, int64_t sinks) {
+    if (!attention_sizes_ok(T, Hq, Hkv, D, B, max_q, max_kv) || T == 0 || window < 0 || sinks < 0) return 0;
+    const tq::AttnPlan p = tq::attn_plan(T, Hq, Hkv, D, B, max_q, max_kv, window, sinks, tq::compute_units());
+    return p.data_bytes ? tq::kFlagBytes + p.data_bytes : 0;
+}
+
+tq_status tq_paged_attention(const void* q, int64_t q_stride, int64_t q_head, tq_dtype dt, int64_t T, int64_t Hq,
+                             int64_t Hkv, int64_t D, const void* k_cache, const void* v_cache, int64_t pages,
+                             int64_t page_size, int64_t page_stride, const int32_t* page_table, int64_t table_stride,
+                             int64_t width, const int32_t* cu_q, const int32_t* kv_lens, int64_t B, int64_t max_q,
+                             int64_t max_kv, float scale, int64_t window, int64_t sinks, void* out, float* lse,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (dt != TQ_F16 && dt != TQ_BF16) return TQ_ERR_DTYPE;
+    if (!attention_sizes_ok(T, Hq, Hkv, D, B, max_q, max_kv) || pages <= 0 || pages > kInt32Max || width <= 0 ||
+        width > kInt32Max)
+        return TQ_ERR_SHAPE;
+    const int shift = page_shift(page_size);
+    if (shift < 0 || page_stride < Hkv * page_size * D || table_stride < width) return TQ_ERR_VALUE;
+    if (!(scale > 0.0f) || !isfinite(scale)) return TQ_ERR_VALUE;
+    if (window < 0 || window > kInt32Max || sinks < 0 || sinks > kInt32Max) return TQ_ERR_VALUE;
+    if (T == 0) return TQ_OK;
+    if (!q || !k_cache || !v_cache || !page_table || !cu_q || !kv_lens || !out) return TQ_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+        !aligned(workspace, 16) || !aligned(page_table, 4) || !aligned(cu_q, 4) || !aligned(kv_lens, 4) ||
+        !aligned(lse, 4) || q_stride % 8 || q_head % 8 || page_stride % 8)
+        return TQ_ERR_ALIGN;
+    tq::AttnPlan plan = tq::attn_plan(T, Hq, Hkv, D, B, max_q, max_kv, window, sinks, tq::compute_units());
+    tq::AttnArgs a{};
+    if (plan.data_bytes && workspace && workspace_bytes >= tq::kFlagBytes + plan.data_bytes) {
+        a.flags = static_cast<uint32_t*>(workspace);
+        a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + tq::kFlagBytes);
+    } else {
+        plan.splits = 1;
+    }
+    a.q = static_cast<const uint16_t*>(q);
+    a.q_stride = q_stride;
+    a.q_head = q_head;
+    a.bf16 = dt == TQ_BF16 ? 1 : 0;
+    a.T = (int)T;
+    a.B = (int)B;
+    a.Hq = (int)Hq;
+    a.Hkv = (int)Hkv;
+    a.G = (int)(Hq / Hkv);
+    a.D = (int)D;
+    a.k = static_cast<const uint16_t*>(k_cache);
+    a.v = static_cast<const uint16_t*>(v_cache);
+    a.pages = pages;
+    a.page_stride = page_stride;
+    a.shift = shift;
+    a.table = page_table;
+    a.table_stride = table_stride;
+    a.width = (int)width;
+    a.cu = cu_q;
+    a.kv = kv_lens;
+    a.max_q = (int)max_q;
+    a.scale_log2 = scale * 1.44269504088896341f;
+    a.window = (int)window;
+    a.sinks = (int)sinks;
+    a.out = static_cast<uint16_t*>(out);
+    a.lse = lse;
+    return from_hip(tq::launch_attention(a, plan, stream));
 }
 
 }  // extern "C"

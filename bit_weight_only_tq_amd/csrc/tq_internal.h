@@ -183,4 +183,40 @@ struct AppendArgs {
 };
 hipError_t launch_kv_append(const AppendArgs& a, hipStream_t s);
 
+// attention.hip: arguments as tq_paged_attention, then the schedule.
+struct AttnArgs {
+    const uint16_t* q;
+    int64_t q_stride, q_head;
+    int bf16;
+    int T, B, Hq, Hkv, G, D;  // G = Hq / Hkv
+    const uint16_t *k, *v;
+    int64_t pages, page_stride;
+    int shift;
+    const int32_t* table;
+    int64_t table_stride;
+    int width;
+    const int32_t *cu, *kv;
+    int max_q;
+    float scale_log2;  // scale * log2(e)
+    int window, sinks;
+    uint16_t* out;
+    float* lse;  // or nullptr
+    // schedule (set by the launcher)
+    float* partials;
+    uint32_t* flags;
+    int R, row_groups, splits, split_blocks;
+    int64_t slab;
+};
+struct AttnPlan {
+    int R;                // 16-row tiles a workgroup holds
+    int64_t row_groups;   // workgroups over the rows of the largest request
+    int64_t splits;       // workgroups over its keys
+    int64_t split_blocks; // key blocks of a split
+    int64_t slab;         // floats of one split's partial result
+    size_t data_bytes;    // partial results of the call
+};
+AttnPlan attn_plan(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q, int64_t max_kv, int64_t window,
+                   int64_t sinks, int compute_units);
+hipError_t launch_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t s);
+
 }  // namespace tq

@@ -178,3 +178,59 @@ def tq_kv_append(q, k, v, k_cache, v_cache, slots, positions=None, rope=None, in
         _ptr(k_cache), _ptr(v_cache), pages, page, stride, _ptr(slots), _ptr(positions), _ptr(rope), rows, rot,
         1 if interleaved else 0, _ptr(out), _stream(dev)))
     return out
+
+
+# ---------------------------------------------------------------- attention
+
+def tq_paged_attention_workspace_bytes(tokens: int, Hq: int, Hkv: int, D: int, B: int, max_q: int, max_kv: int,
+                                       window: int = 0, sinks: int = 0) -> int:
+    """Bytes of workspace tq_paged_attention uses for its fastest schedule (0: none)."""
+    return int(_lib.load().tq_paged_attention_workspace_bytes(tokens, Hq, Hkv, D, B, max_q, max_kv, window, sinks))
+
+
+def tq_paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q: int, max_kv: int, scale: float = None,
+                       window: int = 0, sinks: int = 0, return_lse: bool = False, out=None, workspace="auto"):
+    """Attention of each request's new tokens over its pages; -> out [T, Hq, D], or (out, lse [T, Hq] fp32).
+
+    q [T, Hq, D] fp16/bf16 (token and head strides free, multiples of 8);
+    k_cache, v_cache [pages, Hkv, page_size, D] holding the new tokens already;
+    page_table int32 [B, width]; cu_q int32 [B + 1]; kv_lens int32 [B];
+    max_q, max_kv: the largest numbers of new tokens and of keys of a request;
+    scale: 1 / sqrt(D) by default; window, sinks: a token sees its last
+    `window` keys (0: all) and the first `sinks`.  Causal in each request.
+    workspace: as for tq_gemm ("auto", None or a contiguous device tensor)."""
+    import torch
+    stride = _cache(k_cache, v_cache)
+    pages, Hkv, page, D = k_cache.shape
+    if q.dim() != 3:
+        raise TypeError(f"q must be 3-D [T, heads, {D}], got {q.dim()}-D")
+    T = q.shape[0]
+    Hq, q_tok, q_head = _heads("q", q, k_cache.dtype, T, D)
+    i32 = torch.int32
+    _tensor("page_table", page_table, i32, 2)
+    B, width = page_table.shape
+    _tensor("cu_q", cu_q, i32, 1, (B + 1,))
+    _tensor("kv_lens", kv_lens, i32, 1, (B,))
+    tab = _table_stride(page_table)
+    if out is not None:
+        _tensor("out", out, q.dtype, 3, (T, Hq, D))
+    _contiguous(cu_q=cu_q, kv_lens=kv_lens, out=out)
+    dev = _on_device(q, k_cache, v_cache, page_table, cu_q, kv_lens, out)
+    lib = _lib.load()
+    if out is None:
+        out = q.new_empty((T, Hq, D))
+    lse = q.new_empty((T, Hq), dtype=torch.float32) if return_lse else None
+    if isinstance(workspace, str):
+        workspace = _lib.new_workspace(lib.tq_paged_attention_workspace_bytes(T, Hq, Hkv, D, B, max_q, max_kv, window,
+                                                                              sinks), dev)
+    nbytes = 0
+    if workspace is not None:
+        _on_device(q, workspace)
+        _contiguous(workspace=workspace)
+        nbytes = workspace.numel() * workspace.element_size()
+    _check("tq_paged_attention", lib.tq_paged_attention(
+        _ptr(q), q_tok, q_head if Hq > 1 else 0, _dtype_enum(q), T, Hq, Hkv, D, _ptr(k_cache), _ptr(v_cache), pages, page, stride,
+        _ptr(page_table), tab, width, _ptr(cu_q), _ptr(kv_lens), B, max_q, max_kv,
+        D ** -0.5 if scale is None else scale, window, sinks, _ptr(out), _ptr(lse), _ptr(workspace), nbytes,
+        _stream(dev)))
+    return (out, lse) if return_lse else out

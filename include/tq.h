@@ -451,6 +451,48 @@ tq_status tq_kv_append(const void* q, int64_t q_stride, int64_t q_head, const vo
                        const float* rope, int64_t rope_rows, int64_t rot, int interleaved, void* q_out,
                        hipStream_t stream);
 
+/*
+ * tq_paged_attention - attention of each request's new tokens over its pages.
+ *   q          [T][Hq][D] in `dt`, elements q_stride between tokens and q_head
+ *              between heads (multiples of 8).  Query head i reads KV head
+ *              i / (Hq / Hkv); Hq is a multiple of Hkv; D is 64 or 128.
+ *   page_table [B] rows of `width` page ids, table_stride elements apart.
+ *   cu_q       [B + 1] request b's new tokens are cu_q[b] .. cu_q[b + 1] - 1
+ *              (0 <= cu_q[b] and cu_q[b + 1] <= T; other requests are skipped).
+ *   kv_lens    [B] its keys, the new tokens' own (already appended) included:
+ *              new token i of n sits at position kv - n + i.
+ *   max_q      at least the largest number of new tokens of a request (more
+ *              of them are not computed).
+ *   max_kv     the largest kv_lens, for the schedule: any value is correct.
+ *   scale      positive; scores are scale * q . k.
+ *   window     0: a token sees the keys up to its own position; w > 0: of
+ *              these the last w and, besides, the first `sinks` keys.
+ *   out        [T][Hq][D] in `dt`, contiguous (written).
+ *   lse        [T][Hq] fp32 natural logarithm of the sum of exponentials
+ *              (written; may be NULL).
+ * A row that sees no key gives zeros and -inf.  Keys of a page id outside
+ * [0, pages) and keys past the table's width count as not there.  What a row
+ * does not see does not touch it, also where it is not finite.  Tokens of no
+ * request are not written.  Scores, maxima, sums and outputs are held in
+ * fp32; the weights are rounded to `dt` before the product with the values.
+ *   workspace  as for tq_gemm_ws: with tq_paged_attention_workspace_bytes()
+ *              bytes the keys of few rows are split over workgroups and the
+ *              partial results joined in the kernel in split order; with less
+ *              (or NULL) each row's keys are one workgroup's work.
+ * All pointers of values 16-byte aligned.  T = 0 does nothing.
+ */
+tq_status tq_paged_attention(const void* q, int64_t q_stride, int64_t q_head, tq_dtype dt, int64_t T, int64_t Hq,
+                             int64_t Hkv, int64_t D, const void* k_cache, const void* v_cache, int64_t pages,
+                             int64_t page_size, int64_t page_stride, const int32_t* page_table,
+                             int64_t table_stride, int64_t width, const int32_t* cu_q, const int32_t* kv_lens,
+                             int64_t B, int64_t max_q, int64_t max_kv, float scale, int64_t window, int64_t sinks,
+                             void* out, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace tq_paged_attention uses for its fastest schedule on the current
+ * device (0: none, or invalid arguments). */
+size_t tq_paged_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q,
+                                          int64_t max_kv, int64_t window, int64_t sinks);
+
 /* ----------------------------------------------------------- measurement
  *
  * Instruments for the benchmark, not part of the layer: they measure the

@@ -56,3 +56,51 @@ def test_store_places_rows():
     x = np.arange(1, 17).reshape(2, 2, 4).astype(float)
     out = OP.store(cache, x, [2 * 16 + 5, -1])
     assert np.array_equal(out[2, :, 5], x[0]) and np.count_nonzero(out) == 8
+
+
+# ---------------------------------------------------------------- attention
+
+def test_attention_equal_scores_average_the_visible_values():
+    """Zero queries weigh all visible keys alike, whatever the keys hold."""
+    import oracle.attention as OA
+    rng = np.random.default_rng(3)
+    k, v = rng.standard_normal((2, 4, 1, 16, 8))
+    table = np.array([[2, 0, 3]])
+    flat = v[[2, 0, 3], 0].reshape(48, 8)
+    q = np.zeros((3, 2, 8))
+    for window, sinks in ((0, 0), (5, 0), (5, 2), (1, 0), (100, 3)):
+        r = OA.attend(q, k, v, table, [0, 3], [40], 0.3, window, sinks)
+        for i in range(3):
+            p = 37 + i
+            see = [j for j in range(40) if j <= p and (not window or p - j < window or j < sinks)]
+            assert np.allclose(r["out"][i, 1], flat[see].mean(0), atol=1e-14)
+            assert np.isclose(r["lse"][i, 0], np.log(len(see)), atol=1e-14)
+
+
+def test_attention_is_a_softmax():
+    """Against a dense softmax over a contiguous cache, and the gradient of lse in the scale is the mean score."""
+    import oracle.attention as OA
+    rng = np.random.default_rng(4)
+    k, v = rng.standard_normal((2, 2, 1, 16, 8))
+    q = rng.standard_normal((1, 1, 8))
+    f = lambda s: OA.attend(q, k, v, np.array([[0, 1]]), [0, 1], [23], s)  # noqa: E731
+    s = 0.4 * k[:, 0].reshape(32, 8)[:23] @ q[0, 0]
+    w = np.exp(s) / np.exp(s).sum()
+    assert np.allclose(f(0.4)["out"][0, 0], w @ v[:, 0].reshape(32, 8)[:23], atol=1e-13)
+    d = (f(0.4 + 1e-6)["lse"] - f(0.4 - 1e-6)["lse"]) / 2e-6
+    assert np.isclose(d[0, 0], (w * s).sum() / 0.4, atol=1e-6)
+
+
+def test_attention_empty_and_missing():
+    """No key, rows before the first key, pages that do not exist: zeros and -inf; hidden NaN stays hidden."""
+    import oracle.attention as OA
+    k, v = np.ones((2, 2, 1, 16, 4))
+    v = v * np.arange(1.0, 17)[:, None]
+    v[1, 0, 3:] = np.nan
+    q = np.ones((4, 1, 4))
+    r = OA.attend(q, k, v, np.array([[-1, 1]]), [0, 4], [19], 1.0)
+    assert np.array_equal(r["out"][:3], np.where(np.arange(3)[:, None, None] < 1, 0, [[[1.0]], [[1.0]], [[1.5]]]) *
+                          np.ones((3, 1, 4)))
+    assert np.isneginf(r["lse"][0, 0]) and np.allclose(r["out"][3], 2.0)
+    r = OA.attend(q, k, v, np.array([[0]]), [0, 4], [2], 1.0)
+    assert np.array_equal(np.isneginf(r["lse"][:, 0]), [True, True, False, False])

@@ -122,3 +122,67 @@ def test_append_rejects(change):
     with pytest.raises((ValueError, TypeError)) as e:
         tq.tq_kv_append(**dict(_append_args(), **change))
     assert "device tensors" not in str(e.value)
+
+
+# ---------------------------------------------------------------- attention
+
+ATTN = dict(q=FAKE, qs=128, qh=64, dt=0, T=3, Hq=2, Hkv=1, D=64, kc=FAKE, vc=FAKE, pages=4, page=16, stride=1024,
+            table=FAKE, tstride=4, width=4, cu=FAKE, kv=FAKE, B=1, max_q=3, max_kv=40, scale=0.125, window=0, sinks=0,
+            out=FAKE, lse=FAKE, ws=None, ws_bytes=0, stream=None)
+
+
+@pytest.mark.parametrize("change, want", [
+    *[({n: None}, "TQ_ERR_NULL") for n in ("q", "kc", "vc", "table", "cu", "kv", "out")],
+    *[({n: V(0x10008)}, "TQ_ERR_ALIGN") for n in ("q", "kc", "vc", "out", "ws")],
+    *[({n: ODD}, "TQ_ERR_ALIGN") for n in ("table", "cu", "kv", "lse")],
+    ({"qs": 132}, "TQ_ERR_ALIGN"), ({"qh": 65}, "TQ_ERR_ALIGN"), ({"stride": 1028}, "TQ_ERR_ALIGN"),
+    ({"dt": 2}, "TQ_ERR_DTYPE"), ({"dt": -1}, "TQ_ERR_DTYPE"),
+    *[({n: -1}, "TQ_ERR_SHAPE") for n in ("T", "Hq", "Hkv", "D", "pages", "width", "B", "max_q", "max_kv")],
+    *[({n: 0}, "TQ_ERR_SHAPE") for n in ("Hq", "Hkv", "D", "pages", "width", "B", "max_q")],
+    ({"Hq": 3, "Hkv": 2, "stride": 4096}, "TQ_ERR_SHAPE"), ({"D": 96}, "TQ_ERR_SHAPE"), ({"D": 256}, "TQ_ERR_SHAPE"),
+    *[({"page": p}, "TQ_ERR_VALUE") for p in (0, 8, 48, 2048)],
+    ({"stride": 1016}, "TQ_ERR_VALUE"), ({"tstride": 3}, "TQ_ERR_VALUE"),
+    *[({"scale": x}, "TQ_ERR_VALUE") for x in (0.0, -1.0, float("nan"), float("inf"))],
+    ({"window": -1}, "TQ_ERR_VALUE"), ({"sinks": -1}, "TQ_ERR_VALUE"), ({"window": 1 << 31}, "TQ_ERR_VALUE"),
+    ({"T": 0, "q": None}, "TQ_OK"),
+])
+def test_attention_host_checks(lib, change, want):
+    assert call(lib, "tq_paged_attention", ATTN, **change) == want
+
+
+def test_attention_workspace_query():
+    """Nothing for invalid sizes or where there is nothing to split; the counters and the partials otherwise."""
+    wb = tq.tq_paged_attention_workspace_bytes
+    assert wb(1, 32, 8, 128, 1, 1, 64) == 0           # two key blocks
+    assert wb(1, 32, 8, 96, 1, 1, 9999) == 0 and wb(1, 31, 8, 128, 1, 1, 9999) == 0 and wb(0, 32, 8, 128, 1, 1, 9999) == 0
+    long = wb(2, 32, 8, 128, 2, 1, 131071)
+    assert long > tq.TQ_WORKSPACE_FLAG_BYTES and (long - tq.TQ_WORKSPACE_FLAG_BYTES) % (2 * 8 * 4 * 130 * 4) == 0
+    assert wb(2, 32, 8, 128, 2, 1, 131071, 64) == 0   # a window of 64 keys
+    assert wb(4096, 32, 8, 128, 1024, 4, 4096) == 0   # more tiles than counters
+
+
+def _attn_args(T=3, Hq=2, Hkv=1, D=64, page=16, pages=4):
+    h = lambda *s: torch.zeros(s, dtype=torch.float16)  # noqa: E731
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    return dict(q=h(T, Hq, D), k_cache=h(pages, Hkv, page, D), v_cache=h(pages, Hkv, page, D), page_table=i(1, 4),
+                cu_q=i(2), kv_lens=i(1), max_q=3, max_kv=40)
+
+
+def test_attention_well_formed_cpu_tensors_reach_device_check():
+    with pytest.raises(ValueError, match="device tensors"):
+        tq.tq_paged_attention(**_attn_args())
+
+
+@pytest.mark.parametrize("change", [
+    dict(q=torch.zeros((3, 128), dtype=torch.float16)), dict(q=torch.zeros((3, 2, 64), dtype=torch.bfloat16)),
+    dict(q=torch.zeros((3, 2, 32), dtype=torch.float16)), dict(q=torch.zeros((3, 64, 2), dtype=torch.float16).transpose(1, 2)),
+    dict(v_cache=torch.zeros((4, 1, 16, 64), dtype=torch.bfloat16)), dict(k_cache=torch.zeros((4, 1, 16, 64))),
+    dict(page_table=torch.zeros((1, 4), dtype=torch.int64)), dict(page_table=torch.zeros(4, dtype=torch.int32)),
+    dict(cu_q=torch.zeros(3, dtype=torch.int32)), dict(kv_lens=torch.zeros(1, dtype=torch.int64)),
+    dict(cu_q=torch.zeros(4, dtype=torch.int32)[::2]), dict(out=torch.zeros((3, 2, 64))),
+    dict(out=torch.zeros((3, 4, 64), dtype=torch.float16)[:, ::2]),
+])
+def test_attention_rejects(change):
+    with pytest.raises((ValueError, TypeError)) as e:
+        tq.tq_paged_attention(**dict(_attn_args(), **change))
+    assert "device tensors" not in str(e.value)
