@@ -19,7 +19,7 @@ STATUS_NAMES = {
     9: "TQ_ERR_HIP", 10: "TQ_ERR_PATH", 11: "TQ_ERR_SCRATCH", 12: "TQ_ERR_VALUE",
 }
 # tq_dtype
-TQ_F16, TQ_BF16 = 0, 1
+TQ_F16, TQ_BF16, TQ_F32 = 0, 1, 2
 # tq_path
 PATHS = {"auto": 0, "gemv": 1, "stream_mfma": 2, "gemm": 3}
 PATH_NAMES = {v: k for k, v in PATHS.items()}
@@ -54,6 +54,7 @@ SIGNATURES = {
                                   _i64, _vp, _vp, _i64, _i64, _i64, ctypes.c_float, _i64, _i64, _vp, _vp, _vp, _sz,
                                   _vp]),
     "tq_paged_attention_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64]),
+    "tq_sample": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "tq_diag_stream_read": (_i32, [_vp, _sz, _vp, _i64, _vp]),
     "tq_diag_gemv": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32]),
     "tq_select_path": (_i32, [_i32, _i64, _i64, _i64, _i32]),

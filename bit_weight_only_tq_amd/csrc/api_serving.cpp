@@ -170,4 +170,31 @@ tq_status tq_paged_attention(const void* q, int64_t q_stride, int64_t q_head, tq
     return from_hip(tq::launch_attention(a, plan, stream));
 }
 
+tq_status tq_sample(const void* logits, tq_dtype dt, int64_t B, int64_t V, int64_t row_stride, const float* u,
+                    const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                    int32_t* tokens, float* logprobs, hipStream_t stream) {
+    if (dt != TQ_F16 && dt != TQ_BF16 && dt != TQ_F32) return TQ_ERR_DTYPE;
+    if (B < 0 || B > kInt32Max || V <= 0 || V > tq::kSampleMaxVocab) return TQ_ERR_SHAPE;
+    if (B > 1 && row_stride < V) return TQ_ERR_VALUE;
+    if (B == 0) return TQ_OK;
+    if (!logits || !u || !tokens) return TQ_ERR_NULL;
+    if (!aligned(logits, dt == TQ_F32 ? 4 : 2) || !aligned(u, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) ||
+        !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(tokens, 4) || !aligned(logprobs, 4))
+        return TQ_ERR_ALIGN;
+    tq::SampleArgs a;
+    a.logits = logits;
+    a.dtype = (int)dt;
+    a.B = B;
+    a.V = (int)V;
+    a.row_stride = row_stride;
+    a.u = u;
+    a.temperature = temperature;
+    a.top_k = top_k;
+    a.top_p = top_p;
+    a.min_p = min_p;
+    a.tokens = tokens;
+    a.logprobs = logprobs;
+    return from_hip(tq::launch_sample(a, stream));
+}
+
 }  // extern "C"

@@ -219,4 +219,21 @@ AttnPlan attn_plan(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int
                    int64_t sinks, int compute_units);
 hipError_t launch_attention(const AttnArgs& a, const AttnPlan& plan, hipStream_t s);
 
+// sample.hip: arguments as tq_sample.
+constexpr int64_t kSampleMaxVocab = (int64_t)1 << 20;  // the weights of a row's segments stay in LDS
+struct SampleArgs {
+    const void* logits;
+    int dtype;  // tq_dtype
+    int64_t B;
+    int V;
+    int64_t row_stride;
+    const float *u, *temperature;
+    const int32_t* top_k;
+    const float *top_p, *min_p;
+    int32_t* tokens;
+    float* logprobs;
+    double fix = 0;  // set by the launcher: fixed-point unit of the weights
+};
+hipError_t launch_sample(const SampleArgs& a, hipStream_t s);
+
 }  // namespace tq

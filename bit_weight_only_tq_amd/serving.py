@@ -10,7 +10,9 @@ call (the C ABI takes bare pointers), and there is no CPU fallback.
 from typing import NamedTuple
 
 from . import _lib
-from ._lib import _check, _dtype_enum, _ptr, _stream
+from ._lib import TQ_BF16, TQ_F16, TQ_F32, _check, _dtype_enum, _ptr, _stream
+
+_LOGITS = {"torch.float16": TQ_F16, "torch.bfloat16": TQ_BF16, "torch.float32": TQ_F32}
 
 
 def _tensor(name, t, dtype, dim, shape=None):
@@ -234,3 +236,44 @@ def tq_paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q: in
         D ** -0.5 if scale is None else scale, window, sinks, _ptr(out), _ptr(lse), _ptr(workspace), nbytes,
         _stream(dev)))
     return (out, lse) if return_lse else out
+
+
+# ----------------------------------------------------------------- sampling
+
+def tq_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, out=None):
+    """One token per row: -> (tokens int32 [B], logprobs fp32 [B]).
+
+    logits [B, V] fp16, bf16 or fp32 (rows may be strided); u fp32 [B] in
+    [0, 1).  temperature, top_p, min_p fp32 [B] and top_k int32 [B], or None
+    for 1, 1, 0 and 0 (no cut); temperature 0 takes the best token.  A row
+    without a logit above -inf gives token -1.  out: (tokens, logprobs) to
+    write into."""
+    import torch
+    f32 = torch.float32
+    if logits.dim() != 2:
+        raise TypeError(f"logits must be 2-D [B, V], got {logits.dim()}-D")
+    dt = _LOGITS.get(str(logits.dtype))
+    if dt is None:
+        raise TypeError(f"logits must be float16, bfloat16 or float32, got {logits.dtype}")
+    B, V = logits.shape
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("the rows of logits must be contiguous")
+    stride = logits.stride(0) if B > 1 else V
+    if stride < V:
+        raise ValueError("the rows of logits must not overlap")
+    _tensor("u", u, f32, 1, (B,))
+    for name, t, want in (("temperature", temperature, f32), ("top_k", top_k, torch.int32), ("top_p", top_p, f32),
+                          ("min_p", min_p, f32)):
+        if t is not None:
+            _tensor(name, t, want, 1, (B,))
+    if out is not None:
+        _tensor("tokens", out[0], torch.int32, 1, (B,))
+        _tensor("logprobs", out[1], f32, 1, (B,))
+        _contiguous(tokens=out[0], logprobs=out[1])
+    _contiguous(u=u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p)
+    dev = _on_device(logits, u, temperature, top_k, top_p, min_p, *(out or ()))
+    tokens, logprobs = out or (u.new_empty((B,), dtype=torch.int32), u.new_empty((B,)))
+    _check("tq_sample", _lib.load().tq_sample(
+        _ptr(logits), dt, B, V, stride, _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+        _ptr(tokens), _ptr(logprobs), _stream(dev)))
+    return tokens, logprobs

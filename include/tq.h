@@ -87,7 +87,8 @@ typedef enum tq_status {
 
 typedef enum tq_dtype {
     TQ_F16 = 0,            /* IEEE binary16 activations and outputs */
-    TQ_BF16 = 1            /* bfloat16 activations and outputs */
+    TQ_BF16 = 1,           /* bfloat16 activations and outputs */
+    TQ_F32 = 2             /* binary32: the logits of tq_sample only */
 } tq_dtype;
 
 /* Kernel families the dispatcher chooses between (by M; see tq_select_path). */
@@ -492,6 +493,32 @@ tq_status tq_paged_attention(const void* q, int64_t q_stride, int64_t q_head, tq
  * device (0: none, or invalid arguments). */
 size_t tq_paged_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q,
                                           int64_t max_kv, int64_t window, int64_t sinks);
+
+/*
+ * tq_sample - one token per row of logits.
+ *   logits      [B][V] in `dt` (TQ_F16, TQ_BF16 or TQ_F32), row_stride
+ *               elements between rows, any alignment; V <= 2^20.  NaN counts
+ *               as -inf.
+ *   u           [B] fp32 random numbers in [0, 1) (others are taken to its
+ *               ends, NaN to 0).
+ *   temperature, top_k, top_p, min_p  [B] each, or NULL for 1, 0, 1 and 0.
+ * With w_i = exp((x_i - max x) / temperature) and the tokens ranked by logit,
+ * equal ones by index, a row keeps: its first top_k tokens (all for top_k <= 0
+ * or > V), of these the ones with w >= min_p, of these the ones with less than
+ * top_p times their total weight before them (all for top_p >= 1); the best
+ * token always.  The token drawn is the first index whose running kept
+ * weight, in index order, passes u times the kept total.  temperature <= 0
+ * (or NaN) takes the best token.
+ *   tokens      [B] int32 (written), -1 for a row without a logit above -inf.
+ *   logprobs    [B] fp32 log(w / kept total) of the token (written; may be
+ *               NULL), -inf where there is none.
+ * Weights are fp64, their sums 64-bit fixed point (2^-42 of the largest weight
+ * or finer), so equal inputs give equal tokens whatever the schedule.
+ * Equal infinities share the weight.  B = 0 does nothing.
+ */
+tq_status tq_sample(const void* logits, tq_dtype dt, int64_t B, int64_t V, int64_t row_stride, const float* u,
+                    const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                    int32_t* tokens, float* logprobs, hipStream_t stream);
 
 /* ----------------------------------------------------------- measurement
  *

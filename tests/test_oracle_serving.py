@@ -104,3 +104,36 @@ def test_attention_empty_and_missing():
     assert np.isneginf(r["lse"][0, 0]) and np.allclose(r["out"][3], 2.0)
     r = OA.attend(q, k, v, np.array([[0]]), [0, 4], [2], 1.0)
     assert np.array_equal(np.isneginf(r["lse"][:, 0]), [True, True, False, False])
+
+
+# ----------------------------------------------------------------- sampling
+
+def test_sampling_by_hand():
+    """Five tokens with weights 8, 4, 2, 1, 1 (ties at the end)."""
+    import oracle.sampling as OS
+    row = np.log([2.0, 8.0, 1.0, 4.0, 1.0])
+    full = lambda **kw: OS.kept(row, **kw)[0].tolist()  # noqa: E731
+    assert full() == [1, 3, 0, 2, 4]
+    assert full(top_k=4) == [1, 3, 0, 2] and full(top_k=9) == full()
+    assert full(min_p=0.2) == [1, 3, 0] and full(min_p=2.0) == [1]
+    assert full(top_p=0.51) == [1, 3] and full(top_p=0.8) == [1, 3, 0] and full(top_p=0.0) == [1]
+    assert full(temperature=0.0) == [1] and full(temperature=2.0, min_p=0.4) == [1, 3, 0]
+    assert full(top_k=2, top_p=0.7) == [1, 3] and full(top_k=2, top_p=0.6) == [1]  # of 12, not of 16
+    # index order: 2/16, 10/16, 11/16, 15/16, 16/16
+    got = [OS.sample(row, u)[0] for u in (0.0, 0.12, 0.13, 0.62, 0.63, 0.68, 0.69, 0.93, 0.94, 0.999, 1.5)]
+    assert got == [0, 0, 1, 1, 2, 2, 3, 3, 4, 4, 4]
+    tok, lp = OS.sample(row, 0.5, top_k=2)
+    assert tok == 1 and abs(lp - np.log(8 / 12)) < 1e-14
+    assert OS.sample(np.full(3, -np.inf), 0.5) == (-1, -np.inf)
+    assert OS.sample(np.array([np.nan, 1.0, -np.inf]), 0.9) == (1, 0.0)
+    assert OS.sample(np.array([np.inf, 1.0, np.inf]), 0.6)[0] == 2
+
+
+def test_sampling_frequencies_are_the_probabilities():
+    import oracle.sampling as OS
+    rng = np.random.default_rng(6)
+    row = rng.standard_normal(7)
+    n = 4000
+    count = np.bincount([OS.sample(row, (i + 0.5) / n, temperature=0.7)[0] for i in range(n)], minlength=7)
+    p = np.exp(row / 0.7) / np.exp(row / 0.7).sum()
+    assert np.abs(count / n - p).max() <= 1.0 / n

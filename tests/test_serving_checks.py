@@ -186,3 +186,39 @@ def test_attention_rejects(change):
     with pytest.raises((ValueError, TypeError)) as e:
         tq.tq_paged_attention(**dict(_attn_args(), **change))
     assert "device tensors" not in str(e.value)
+
+
+# ----------------------------------------------------------------- sampling
+
+SAMPLE = dict(logits=FAKE, dt=2, B=2, V=100, stride=100, u=FAKE, temperature=FAKE, top_k=FAKE, top_p=FAKE, min_p=FAKE,
+              tokens=FAKE, logprobs=FAKE, stream=None)
+
+
+@pytest.mark.parametrize("change, want", [
+    *[({n: None}, "TQ_ERR_NULL") for n in ("logits", "u", "tokens")],
+    *[({n: ODD}, "TQ_ERR_ALIGN") for n in ("logits", "u", "temperature", "top_k", "top_p", "min_p", "tokens", "logprobs")],
+    ({"logits": V(0x10002)}, "TQ_ERR_ALIGN"), ({"logits": V(0x10001), "dt": 0}, "TQ_ERR_ALIGN"),
+    ({"dt": 3}, "TQ_ERR_DTYPE"), ({"B": -1}, "TQ_ERR_SHAPE"), ({"V": 0}, "TQ_ERR_SHAPE"),
+    ({"V": (1 << 20) + 1, "stride": 1 << 21}, "TQ_ERR_SHAPE"), ({"stride": 99}, "TQ_ERR_VALUE"),
+    ({"B": 0, "logits": None}, "TQ_OK"),
+])
+def test_sample_host_checks(lib, change, want):
+    assert call(lib, "tq_sample", SAMPLE, **change) == want
+
+
+def test_sample_well_formed_cpu_tensors_reach_device_check():
+    with pytest.raises(ValueError, match="device tensors"):
+        tq.tq_sample(torch.zeros((2, 100)), torch.zeros(2))
+
+
+@pytest.mark.parametrize("change", [
+    dict(logits=torch.zeros(100)), dict(logits=torch.zeros((2, 100), dtype=torch.float64)),
+    dict(logits=torch.zeros((100, 2)).T), dict(logits=torch.zeros((1, 100)).expand(2, 100)),
+    dict(u=torch.zeros(3)), dict(u=torch.zeros(2, dtype=torch.float64)), dict(temperature=torch.zeros(1)),
+    dict(top_k=torch.zeros(2)), dict(top_p=torch.zeros((2, 1))), dict(min_p=torch.zeros(4)[::2]),
+    dict(out=(torch.zeros(2, dtype=torch.int64), torch.zeros(2))),
+])
+def test_sample_rejects(change):
+    with pytest.raises((ValueError, TypeError)) as e:
+        tq.tq_sample(**dict(dict(logits=torch.zeros((2, 100)), u=torch.zeros(2)), **change))
+    assert "device tensors" not in str(e.value)
