@@ -29,6 +29,8 @@ SOURCES = {
     "gemm.hip": [],
     "diag.hip": [],
     "paged.hip": [],
+    "attention.hip": [],
+    "sample.hip": [],
     "api.cpp": ["-x", "hip"],
     "api_serving.cpp": ["-x", "hip"],
 }
