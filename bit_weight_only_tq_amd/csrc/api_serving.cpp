@@ -133,13 +133,11 @@ tq_status tq_paged_attention(const void* q, int64_t q_stride, int64_t q_head, tq
         !aligned(workspace, 16) || !aligned(page_table, 4) || !aligned(cu_q, 4) || !aligned(kv_lens, 4) ||
         !aligned(lse, 4) || q_stride % 8 || q_head % 8 || page_stride % 8)
         return TQ_ERR_ALIGN;
-    tq::AttnPlan plan = tq::attn_plan(T, Hq, Hkv, D, B, max_q, max_kv, window, sinks, tq::compute_units());
+    const tq::AttnPlan plan = tq::attn_plan(T, Hq, Hkv, D, B, max_q, max_kv, window, sinks, tq::compute_units());
     tq::AttnArgs a{};
     if (plan.data_bytes && workspace && workspace_bytes >= tq::kFlagBytes + plan.data_bytes) {
         a.flags = static_cast<uint32_t*>(workspace);
         a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + tq::kFlagBytes);
-    } else {
-        plan.splits = 1;
     }
     a.q = static_cast<const uint16_t*>(q);
     a.q_stride = q_stride;

@@ -30,6 +30,9 @@ struct AttnF16 {
     static __device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
     }
+    static __device__ __forceinline__ f32x16 mfma32(uint4 a, uint4 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    }
     static __device__ __forceinline__ uint32_t pack2(float x, float y) {
         return __builtin_bit_cast(uint32_t, f16x2{(_Float16)x, (_Float16)y});
     }
@@ -40,6 +43,9 @@ struct AttnF16 {
 struct AttnBF16 {
     static __device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ f32x16 mfma32(uint4 a, uint4 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
     }
     static __device__ __forceinline__ uint32_t pack2(float x, float y) {
         return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)x, (__bf16)y});
@@ -76,20 +82,21 @@ __device__ __forceinline__ Request request_of(const AttnArgs& a, int b) {
     return r;
 }
 
-// The key blocks (32 keys, aligned) a run of positions p0 .. p1 can see:
+// The key blocks (2^LOG keys, aligned) a run of positions p0 .. p1 can see:
 // `head` blocks of sinks from key 0, then [main0, main1).
 struct Blocks {
     int head, main0, count;
     __device__ __forceinline__ int at(int i) const { return i < head ? i : main0 + (i - head); }
 };
+template <int LOG>
 __device__ __forceinline__ Blocks blocks_of(const AttnArgs& a, const Request& r, int p0, int p1) {
     Blocks k;
     const int end = min(p1, r.keys - 1) + 1;  // first key nobody sees
-    const int main1 = end > 0 ? (int)(((uint32_t)end + 31u) >> 5) : 0;
+    const int main1 = end > 0 ? (int)(((uint32_t)end + (1u << LOG) - 1u) >> LOG) : 0;
     int lo = 0;
     if (a.window > 0) lo = max(p0 - a.window + 1, 0);
-    k.main0 = min(lo >> 5, main1);
-    k.head = min((int)(((uint32_t)a.sinks + 31u) >> 5), k.main0);
+    k.main0 = min(lo >> LOG, main1);
+    k.head = min((int)(((uint32_t)a.sinks + (1u << LOG) - 1u) >> LOG), k.main0);
     k.count = k.head + (main1 - k.main0);
     return k;
 }
@@ -140,6 +147,67 @@ __device__ __forceinline__ VRow<VD> load_vrow(const uint16_t* p) {
     return r;
 }
 
+// Joins the partial results of a workgroup tile's splits, in split order, by
+// the last workgroup to arrive (256 threads): weights of the splits from their
+// row statistics ([row][2] at the front of each slab), then the weighted sum
+// of their outputs ([row][D] from `out_at` on).  `wgt` has room for
+// rows * nsplit floats.
+template <class E, int D>
+__device__ __forceinline__ void join_splits(const AttnArgs& a, const Request& rq, int h, int64_t row0, int rows, int out_at,
+                                            int64_t wg_tile, int nsplit, float* wgt, float* row_m, float* row_l) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, G = a.G;
+    const float* slabs = a.partials + wg_tile * a.splits * a.slab;
+    for (int row = wave; row < rows; row += 4) {
+        float M = -INFINITY;
+        for (int s = lane; s < nsplit; s += 64)
+            M = fmaxf(M, __hip_atomic_load(slabs + s * a.slab + 2 * row, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+#pragma unroll
+        for (int x = 32; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor(M, x, 64));
+        const float ms = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        for (int s = lane; s < nsplit; s += 64) {
+            const float ps = __hip_atomic_load(slabs + s * a.slab + 2 * row, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            const float pl = __hip_atomic_load(slabs + s * a.slab + 2 * row + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            const float f = exp2_fast(ps - ms);
+            wgt[row * nsplit + s] = f;
+            L += f * pl;
+        }
+        L = wave_sum(L);
+        if (lane == 0) {
+            row_m[row] = M;
+            row_l[row] = L;
+        }
+    }
+    __syncthreads();
+    for (int u = tid; u < rows * (D / 2); u += kRowsThreads) {
+        const int row = u / (D / 2), d = (u - row * (D / 2)) * 2;
+        float x0 = 0.f, x1 = 0.f;
+        const float* base = slabs + out_at + row * D + d;
+        constexpr int RS = 8;  // splits in flight
+        for (int s0 = 0; s0 < nsplit; s0 += RS) {
+            uint64_t v[RS];
+#pragma unroll
+            for (int s = 0; s < RS; ++s)
+                v[s] = __hip_atomic_load(reinterpret_cast<const uint64_t*>(base + (int64_t)min(s0 + s, nsplit - 1) * a.slab),
+                                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+            for (int s = 0; s < RS; ++s)
+                if (s0 + s < nsplit) {
+                    const float f = wgt[row * nsplit + s0 + s];
+                    x0 += f * __uint_as_float((uint32_t)v[s]);
+                    x1 += f * __uint_as_float((uint32_t)(v[s] >> 32));
+                }
+        }
+        const float L = row_l[row];
+        const int64_t r = row0 + row;
+        const int tok = (int)(r / G);
+        const int64_t at = (int64_t)(rq.t0 + tok) * a.Hq + h * G + (int)(r - (int64_t)tok * G);
+        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN);
+        *reinterpret_cast<uint32_t*>(a.out + at * D + d) = E::pack2(x0 * inv, x1 * inv);
+        if (d == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : kLn2 * (row_m[row] + log2f(L));
+    }
+}
+
 template <class E, int D>
 __global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
     constexpr int ST = D / 32, DV = D / 16, VD = DV / 2;
@@ -163,10 +231,10 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
     const int R = a.R, G = a.G;
     const int64_t rows_all = (int64_t)min(rq.n, a.max_q) * G;
     const int64_t row0 = (int64_t)rg * 16 * R;
-    if (row0 >= rows_all) return;
+    if (row0 >= rows_all || rows_all > a.rows_most) return;
     const int rows = (int)(rows_all - row0 < 16 * R ? rows_all - row0 : 16 * R);  // of this workgroup
     // the keys any of its rows sees, cut into splits
-    const Blocks bl = blocks_of(a, rq, rq.first + (int)(row0 / G), rq.first + (int)((row0 + rows - 1) / G));
+    const Blocks bl = blocks_of<5>(a, rq, rq.first + (int)(row0 / G), rq.first + (int)((row0 + rows - 1) / G));
     int per = a.split_blocks;
     if ((int64_t)per * a.splits < bl.count) per = (bl.count + a.splits - 1) / a.splits;
     const int nsplit = bl.count > per ? (bl.count + per - 1) / per : 1;
@@ -382,118 +450,461 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
     if (!parts) return;
     if (!split_last_arrival(a.flags, (uint32_t)wg_tile, nsplit, &word)) return;
 
-    // join the splits, in split order
-    const float* slabs = a.partials + wg_tile * a.splits * a.slab;
-    float* wgt = lds_o;  // [row][nsplit] weights of the splits; splits * rows <= 4096
-    for (int row = wave; row < rows; row += 4) {
-        float M = -INFINITY;
-        for (int s = lane; s < nsplit; s += 64)
-            M = fmaxf(M, __hip_atomic_load(slabs + s * a.slab + 2 * row, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    join_splits<E, D>(a, rq, h, row0, rows, 2 * rows, wg_tile, nsplit, lds_o, row_m, row_l);
+}
+
+// ---- tile kernel: 32 rows a wave, 128 a workgroup, keys in tiles of 64.
+//
+// Prompt chunks are bound by the matrix cores.  K and V tiles go from their
+// pages to LDS by DMA, one tile ahead, and are shared by the four waves; the
+// transposed products are as in the rows kernel, with 32 x 32 matrix tiles:
+// S^T = K Q^T leaves row n = lane % 32 of the queries in lanes n and n + 32,
+// each with 4 of every 8 keys, and these scores, rounded, are the second
+// operand of O^T = V^T P^T with the keys of a step of 16 dealt as
+// (4 h .. 4 h + 3, 8 + 4 h .. 8 + 4 h + 3), h = lane / 32.  V^T comes from
+// LDS through the transposing read, which gives a lane four keys of one
+// column.  So the weights never leave their registers, and a row's maximum
+// and sum need no exchange between lanes but where the maximum is raised.
+//
+// 16-byte chunks of a row are stored at chunk ^ f(key): with f = key % 16
+// (K, D = 128), key % 8 (K, D = 64), 2 (key % 8) (V, D = 128) and 2 (key % 4)
+// (V, D = 64) the lanes that read together fall into different banks.
+constexpr int kTileKeys = 64;
+constexpr int kTileRows = 128;
+constexpr int kTileThreads = 256;
+
+typedef const __attribute__((address_space(4))) int32_t* const_i32;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+template <int D>
+struct TileGeom {
+    static constexpr int kRowBytes = D * 2;
+    static constexpr int kMatBytes = kTileKeys * kRowBytes;  // one of K and V
+    static constexpr int kStageBytes = 2 * kMatBytes;
+    static constexpr int kLdsBytes = 2 * kStageBytes;
+    static __device__ __forceinline__ int kswz(int key) { return D == 128 ? (key & 15) : (key & 7); }
+    static __device__ __forceinline__ int vswz(int key) { return D == 128 ? 2 * (key & 7) : 2 * (key & 3); }
+};
+
+// The request of tile `t` of a call: request b's tiles begin at
+// floor(cu[b] G / 128) + b, which leaves room for the ceil(n G / 128) it
+// needs.  Finds the last b that begins at or before t (offsets ascending);
+// 64 places a round, so that a batch of 64 costs one read.
+__device__ __forceinline__ int64_t tiles_before(const AttnArgs& a, int b) {
+    const int c = min(max(a.cu[b], 0), a.T);
+    return (int64_t)c * a.G / kTileRows + b;
+}
+__device__ __forceinline__ int request_of_tile(const AttnArgs& a, int64_t t) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = a.B;  // the answer lies in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 63) / 64;
+        const int probe = lo + lane * step;
+        const bool in = lane * step < n && tiles_before(a, probe) <= t;
+        const int last = 63 - __clzll((long long)(__ballot(in) | 1ull));
+        n = min(step, n - last * step);
+        lo += last * step;
+    }
+    return lo;
+}
+
+template <class E, int D>
+__global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(AttnArgs a) {
+    using TG = TileGeom<D>;
+    constexpr int KS = D / 16;        // steps of S^T = K Q^T
+    constexpr int DB = D / 32;        // 32-column blocks of O
+    constexpr int CPR = D / 8;        // chunks of a row
+    constexpr int RPD = 64 / CPR;     // rows a DMA of one wave fills
+    extern __shared__ uint4 smem_tile[];
+    __shared__ uint32_t word;
+    __shared__ float row_m[kTileRows], row_l[kTileRows];
+    const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem_tile;
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 31, half = lane >> 5;
+    // workgroup -> KV head (fastest), split, tile (the last rows, which see most keys, first)
+    int64_t id = blockIdx.x;
+    const int h = (int)(id % a.Hkv);
+    id /= a.Hkv;
+    const int split = (int)(id % a.splits);
+    id /= a.splits;
+    const int64_t t = a.tiles - 1 - id;
+    const int b = __builtin_amdgcn_readfirstlane(request_of_tile(a, t));
+    const Request rq = request_of(a, b);
+    const int G = a.G;
+    const int64_t rows_all = (int64_t)min(rq.n, a.max_q) * G;
+    const int64_t row0 = (t - tiles_before(a, b)) * kTileRows;
+    if (row0 < 0 || row0 >= rows_all || rows_all <= a.rows_most) return;
+    const int rows = (int)(rows_all - row0 < kTileRows ? rows_all - row0 : kTileRows);
+    const int wg_p0 = rq.first + (int)(row0 / G), wg_p1 = rq.first + (int)((row0 + rows - 1) / G);
+    const Blocks bl = blocks_of<6>(a, rq, wg_p0, wg_p1);
+    int per = a.split_blocks;
+    if ((int64_t)per * a.splits < bl.count) per = (bl.count + a.splits - 1) / a.splits;
+    const int nsplit = bl.count > per ? (bl.count + per - 1) / per : 1;
+    if (split >= nsplit) return;
+
+    const int64_t my_row = row0 + 32 * wave + n;
+    const bool row_ok = my_row < rows_all;
+    const int my_tok = (int)((row_ok ? my_row : row0) / G);
+    const int my_head = h * G + (int)((row_ok ? my_row : row0) - (int64_t)my_tok * G);
+    const int my_pos = row_ok ? rq.first + my_tok : INT32_MIN;
+    const bool wave_ok = 32 * wave < rows;
+    const int64_t last_row = row0 + 32 * wave + 31 < rows_all ? row0 + 32 * wave + 31 : rows_all - 1;
+    const int p0 = rq.first + (int)((row0 + 32 * wave) / G), p1 = rq.first + (int)(last_row / G);
+
+    uint4 qf[KS];
+    {
+        const uint16_t* src = a.q + (int64_t)(rq.t0 + my_tok) * a.q_stride + my_head * a.q_head + 8 * half;
 #pragma unroll
-        for (int x = 32; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor(M, x, 64));
-        const float ms = M == -INFINITY ? 0.f : M;
-        float L = 0.f;
-        for (int s = lane; s < nsplit; s += 64) {
-            const float ps = __hip_atomic_load(slabs + s * a.slab + 2 * row, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            const float pl = __hip_atomic_load(slabs + s * a.slab + 2 * row + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            const float f = exp2_fast(ps - ms);
-            wgt[row * nsplit + s] = f;
-            L += f * pl;
-        }
-        L = wave_sum(L);
-        if (lane == 0) {
-            row_m[row] = M;
-            row_l[row] = L;
+        for (int s = 0; s < KS; ++s) {
+            qf[s] = *reinterpret_cast<const uint4*>(src + 16 * s);
+            if (!row_ok) qf[s] = make_uint4(0, 0, 0, 0);
         }
     }
-    __syncthreads();
-    for (int u = tid; u < rows * (D / 2); u += kRowsThreads) {
-        const int row = u / (D / 2), d = (u - row * (D / 2)) * 2;
-        float x0 = 0.f, x1 = 0.f;
-        const float* base = slabs + 2 * rows + row * D + d;
-        constexpr int RS = 8;  // splits in flight
-        for (int s0 = 0; s0 < nsplit; s0 += RS) {
-            uint64_t v[RS];
+    f32x16 o[DB];
 #pragma unroll
-            for (int s = 0; s < RS; ++s)
-                v[s] = __hip_atomic_load(reinterpret_cast<const uint64_t*>(base + (int64_t)min(s0 + s, nsplit - 1) * a.slab),
-                                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int d = 0; d < DB; ++d)
 #pragma unroll
-            for (int s = 0; s < RS; ++s)
-                if (s0 + s < nsplit) {
-                    const float f = wgt[row * nsplit + s0 + s];
-                    x0 += f * __uint_as_float((uint32_t)v[s]);
-                    x1 += f * __uint_as_float((uint32_t)(v[s] >> 32));
+        for (int r = 0; r < 16; ++r) o[d][r] = 0.f;
+    float m = -INFINITY, l = 0.f;
+
+    const int i0 = split * per, i1 = min(bl.count, i0 + per);
+    // the table as constant memory: page ids come through the scalar cache and
+    // wait for no DMA in flight
+    const const_i32 trow = (const_i32)(uintptr_t)(a.table + (int64_t)b * a.table_stride);
+    const int last_key = rq.keys - 1;
+    const int page_mask = (1 << a.shift) - 1;
+
+    // DMA of a tile: wave w fills keys 16 w .. 16 w + 15, which lie in one
+    // page; lane -> (row lane / CPR, chunk lane % CPR) of each run of RPD rows
+    uint32_t dma_k[16 / RPD], dma_v[16 / RPD];  // byte offsets in the page's head from the first key of the wave
+#pragma unroll
+    for (int u = 0; u < 16 / RPD; ++u) {
+        const int r = u * RPD + lane / CPR, c = lane % CPR;
+        dma_k[u] = (uint32_t)(r * TG::kRowBytes + ((c ^ TG::kswz(r)) << 4));
+        dma_v[u] = (uint32_t)(r * TG::kRowBytes + ((c ^ TG::vswz(r)) << 4));
+    }
+    // The page of keys j .. j + 15 (j a multiple of 16), -1 where there is none
+    auto page_at = [&](int j) {
+        if (j > last_key) return -1;
+        const int pg = trow[j >> a.shift];
+        return (uint32_t)pg < (uint32_t)a.pages ? pg : -1;
+    };
+    auto issue = [&](int key0, int stage) {
+        const int j = key0 + 16 * wave;
+        const int pg = __builtin_amdgcn_readfirstlane(page_at(j));
+        const int64_t at = (int64_t)(pg < 0 ? 0 : pg) * a.page_stride + (((int64_t)h << a.shift) + (j & page_mask)) * D;
+        const uint32_t dst = lds + (uint32_t)(stage * TG::kStageBytes + 16 * wave * TG::kRowBytes);
+#pragma unroll
+        for (int u = 0; u < 16 / RPD; ++u) dma16s(a.k + at, dma_k[u], dst + 1024u * u);
+#pragma unroll
+        for (int u = 0; u < 16 / RPD; ++u) dma16s(a.v + at, dma_v[u], dst + (uint32_t)TG::kMatBytes + 1024u * u);
+    };
+    // LDS addresses of this lane's operands in stage 0
+    uint32_t kaddr[KS], vaddr[DB];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) kaddr[s] = (uint32_t)(n * TG::kRowBytes + (((2 * s + half) ^ TG::kswz(n)) << 4));
+    {
+        const int key = 4 * half + ((lane & 15) >> 2);
+        const int x = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+            vaddr[d] = (uint32_t)(TG::kMatBytes + key * TG::kRowBytes + (((4 * d + x) ^ TG::vswz(key)) << 4) + 8 * (lane & 1));
+    }
+    char* smem = reinterpret_cast<char*>(smem_tile);
+    uint32_t* poison = &word;  // set for good by the first such value the workgroup meets
+    if (tid == 0) *poison = 0u;
+
+    if (i0 < i1) issue(bl.at(i0) * kTileKeys, 0);
+    for (int i = i0; i < i1; ++i) {
+        const int stage = (i - i0) & 1;
+        const int key0 = bl.at(i) * kTileKeys;
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's part of the tile is in LDS
+        __syncthreads();                                  // everybody's, and the tile before is no longer read
+        if (i + 1 < i1) issue(bl.at(i + 1) * kTileKeys, stage ^ 1);
+        uint32_t there = 0;  // bit x: keys key0 + 16 x .. of the tile have a page
+#pragma unroll
+        for (int x = 0; x < 4; ++x) there |= (page_at(key0 + 16 * x) >= 0 ? 1u : 0u) << x;
+        there = __builtin_amdgcn_readfirstlane(there);
+
+        // Tiles that not every row sees whole: a weight of 0 times a value that
+        // is not finite would be NaN, so such values leave the tile first; the
+        // ones that some row sees are added in the end.
+        const int end = min(wg_p1, last_key);
+        bool masked = there != 15u || key0 + kTileKeys - 1 > min(wg_p0, last_key);
+        if (a.window > 0) masked = masked || (wg_p1 - key0 >= a.window && key0 + kTileKeys > a.sinks);
+        char* st = smem + stage * TG::kStageBytes;
+        if (masked) {
+            for (int u = tid; u < kTileKeys * CPR; u += kTileThreads) {
+                uint4* at = reinterpret_cast<uint4*>(st + TG::kMatBytes) + u;
+                const uint4 v = *at;
+                const uint32_t bx = nonfinite<E>(v.x), by = nonfinite<E>(v.y), bz = nonfinite<E>(v.z), bw = nonfinite<E>(v.w);
+                if (bx | by | bz | bw) {
+                    *at = make_uint4(v.x & ~((bx >> 15) * 0xFFFFu), v.y & ~((by >> 15) * 0xFFFFu),
+                                     v.z & ~((bz >> 15) * 0xFFFFu), v.w & ~((bw >> 15) * 0xFFFFu));
+                    const int x = u / CPR, j = key0 + x;
+                    if (j <= end && ((there >> (x >> 4)) & 1u) && !(a.window > 0 && wg_p0 - j >= a.window && j >= a.sinks))
+                        *poison = 1u;
+                }
+            }
+            __syncthreads();
+        }
+        if (!wave_ok || key0 > p1) continue;
+        if (a.window > 0 && p0 - (key0 + kTileKeys - 1) >= a.window && key0 >= a.sinks) continue;
+
+        f32x16 s[2];
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[kt][r] = 0.f;
+#pragma unroll
+            for (int x = 0; x < KS; ++x) {
+                const uint4 kf = *reinterpret_cast<const uint4*>(st + kaddr[x] + 32 * kt * TG::kRowBytes);
+                s[kt] = E::mfma32(kf, qf[x], s[kt]);
+            }
+        }
+        // tiles that every row of the wave sees whole need no mask
+        bool whole = there == 15u && key0 + kTileKeys - 1 <= min(p0, last_key);
+        if (a.window > 0) whole = whole && (p1 - key0 < a.window || key0 + kTileKeys <= a.sinks);
+        if (!whole) {
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int x = 32 * kt + 8 * (r >> 2) + 4 * half + (r & 3), j = key0 + x;
+                    if (!((there >> (x >> 4)) & 1u) || j > last_key || !sees(a, my_pos, j)) s[kt][r] = -INFINITY;
                 }
         }
-        const float L = row_l[row];
-        const int64_t r = row0 + row;
-        const int tok = (int)(r / G);
-        const int64_t at = (int64_t)(rq.t0 + tok) * a.Hq + h * G + (int)(r - (int64_t)tok * G);
-        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN);
-        *reinterpret_cast<uint32_t*>(a.out + at * D + d) = E::pack2(x0 * inv, x1 * inv);
-        if (d == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : kLn2 * (row_m[row] + log2f(L));
+        // running maximum of the scaled scores, raised as in the rows kernel
+        float mx = s[0][0];
+#pragma unroll
+        for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[0][r]);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[1][r]);
+        mx *= a.scale_log2;
+        if (__any(mx > m + 8.f)) {
+            mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+            const float mn = fmaxf(m, mx);
+            const float f = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DB; ++d) o[d] *= f;
+        }
+        const float ms = m == -INFINITY ? 0.f : m;
+        uint32_t pw[16];
+        float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int r = 0; r < 16; r += 2) {
+                const float x0 = exp2_fast(fmaf(s[kt][r], a.scale_log2, -ms)), x1 = exp2_fast(fmaf(s[kt][r + 1], a.scale_log2, -ms));
+                add[r & 2] += x0;
+                add[(r & 2) + 1] += x1;
+                pw[8 * kt + r / 2] = E::pack2(x0, x1);
+            }
+        l += (add[0] + add[1]) + (add[2] + add[3]);
+
+        // step x: keys 16 x .. 16 x + 15
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const uint4 pf = make_uint4(pw[4 * x], pw[4 * x + 1], pw[4 * x + 2], pw[4 * x + 3]);
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+                const uint32_t at = lds + (uint32_t)(stage * TG::kStageBytes) + vaddr[d] + (uint32_t)(16 * x * TG::kRowBytes);
+                const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                               (lds_s16x4*)(uintptr_t)at));
+                const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                               (lds_s16x4*)(uintptr_t)(at + 8 * TG::kRowBytes)));
+                const uint4 vf = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                o[d] = E::mfma32(vf, pf, o[d]);
+            }
+        }
+        if (masked && *poison) {
+            // A value that some rows see and others do not is not finite (it
+            // is zero in LDS): such values are added one by one, from their
+            // page, to the rows that see them.  Lane (n, half) owns row n,
+            // columns 8 y + 4 half .. + 3.
+            for (int x = 0; x < kTileKeys; ++x) {
+                const int j = key0 + x, src = n + 32 * ((x >> 2) & 1), pg = page_at(j);
+                float p = 0.f;
+#pragma unroll
+                for (int w = 0; w < 16; ++w) {
+                    // dword w holds keys 32 (w / 8) + 8 ((w % 8) / 2) + 4 half + 2 (w % 2) and the next
+                    const int k = 32 * (w >> 3) + 8 * ((w & 7) >> 1) + 2 * (w & 1);
+                    const uint32_t got = __shfl(pw[w], src, 64);
+                    if (k == (x & ~5)) p = (x & 1) ? E::hi(got) : E::lo(got);
+                }
+                if (pg < 0 || !sees(a, my_pos, j)) continue;
+                const uint16_t* row = a.v + (int64_t)pg * a.page_stride + (((int64_t)h << a.shift) + (j & page_mask)) * D;
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const uint32_t w = row[32 * d + 8 * (r >> 2) + 4 * half + (r & 3)];
+                        if (nonfinite<E>(w) & 0x8000u) o[d][r] = fmaf(p, E::lo(w), o[d][r]);
+                    }
+            }
+        }
     }
+    l += __shfl_xor(l, 32, 64);
+
+    const bool parts = nsplit > 1;
+    const int64_t wg_tile = t * a.Hkv + h;
+    if (!parts) {
+        if (!row_ok) return;
+        const int64_t at = (int64_t)(rq.t0 + my_tok) * a.Hq + my_head;
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : NAN);
+        uint16_t* dst = a.out + at * D + 4 * half;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                *reinterpret_cast<uint2*>(dst + 32 * d + 8 * y) =
+                    make_uint2(E::pack2(o[d][4 * y] * inv, o[d][4 * y + 1] * inv), E::pack2(o[d][4 * y + 2] * inv, o[d][4 * y + 3] * inv));
+        if (half == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+        return;
+    }
+    float* slab = a.partials + (wg_tile * a.splits + split) * a.slab;  // [128][2], then [128][D]
+    if (row_ok) {
+        const int row = 32 * wave + n;
+        if (half == 0) {
+            store_partial(slab + 2 * row, m);
+            store_partial(slab + 2 * row + 1, l);
+        }
+        float* dst = slab + 2 * kTileRows + row * D + 4 * half;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) store_partial(dst + 32 * d + 8 * (r >> 2) + (r & 3), o[d][r]);
+    }
+    if (!split_last_arrival(a.flags, (uint32_t)wg_tile, nsplit, &word)) return;
+    join_splits<E, D>(a, rq, h, row0, rows, 2 * kTileRows, wg_tile, nsplit, reinterpret_cast<float*>(smem_tile), row_m, row_l);
 }
 
 }  // namespace
 
-// Schedule of a call.  Row tiles a workgroup holds: as many as the largest
-// request needs, up to 4 (its waves then share the keys).  The key axis is
-// split until the grid has about 8 workgroups a compute unit (lengths are
-// ragged, and short splits even them out), but no split is shorter than
-// 8 blocks: below that its partial results cost more than its keys.
+// Schedule of a call.
+//
+// Requests of more than kRowsMost rows (new tokens times the group's heads)
+// go to the tile kernel, the others to the rows kernel; a call whose requests
+// may be of both kinds launches both, one request alone the one it needs.
+//
+// Rows kernel: row tiles a workgroup holds: as many as its largest request
+// needs, up to 4 (its waves then share the keys).  The key axis is split
+// until the grid has about 8 workgroups a compute unit (lengths are ragged,
+// and short splits even them out), but no split is shorter than 8 blocks:
+// below that its partial results cost more than its keys.
+//
+// Tile kernel: split until the grid has about 4 workgroups a compute unit (two
+// are resident), no split shorter than 8 tiles.
+constexpr int64_t kRowsMost = 64;
+
+namespace {
+
+// Splits of `blocks` key blocks: `per` blocks each, at least `least`, such
+// that `tiles` tiles make about `want` workgroups; at most `most` splits.
+int64_t split_keys(int64_t tiles, int64_t blocks, int64_t want, int64_t least, int64_t most, int64_t* per_out) {
+    *per_out = blocks > 0 ? blocks : 1;
+    if (tiles > kMaxFlags || blocks <= least) return 1;
+    int64_t per = (tiles * blocks + want - 1) / want;
+    if (per < least) per = least;
+    int64_t s = (blocks + per - 1) / per;
+    if (s > most) s = most;
+    per = (blocks + s - 1) / s;
+    *per_out = per;
+    return (blocks + per - 1) / per;
+}
+
+}  // namespace
+
 AttnPlan attn_plan(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q, int64_t max_kv, int64_t window,
                    int64_t sinks, int compute_units) {
     AttnPlan p{};
     const int64_t G = Hq / Hkv;
     if (max_q > T) max_q = T;
-    const int64_t rows = max_q * G;
-    p.R = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-    p.row_groups = (rows + 16 * p.R - 1) / (16 * p.R);
-    const int64_t tiles = B * p.row_groups * Hkv;
-    int64_t keys = max_kv;
-    if (window > 0) {
-        const int64_t reach = window + sinks + (16 * p.R + G - 1) / G + 2 * kBlockKeys;
-        if (reach < keys) keys = reach;
+    int64_t rows = max_q * G;
+    const bool large = rows > kRowsMost;
+    // the keys that a run of `r` rows reads, at most
+    auto reach = [&](int64_t r) {
+        const int64_t w = window + sinks + (r + G - 1) / G + 2 * kTileKeys;
+        return window > 0 && w < max_kv ? w : max_kv;
+    };
+    size_t bytes = 0;
+    if (large) {
+        p.rows_most = B > 1 ? kRowsMost : 0;
+        p.tiles = T * G / kTileRows + B;
+        const int64_t blocks = (reach(kTileRows) + kTileKeys - 1) / kTileKeys;
+        p.tile_splits = split_keys(p.tiles * Hkv, blocks, compute_units * 4, 8, D == 128 ? 128 : 64, &p.tile_split_blocks);
+        p.tile_slab = kTileRows * (D + 2);
+        if (p.tile_splits > 1) bytes = (size_t)(p.tiles * Hkv * p.tile_splits * p.tile_slab) * 4;
+        rows = kRowsMost;
+    } else {
+        p.rows_most = rows;
     }
-    const int64_t blocks = (keys + kBlockKeys - 1) / kBlockKeys;
-    p.splits = 1;
-    p.split_blocks = blocks > 0 ? blocks : 1;
-    if (tiles <= kMaxFlags && blocks > 8) {
-        int64_t per = (tiles * blocks + compute_units * 8 - 1) / (compute_units * 8);
-        if (per < 8) per = 8;
-        int64_t s = (blocks + per - 1) / per;
-        const int64_t most = 256 / p.R;  // the join's weights: splits * rows <= 4096 floats of LDS
-        if (s > most) s = most;
-        per = (blocks + s - 1) / s;
-        p.splits = (blocks + per - 1) / per;
-        p.split_blocks = per;
+    if (p.rows_most > 0) {
+        p.R = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+        p.row_groups = (rows + 16 * p.R - 1) / (16 * p.R);
+        const int64_t tiles = B * p.row_groups * Hkv;
+        const int64_t blocks = (reach(16 * p.R) + kBlockKeys - 1) / kBlockKeys;
+        // the join's weights: splits * rows <= 4096 floats of LDS
+        p.splits = split_keys(tiles, blocks, compute_units * 8, 8, 256 / p.R, &p.split_blocks);
+        p.slab = (rows < 16 * p.R ? rows : 16 * p.R) * (D + 2);
+        if (p.splits > 1) {
+            const size_t need = (size_t)(tiles * p.splits * p.slab) * 4;
+            if (need > bytes) bytes = need;
+        }
     }
-    const int64_t held = rows < 16 * p.R ? rows : 16 * p.R;
-    p.slab = held * (D + 2);
-    p.data_bytes = p.splits > 1 ? (size_t)(tiles * p.splits * p.slab) * 4 : 0;
+    p.data_bytes = bytes;
     return p;
 }
 
+namespace {
+
+template <class E, int D>
+hipError_t launch_rows(const AttnArgs& a, unsigned grid, hipStream_t s) {
+    rows_kernel<E, D><<<dim3(grid), dim3(kRowsThreads), 0, s>>>(a);
+    return hipGetLastError();
+}
+
+template <class E, int D>
+hipError_t launch_tiles(const AttnArgs& a, unsigned grid, hipStream_t s) {
+    static DeviceFlags raised;
+    const hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&tile_kernel<E, D>), TileGeom<D>::kLdsBytes, raised);
+    if (e != hipSuccess) return e;
+    tile_kernel<E, D><<<dim3(grid), dim3(kTileThreads), TileGeom<D>::kLdsBytes, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_attention(const AttnArgs& args, const AttnPlan& plan, hipStream_t s) {
     AttnArgs a = args;
+    a.rows_most = plan.rows_most;
+    if (plan.tiles > 0) {
+        a.tiles = plan.tiles;
+        a.splits = a.partials ? (int)plan.tile_splits : 1;
+        a.split_blocks = (int)plan.tile_split_blocks;
+        a.slab = plan.tile_slab;
+        const int64_t grid = plan.tiles * a.splits * a.Hkv;
+        if (grid <= 0 || grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+        const unsigned gd = (unsigned)grid;
+        const hipError_t e = a.bf16 ? (a.D == 64 ? launch_tiles<AttnBF16, 64>(a, gd, s) : launch_tiles<AttnBF16, 128>(a, gd, s))
+                                    : (a.D == 64 ? launch_tiles<AttnF16, 64>(a, gd, s) : launch_tiles<AttnF16, 128>(a, gd, s));
+        if (e != hipSuccess) return e;
+    }
+    if (plan.rows_most == 0) return hipSuccess;
     a.R = plan.R;
     a.row_groups = (int)plan.row_groups;
-    a.splits = (int)plan.splits;
+    a.splits = a.partials ? (int)plan.splits : 1;
     a.split_blocks = (int)plan.split_blocks;
     a.slab = plan.slab;
-    const int64_t grid = (int64_t)a.B * plan.row_groups * plan.splits * a.Hkv;
+    const int64_t grid = (int64_t)a.B * plan.row_groups * a.splits * a.Hkv;
     if (grid <= 0 || grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-    const dim3 gd((unsigned)grid), bd(kRowsThreads);
-    if (a.bf16) {
-        if (a.D == 64) rows_kernel<AttnBF16, 64><<<gd, bd, 0, s>>>(a);
-        else rows_kernel<AttnBF16, 128><<<gd, bd, 0, s>>>(a);
-    } else {
-        if (a.D == 64) rows_kernel<AttnF16, 64><<<gd, bd, 0, s>>>(a);
-        else rows_kernel<AttnF16, 128><<<gd, bd, 0, s>>>(a);
-    }
-    return hipGetLastError();
+    const unsigned gd = (unsigned)grid;
+    if (a.bf16) return a.D == 64 ? launch_rows<AttnBF16, 64>(a, gd, s) : launch_rows<AttnBF16, 128>(a, gd, s);
+    return a.D == 64 ? launch_rows<AttnF16, 64>(a, gd, s) : launch_rows<AttnF16, 128>(a, gd, s);
 }
 
 }  // namespace tq

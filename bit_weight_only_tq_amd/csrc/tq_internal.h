@@ -202,12 +202,21 @@ struct AttnArgs {
     uint16_t* out;
     float* lse;  // or nullptr
     // schedule (set by the launcher)
-    float* partials;
+    float* partials;  // nullptr: no split
     uint32_t* flags;
+    int64_t rows_most;  // requests of more rows are the tile kernel's
+    int64_t tiles;      // of the tile kernel, with room for every request's last
     int R, row_groups, splits, split_blocks;
     int64_t slab;
 };
 struct AttnPlan {
+    // tile kernel
+    int64_t tiles;              // 0: not launched
+    int64_t tile_splits;        // workgroups over a tile's keys
+    int64_t tile_split_blocks;  // key tiles of a split
+    int64_t tile_slab;          // floats of one split's partial result
+    // rows kernel
+    int64_t rows_most;    // 0: not launched
     int R;                // 16-row tiles a workgroup holds
     int64_t row_groups;   // workgroups over the rows of the largest request
     int64_t splits;       // workgroups over its keys

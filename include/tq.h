@@ -458,8 +458,10 @@ tq_status tq_kv_append(const void* q, int64_t q_stride, int64_t q_head, const vo
  *              between heads (multiples of 8).  Query head i reads KV head
  *              i / (Hq / Hkv); Hq is a multiple of Hkv; D is 64 or 128.
  *   page_table [B] rows of `width` page ids, table_stride elements apart.
- *   cu_q       [B + 1] request b's new tokens are cu_q[b] .. cu_q[b + 1] - 1
- *              (0 <= cu_q[b] and cu_q[b + 1] <= T; other requests are skipped).
+ *   cu_q       [B + 1] ascending: request b's new tokens are cu_q[b] ..
+ *              cu_q[b + 1] - 1 (0 <= cu_q[b] and cu_q[b + 1] <= T; a request
+ *              whose offsets are not so is skipped, and requests after it may
+ *              be).
  *   kv_lens    [B] its keys, the new tokens' own (already appended) included:
  *              new token i of n sits at position kv - n + i.
  *   max_q      at least the largest number of new tokens of a request (more
