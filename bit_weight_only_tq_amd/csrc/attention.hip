@@ -466,9 +466,13 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
 // column.  So the weights never leave their registers, and a row's maximum
 // and sum need no exchange between lanes but where the maximum is raised.
 //
-// 16-byte chunks of a row are stored at chunk ^ f(key): with f = key % 16
-// (K, D = 128), key % 8 (K, D = 64), 2 (key % 8) (V, D = 128) and 2 (key % 4)
-// (V, D = 64) the lanes that read together fall into different banks.
+// 16-byte chunks of a row are stored at chunk ^ f(key) (kswz, vswz), so that 8
+// or 16 lanes of a K read, and 16 or 32 of a V read (4 keys, 32 or 64 bytes of
+// each), fall into different banks.
+//
+// The scores of tile i + 1 are computed in the same run of instructions as the
+// exponentials and the products with V of tile i, so that the matrix cores and
+// the vector unit work at once within a wave: K runs one tile ahead of V.
 constexpr int kTileKeys = 64;
 constexpr int kTileRows = 128;
 constexpr int kTileThreads = 256;
@@ -481,10 +485,13 @@ template <int D>
 struct TileGeom {
     static constexpr int kRowBytes = D * 2;
     static constexpr int kMatBytes = kTileKeys * kRowBytes;  // one of K and V
-    static constexpr int kStageBytes = 2 * kMatBytes;
-    static constexpr int kLdsBytes = 2 * kStageBytes;
-    static __device__ __forceinline__ int kswz(int key) { return D == 128 ? (key & 15) : (key & 7); }
-    static __device__ __forceinline__ int vswz(int key) { return D == 128 ? 2 * (key & 7) : 2 * (key & 3); }
+    static constexpr int kLdsBytes = 4 * kMatBytes;          // two of K, then two of V
+    static __device__ __forceinline__ int kswz(int key) {
+        return D == 128 ? (key & 15) : ((key & 7) ^ ((key >> 3) & 1));
+    }
+    static __device__ __forceinline__ int vswz(int key) {
+        return D == 128 ? 2 * ((key & 3) ^ ((key & 3) << 1)) : 2 * (key & 3);
+    }
 };
 
 // The request of tile `t` of a call: request b's tiles begin at
@@ -510,7 +517,7 @@ __device__ __forceinline__ int request_of_tile(const AttnArgs& a, int64_t t) {
 }
 
 template <class E, int D>
-__global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(AttnArgs a) {
     using TG = TileGeom<D>;
     constexpr int KS = D / 16;        // steps of S^T = K Q^T
     constexpr int DB = D / 32;        // 32-column blocks of O
@@ -591,17 +598,38 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(AttnArgs a) {
         const int pg = trow[j >> a.shift];
         return (uint32_t)pg < (uint32_t)a.pages ? pg : -1;
     };
-    auto issue = [&](int key0, int stage) {
-        const int j = key0 + 16 * wave;
-        const int pg = __builtin_amdgcn_readfirstlane(page_at(j));
-        const int64_t at = (int64_t)(pg < 0 ? 0 : pg) * a.page_stride + (((int64_t)h << a.shift) + (j & page_mask)) * D;
-        const uint32_t dst = lds + (uint32_t)(stage * TG::kStageBytes + 16 * wave * TG::kRowBytes);
-#pragma unroll
-        for (int u = 0; u < 16 / RPD; ++u) dma16s(a.k + at, dma_k[u], dst + 1024u * u);
-#pragma unroll
-        for (int u = 0; u < 16 / RPD; ++u) dma16s(a.v + at, dma_v[u], dst + (uint32_t)TG::kMatBytes + 1024u * u);
+    // A tile: its first key, which of its four runs of 16 keys have a page, and
+    // where this wave's run lies in the caches
+    struct Tile {
+        int key0;
+        uint32_t there;
+        int64_t at;
     };
-    // LDS addresses of this lane's operands in stage 0
+    auto tile_at = [&](int i) {
+        Tile t;
+        t.key0 = bl.at(i < i1 ? i : i1 - 1) * kTileKeys;
+        t.there = 0;
+        int mine = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int pg = page_at(t.key0 + 16 * x);
+            t.there |= (pg >= 0 ? 1u : 0u) << x;
+            if (x == wave) mine = pg < 0 ? 0 : pg;
+        }
+        t.at = (int64_t)mine * a.page_stride + (((int64_t)h << a.shift) + ((t.key0 + 16 * wave) & page_mask)) * D;
+        return t;
+    };
+    auto issue_k = [&](const Tile& t, int i) {
+        const uint32_t dst = lds + (uint32_t)((i & 1) * TG::kMatBytes + 16 * wave * TG::kRowBytes);
+#pragma unroll
+        for (int u = 0; u < 16 / RPD; ++u) dma16s(a.k + t.at, dma_k[u], dst + 1024u * u);
+    };
+    auto issue_v = [&](const Tile& t, int i) {
+        const uint32_t dst = lds + (uint32_t)((2 + (i & 1)) * TG::kMatBytes + 16 * wave * TG::kRowBytes);
+#pragma unroll
+        for (int u = 0; u < 16 / RPD; ++u) dma16s(a.v + t.at, dma_v[u], dst + 1024u * u);
+    };
+    // this lane's operands: byte offsets in a K and in a V tile
     uint32_t kaddr[KS], vaddr[DB];
 #pragma unroll
     for (int s = 0; s < KS; ++s) kaddr[s] = (uint32_t)(n * TG::kRowBytes + (((2 * s + half) ^ TG::kswz(n)) << 4));
@@ -610,50 +638,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(AttnArgs a) {
         const int x = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
 #pragma unroll
         for (int d = 0; d < DB; ++d)
-            vaddr[d] = (uint32_t)(TG::kMatBytes + key * TG::kRowBytes + (((4 * d + x) ^ TG::vswz(key)) << 4) + 8 * (lane & 1));
+            vaddr[d] = (uint32_t)(key * TG::kRowBytes + (((4 * d + x) ^ TG::vswz(key)) << 4) + 8 * (lane & 1));
     }
     char* smem = reinterpret_cast<char*>(smem_tile);
     uint32_t* poison = &word;  // set for good by the first such value the workgroup meets
     if (tid == 0) *poison = 0u;
 
-    if (i0 < i1) issue(bl.at(i0) * kTileKeys, 0);
-    for (int i = i0; i < i1; ++i) {
-        const int stage = (i - i0) & 1;
-        const int key0 = bl.at(i) * kTileKeys;
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's part of the tile is in LDS
-        __syncthreads();                                  // everybody's, and the tile before is no longer read
-        if (i + 1 < i1) issue(bl.at(i + 1) * kTileKeys, stage ^ 1);
-        uint32_t there = 0;  // bit x: keys key0 + 16 x .. of the tile have a page
-#pragma unroll
-        for (int x = 0; x < 4; ++x) there |= (page_at(key0 + 16 * x) >= 0 ? 1u : 0u) << x;
-        there = __builtin_amdgcn_readfirstlane(there);
-
-        // Tiles that not every row sees whole: a weight of 0 times a value that
-        // is not finite would be NaN, so such values leave the tile first; the
-        // ones that some row sees are added in the end.
-        const int end = min(wg_p1, last_key);
-        bool masked = there != 15u || key0 + kTileKeys - 1 > min(wg_p0, last_key);
-        if (a.window > 0) masked = masked || (wg_p1 - key0 >= a.window && key0 + kTileKeys > a.sinks);
-        char* st = smem + stage * TG::kStageBytes;
-        if (masked) {
-            for (int u = tid; u < kTileKeys * CPR; u += kTileThreads) {
-                uint4* at = reinterpret_cast<uint4*>(st + TG::kMatBytes) + u;
-                const uint4 v = *at;
-                const uint32_t bx = nonfinite<E>(v.x), by = nonfinite<E>(v.y), bz = nonfinite<E>(v.z), bw = nonfinite<E>(v.w);
-                if (bx | by | bz | bw) {
-                    *at = make_uint4(v.x & ~((bx >> 15) * 0xFFFFu), v.y & ~((by >> 15) * 0xFFFFu),
-                                     v.z & ~((bz >> 15) * 0xFFFFu), v.w & ~((bw >> 15) * 0xFFFFu));
-                    const int x = u / CPR, j = key0 + x;
-                    if (j <= end && ((there >> (x >> 4)) & 1u) && !(a.window > 0 && wg_p0 - j >= a.window && j >= a.sinks))
-                        *poison = 1u;
-                }
-            }
-            __syncthreads();
-        }
-        if (!wave_ok || key0 > p1) continue;
-        if (a.window > 0 && p0 - (key0 + kTileKeys - 1) >= a.window && key0 >= a.sinks) continue;
-
-        f32x16 s[2];
+    f32x16 s[2];  // scores of the tile to come
+    auto scores = [&](int i) {
+        const char* st = smem + (i & 1) * TG::kMatBytes;
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt) {
 #pragma unroll
@@ -664,87 +657,148 @@ __global__ __launch_bounds__(kTileThreads, 2) void tile_kernel(AttnArgs a) {
                 s[kt] = E::mfma32(kf, qf[x], s[kt]);
             }
         }
-        // tiles that every row of the wave sees whole need no mask
-        bool whole = there == 15u && key0 + kTileKeys - 1 <= min(p0, last_key);
-        if (a.window > 0) whole = whole && (p1 - key0 < a.window || key0 + kTileKeys <= a.sinks);
-        if (!whole) {
+    };
+    Tile cur{}, next{};
+    if (i0 < i1) {
+        cur = tile_at(i0);
+        issue_k(cur, i0);
+        next = tile_at(i0 + 1);
+        issue_v(cur, i0);
+        if (i0 + 1 < i1) {
+            issue_k(next, i0 + 1);
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * (16 / RPD)) : "memory");  // K of the first tile is in LDS
+        } else {
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(16 / RPD) : "memory");
+        }
+        __syncthreads();
+        scores(i0);
+        for (int i = i0; i < i1; ++i) {
+            const Tile tile = cur;
+            const int key0 = tile.key0;
+            const uint32_t there = tile.there;
+            cur = next;
+            next = tile_at(i + 2);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's part of V of tile i and of K of tile i + 1
+            __syncthreads();                                  // everybody's, and what the next DMAs replace is read
+            if (i + 2 < i1) issue_k(next, i + 2);  // no DMA is in flight when the loop ends
+            if (i + 1 < i1) issue_v(cur, i + 1);
+
+            // Tiles that not every row sees whole: a weight of 0 times a value that
+            // is not finite would be NaN, so such values leave the tile first; the
+            // ones that some row sees are added in the end.
+            const int end = min(wg_p1, last_key);
+            bool masked = there != 15u || key0 + kTileKeys - 1 > min(wg_p0, last_key);
+            if (a.window > 0) masked = masked || (wg_p1 - key0 >= a.window && key0 + kTileKeys > a.sinks);
+            if (masked) {
+                char* st = smem + (2 + (i & 1)) * TG::kMatBytes;
+                int u0 = tid;
+                asm volatile("" : "+v"(u0));  // nothing of this path is held in registers through the loop
+                for (int u = u0; u < kTileKeys * CPR; u += kTileThreads) {
+                    uint4* at = reinterpret_cast<uint4*>(st) + u;
+                    const uint4 v = *at;
+                    const uint32_t bx = nonfinite<E>(v.x), by = nonfinite<E>(v.y), bz = nonfinite<E>(v.z), bw = nonfinite<E>(v.w);
+                    if (bx | by | bz | bw) {
+                        *at = make_uint4(v.x & ~((bx >> 15) * 0xFFFFu), v.y & ~((by >> 15) * 0xFFFFu),
+                                         v.z & ~((bz >> 15) * 0xFFFFu), v.w & ~((bw >> 15) * 0xFFFFu));
+                        const int x = u / CPR, j = key0 + x;
+                        if (j <= end && ((there >> (x >> 4)) & 1u) && !(a.window > 0 && wg_p0 - j >= a.window && j >= a.sinks))
+                            *poison = 1u;
+                    }
+                }
+                __syncthreads();
+            }
+            if (!wave_ok) continue;  // no rows: this wave only helps to fill the tiles
+            // tiles that every row of the wave sees whole need no mask
+            bool whole = there == 15u && key0 + kTileKeys - 1 <= min(p0, last_key);
+            if (a.window > 0) whole = whole && (p1 - key0 < a.window || key0 + kTileKeys <= a.sinks);
+            if (!whole) {
+                // key x of the tile (x - 4 half below, a constant) is seen up to
+                // `most`, and with a window above `low` or below `sink`
+                const int base = key0 + 4 * half;
+                const int most = min(my_pos, last_key) - base;
+                const int low = a.window > 0 ? my_pos - a.window - base : INT32_MIN, sink = a.sinks - base;
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int x = 32 * kt + 8 * (r >> 2) + (r & 3);
+                        if (!((there >> (x >> 4)) & 1u) || x > most || (x <= low && x >= sink)) s[kt][r] = -INFINITY;
+                    }
+            }
+            // running maximum of the scaled scores, raised as in the rows kernel
+            float mx = s[0][0];
+#pragma unroll
+            for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[0][r]);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[1][r]);
+            mx *= a.scale_log2;
+            if (__any(mx > m + 8.f)) {
+                mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+                const float mn = fmaxf(m, mx);
+                const float f = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
+                m = mn;
+                l *= f;
+#pragma unroll
+                for (int d = 0; d < DB; ++d) o[d] *= f;
+            }
+            const float ms = m == -INFINITY ? 0.f : m;
+            const f32x16 sc[2] = {s[0], s[1]};
+            scores(i + 1);  // past the last tile: of what its buffer holds, not used
+            uint32_t pw[16];
+            float add[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int x = 32 * kt + 8 * (r >> 2) + 4 * half + (r & 3), j = key0 + x;
-                    if (!((there >> (x >> 4)) & 1u) || j > last_key || !sees(a, my_pos, j)) s[kt][r] = -INFINITY;
+                for (int r = 0; r < 16; r += 2) {
+                    const float x0 = exp2_fast(fmaf(sc[kt][r], a.scale_log2, -ms)), x1 = exp2_fast(fmaf(sc[kt][r + 1], a.scale_log2, -ms));
+                    add[r & 2] += x0;
+                    add[(r & 2) + 1] += x1;
+                    pw[8 * kt + r / 2] = E::pack2(x0, x1);
                 }
-        }
-        // running maximum of the scaled scores, raised as in the rows kernel
-        float mx = s[0][0];
-#pragma unroll
-        for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[0][r]);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[1][r]);
-        mx *= a.scale_log2;
-        if (__any(mx > m + 8.f)) {
-            mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-            const float mn = fmaxf(m, mx);
-            const float f = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
-            m = mn;
-            l *= f;
-#pragma unroll
-            for (int d = 0; d < DB; ++d) o[d] *= f;
-        }
-        const float ms = m == -INFINITY ? 0.f : m;
-        uint32_t pw[16];
-        float add[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int r = 0; r < 16; r += 2) {
-                const float x0 = exp2_fast(fmaf(s[kt][r], a.scale_log2, -ms)), x1 = exp2_fast(fmaf(s[kt][r + 1], a.scale_log2, -ms));
-                add[r & 2] += x0;
-                add[(r & 2) + 1] += x1;
-                pw[8 * kt + r / 2] = E::pack2(x0, x1);
-            }
-        l += (add[0] + add[1]) + (add[2] + add[3]);
+            l += (add[0] + add[1]) + (add[2] + add[3]);
 
-        // step x: keys 16 x .. 16 x + 15
+            // step x: keys 16 x .. 16 x + 15
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const uint4 pf = make_uint4(pw[4 * x], pw[4 * x + 1], pw[4 * x + 2], pw[4 * x + 3]);
+            for (int x = 0; x < 4; ++x) {
+                const uint4 pf = make_uint4(pw[4 * x], pw[4 * x + 1], pw[4 * x + 2], pw[4 * x + 3]);
 #pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                const uint32_t at = lds + (uint32_t)(stage * TG::kStageBytes) + vaddr[d] + (uint32_t)(16 * x * TG::kRowBytes);
-                const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                               (lds_s16x4*)(uintptr_t)at));
-                const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                               (lds_s16x4*)(uintptr_t)(at + 8 * TG::kRowBytes)));
-                const uint4 vf = make_uint4(lo.x, lo.y, hi.x, hi.y);
-                o[d] = E::mfma32(vf, pf, o[d]);
-            }
-        }
-        if (masked && *poison) {
-            // A value that some rows see and others do not is not finite (it
-            // is zero in LDS): such values are added one by one, from their
-            // page, to the rows that see them.  Lane (n, half) owns row n,
-            // columns 8 y + 4 half .. + 3.
-            for (int x = 0; x < kTileKeys; ++x) {
-                const int j = key0 + x, src = n + 32 * ((x >> 2) & 1), pg = page_at(j);
-                float p = 0.f;
-#pragma unroll
-                for (int w = 0; w < 16; ++w) {
-                    // dword w holds keys 32 (w / 8) + 8 ((w % 8) / 2) + 4 half + 2 (w % 2) and the next
-                    const int k = 32 * (w >> 3) + 8 * ((w & 7) >> 1) + 2 * (w & 1);
-                    const uint32_t got = __shfl(pw[w], src, 64);
-                    if (k == (x & ~5)) p = (x & 1) ? E::hi(got) : E::lo(got);
+                for (int d = 0; d < DB; ++d) {
+                    const uint32_t at = lds + (uint32_t)((2 + (i & 1)) * TG::kMatBytes) + vaddr[d] + (uint32_t)(16 * x * TG::kRowBytes);
+                    const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                                   (lds_s16x4*)(uintptr_t)at));
+                    const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                                   (lds_s16x4*)(uintptr_t)(at + 8 * TG::kRowBytes)));
+                    const uint4 vf = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                    o[d] = E::mfma32(vf, pf, o[d]);
                 }
-                if (pg < 0 || !sees(a, my_pos, j)) continue;
-                const uint16_t* row = a.v + (int64_t)pg * a.page_stride + (((int64_t)h << a.shift) + (j & page_mask)) * D;
+            }
+            if (masked && *poison) {
+                // A value that some rows see and others do not is not finite (it
+                // is zero in LDS): such values are added one by one, from their
+                // page, to the rows that see them.  Lane (n, half) owns row n,
+                // columns 8 y + 4 half .. + 3.
+                int n_ = n, half_ = half;
+                asm volatile("" : "+v"(n_), "+v"(half_));  // as above
+                for (int x = 0; x < kTileKeys; ++x) {
+                    const int j = key0 + x, src = n_ + 32 * ((x >> 2) & 1), pg = page_at(j);
+                    float p = 0.f;
 #pragma unroll
-                for (int d = 0; d < DB; ++d)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const uint32_t w = row[32 * d + 8 * (r >> 2) + 4 * half + (r & 3)];
-                        if (nonfinite<E>(w) & 0x8000u) o[d][r] = fmaf(p, E::lo(w), o[d][r]);
+                    for (int w = 0; w < 16; ++w) {
+                        // dword w holds keys 32 (w / 8) + 8 ((w % 8) / 2) + 4 half + 2 (w % 2) and the next
+                        const int k = 32 * (w >> 3) + 8 * ((w & 7) >> 1) + 2 * (w & 1);
+                        const uint32_t got = __shfl(pw[w], src, 64);
+                        if (k == (x & ~5)) p = (x & 1) ? E::hi(got) : E::lo(got);
                     }
+                    if (pg < 0 || !sees(a, my_pos, j)) continue;
+                    const uint16_t* row = a.v + (int64_t)pg * a.page_stride + (((int64_t)h << a.shift) + (j & page_mask)) * D;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            const uint32_t w = row[32 * d + 8 * (r >> 2) + 4 * half_ + (r & 3)];
+                            if (nonfinite<E>(w) & 0x8000u) o[d][r] = fmaf(p, E::lo(w), o[d][r]);
+                        }
+                }
             }
         }
     }
