@@ -480,6 +480,30 @@ constexpr int kTileThreads = 256;
 typedef const __attribute__((address_space(4))) int32_t* const_i32;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) char lds_char;
+
+// 8 bytes a lane from LDS, transposed over 16 lanes: lane i of the 16 gives
+// the address of 4 values of row i / 4, columns 4 (i % 4) .. + 3, and gets the
+// values of column i in the four rows.
+__device__ __forceinline__ uint2 lds_transposed(const lds_char* p) {
+    return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
+}
+
+// N DMAs of 16 bytes a lane from a wave-uniform base (see dma16s): run u from
+// base + 1024 u + off[u] to lds_addr + 1024 u + 16 * lane.
+template <int N>
+__device__ __forceinline__ void dma_runs(const void* base, const uint32_t (&off)[N], uint32_t lds_addr) {
+    static_assert(N == 2 || N == 4, "runs of a wave's 16 keys");
+    if constexpr (N == 4)
+        asm volatile("s_mov_b32 m0, %5\n\ts_nop 0\n\t"
+                     "global_load_lds_dwordx4 %0, %4\n\tglobal_load_lds_dwordx4 %1, %4 offset:1024\n\t"
+                     "global_load_lds_dwordx4 %2, %4 offset:2048\n\tglobal_load_lds_dwordx4 %3, %4 offset:3072"
+                     :: "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(base), "s"(lds_addr) : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\t"
+                     "global_load_lds_dwordx4 %0, %2\n\tglobal_load_lds_dwordx4 %1, %2 offset:1024"
+                     :: "v"(off[0]), "v"(off[1]), "s"(base), "s"(lds_addr) : "memory", "m0");
+}
 
 template <int D>
 struct TileGeom {
@@ -524,7 +548,7 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
     constexpr int CPR = D / 8;        // chunks of a row
     constexpr int RPD = 64 / CPR;     // rows a DMA of one wave fills
     extern __shared__ uint4 smem_tile[];
-    __shared__ uint32_t word;
+    __shared__ uint32_t ctrl[3];
     __shared__ float row_m[kTileRows], row_l[kTileRows];
     const uint32_t lds = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem_tile;
 
@@ -584,13 +608,16 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
     const int page_mask = (1 << a.shift) - 1;
 
     // DMA of a tile: wave w fills keys 16 w .. 16 w + 15, which lie in one
-    // page; lane -> (row lane / CPR, chunk lane % CPR) of each run of RPD rows
-    uint32_t dma_k[16 / RPD], dma_v[16 / RPD];  // byte offsets in the page's head from the first key of the wave
+    // page; lane -> (row lane / CPR, chunk lane % CPR) of each run of RPD rows.
+    // Byte offsets in the run, which begins 1024 u behind the wave's first key
+    // in the page and in LDS alike.
+    constexpr int RUNS = 16 / RPD;
+    uint32_t dma_k[RUNS], dma_v[RUNS];
 #pragma unroll
-    for (int u = 0; u < 16 / RPD; ++u) {
-        const int r = u * RPD + lane / CPR, c = lane % CPR;
-        dma_k[u] = (uint32_t)(r * TG::kRowBytes + ((c ^ TG::kswz(r)) << 4));
-        dma_v[u] = (uint32_t)(r * TG::kRowBytes + ((c ^ TG::vswz(r)) << 4));
+    for (int u = 0; u < RUNS; ++u) {
+        const int r = lane / CPR, c = lane % CPR;
+        dma_k[u] = (uint32_t)(r * TG::kRowBytes + ((c ^ TG::kswz(u * RPD + r)) << 4));
+        dma_v[u] = (uint32_t)(r * TG::kRowBytes + ((c ^ TG::vswz(u * RPD + r)) << 4));
     }
     // The page of keys j .. j + 15 (j a multiple of 16), -1 where there is none
     auto page_at = [&](int j) {
@@ -598,36 +625,35 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
         const int pg = trow[j >> a.shift];
         return (uint32_t)pg < (uint32_t)a.pages ? pg : -1;
     };
-    // A tile: its first key, which of its four runs of 16 keys have a page, and
-    // where this wave's run lies in the caches
+    // Set for good by the first one of its kind that the workgroup meets: a
+    // value that is not finite in a tile that not every row sees whole, and a
+    // page that is not there.
+    uint32_t *poison = &ctrl[0], *absent = &ctrl[1];
+    // A tile: its first key, and where this wave's run lies in the caches.
+    // The page id is read one tile before it is used (id_of, then tile_at).
     struct Tile {
         int key0;
-        uint32_t there;
         int64_t at;
     };
-    auto tile_at = [&](int i) {
+    const int64_t head_at = ((int64_t)h << a.shift) * D;
+    auto first_key = [&](int i) { return bl.at(i < i1 ? i : i1 - 1) * kTileKeys; };
+    auto id_of = [&](int i) { return trow[min(first_key(i) + 16 * wave, last_key) >> a.shift]; };
+    auto tile_at = [&](int i, int id) {
         Tile t;
-        t.key0 = bl.at(i < i1 ? i : i1 - 1) * kTileKeys;
-        t.there = 0;
-        int mine = 0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int pg = page_at(t.key0 + 16 * x);
-            t.there |= (pg >= 0 ? 1u : 0u) << x;
-            if (x == wave) mine = pg < 0 ? 0 : pg;
+        t.key0 = first_key(i);
+        const int j = t.key0 + 16 * wave;
+        if ((uint32_t)id >= (uint32_t)a.pages) {
+            id = 0;
+            *absent = 1u;
         }
-        t.at = (int64_t)mine * a.page_stride + (((int64_t)h << a.shift) + ((t.key0 + 16 * wave) & page_mask)) * D;
+        t.at = (int64_t)id * a.page_stride + head_at + (uint32_t)((j & page_mask) * D);
         return t;
     };
     auto issue_k = [&](const Tile& t, int i) {
-        const uint32_t dst = lds + (uint32_t)((i & 1) * TG::kMatBytes + 16 * wave * TG::kRowBytes);
-#pragma unroll
-        for (int u = 0; u < 16 / RPD; ++u) dma16s(a.k + t.at, dma_k[u], dst + 1024u * u);
+        dma_runs(a.k + t.at, dma_k, lds + (uint32_t)((i & 1) * TG::kMatBytes + 16 * wave * TG::kRowBytes));
     };
     auto issue_v = [&](const Tile& t, int i) {
-        const uint32_t dst = lds + (uint32_t)((2 + (i & 1)) * TG::kMatBytes + 16 * wave * TG::kRowBytes);
-#pragma unroll
-        for (int u = 0; u < 16 / RPD; ++u) dma16s(a.v + t.at, dma_v[u], dst + 1024u * u);
+        dma_runs(a.v + t.at, dma_v, lds + (uint32_t)((2 + (i & 1)) * TG::kMatBytes + 16 * wave * TG::kRowBytes));
     };
     // this lane's operands: byte offsets in a K and in a V tile
     uint32_t kaddr[KS], vaddr[DB];
@@ -641,8 +667,9 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
             vaddr[d] = (uint32_t)(key * TG::kRowBytes + (((4 * d + x) ^ TG::vswz(key)) << 4) + 8 * (lane & 1));
     }
     char* smem = reinterpret_cast<char*>(smem_tile);
-    uint32_t* poison = &word;  // set for good by the first such value the workgroup meets
-    if (tid == 0) *poison = 0u;
+    if (tid == 0) *poison = *absent = 0u;
+    __syncthreads();
+    const int wg_whole = min(wg_p0, last_key) - (kTileKeys - 1);  // tiles up to here are seen whole but for a window
 
     f32x16 s[2];  // scores of the tile to come
     auto scores = [&](int i) {
@@ -660,9 +687,10 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
     };
     Tile cur{}, next{};
     if (i0 < i1) {
-        cur = tile_at(i0);
+        cur = tile_at(i0, id_of(i0));
         issue_k(cur, i0);
-        next = tile_at(i0 + 1);
+        next = tile_at(i0 + 1, id_of(i0 + 1));
+        int id = id_of(i0 + 2);
         issue_v(cur, i0);
         if (i0 + 1 < i1) {
             issue_k(next, i0 + 1);
@@ -673,11 +701,11 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
         __syncthreads();
         scores(i0);
         for (int i = i0; i < i1; ++i) {
-            const Tile tile = cur;
-            const int key0 = tile.key0;
-            const uint32_t there = tile.there;
+            const int key0 = cur.key0;
+            const bool gaps = *absent != 0u;  // of the tiles up to i + 1 at least
             cur = next;
-            next = tile_at(i + 2);
+            next = tile_at(i + 2, id);
+            id = id_of(i + 3);
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's part of V of tile i and of K of tile i + 1
             __syncthreads();                                  // everybody's, and what the next DMAs replace is read
             if (i + 2 < i1) issue_k(next, i + 2);  // no DMA is in flight when the loop ends
@@ -686,10 +714,20 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
             // Tiles that not every row sees whole: a weight of 0 times a value that
             // is not finite would be NaN, so such values leave the tile first; the
             // ones that some row sees are added in the end.
-            const int end = min(wg_p1, last_key);
-            bool masked = there != 15u || key0 + kTileKeys - 1 > min(wg_p0, last_key);
+            bool masked = gaps || key0 > wg_whole;
             if (a.window > 0) masked = masked || (wg_p1 - key0 >= a.window && key0 + kTileKeys > a.sinks);
+            bool hide = false;
+            uint32_t there = 15u;  // bit x: keys key0 + 16 x .. have a page (or lie past the last key)
             if (masked) {
+                if (gaps) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        if (page_at(key0 + 16 * x) < 0) there &= ~(1u << x);
+                }
+                // does this wave have a row that does not see the tile whole?
+                hide = there != 15u || key0 + kTileKeys - 1 > min(p0, last_key);
+                if (a.window > 0) hide = hide || (p1 - key0 >= a.window && key0 + kTileKeys > a.sinks);
+                const int end = min(wg_p1, last_key);
                 char* st = smem + (2 + (i & 1)) * TG::kMatBytes;
                 int u0 = tid;
                 asm volatile("" : "+v"(u0));  // nothing of this path is held in registers through the loop
@@ -708,22 +746,26 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
                 __syncthreads();
             }
             if (!wave_ok) continue;  // no rows: this wave only helps to fill the tiles
-            // tiles that every row of the wave sees whole need no mask
-            bool whole = there == 15u && key0 + kTileKeys - 1 <= min(p0, last_key);
-            if (a.window > 0) whole = whole && (p1 - key0 < a.window || key0 + kTileKeys <= a.sinks);
-            if (!whole) {
-                // key x of the tile (x - 4 half below, a constant) is seen up to
-                // `most`, and with a window above `low` or below `sink`
-                const int base = key0 + 4 * half;
-                const int most = min(my_pos, last_key) - base;
-                const int low = a.window > 0 ? my_pos - a.window - base : INT32_MIN, sink = a.sinks - base;
+            if (hide) {
+                // Key x of the tile (x - 4 half below, a constant) is seen up to
+                // `most`, with a window not from `sink` to `low`, and only where
+                // it has a page.
+                const int64_t base = key0 + 4 * half;
+                auto in_tile = [&](int64_t x) { return (int)(x < -1 ? -1 : x > kTileKeys ? kTileKeys : x); };
+                const int most = in_tile((int64_t)min(my_pos, last_key) - base);
+                const auto each = [&](auto hidden) {
 #pragma unroll
-                for (int kt = 0; kt < 2; ++kt)
+                    for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        const int x = 32 * kt + 8 * (r >> 2) + (r & 3);
-                        if (!((there >> (x >> 4)) & 1u) || x > most || (x <= low && x >= sink)) s[kt][r] = -INFINITY;
-                    }
+                        for (int r = 0; r < 16; ++r) s[kt][r] = hidden(32 * kt + 8 * (r >> 2) + (r & 3)) ? -INFINITY : s[kt][r];
+                };
+                each([&](int x) { return x > most; });
+                if (a.window > 0) {
+                    const int sink = in_tile((int64_t)a.sinks - base), low = in_tile((int64_t)my_pos - a.window - base);
+                    const uint32_t gap = (uint32_t)max(low - sink + 1, 0);
+                    each([&](int x) { return (uint32_t)(x - sink) < gap; });
+                }
+                if (there != 15u) each([&](int x) { return !((there >> (x >> 4)) & 1u); });
             }
             // running maximum of the scaled scores, raised as in the rows kernel
             float mx = s[0][0];
@@ -758,18 +800,18 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
             l += (add[0] + add[1]) + (add[2] + add[3]);
 
             // step x: keys 16 x .. 16 x + 15
+            const lds_char* vt[DB];
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+                vt[d] = (const lds_char*)smem_tile + (2 + (i & 1)) * TG::kMatBytes + vaddr[d];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const uint4 pf = make_uint4(pw[4 * x], pw[4 * x + 1], pw[4 * x + 2], pw[4 * x + 3]);
 #pragma unroll
                 for (int d = 0; d < DB; ++d) {
-                    const uint32_t at = lds + (uint32_t)((2 + (i & 1)) * TG::kMatBytes) + vaddr[d] + (uint32_t)(16 * x * TG::kRowBytes);
-                    const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                                   (lds_s16x4*)(uintptr_t)at));
-                    const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                                   (lds_s16x4*)(uintptr_t)(at + 8 * TG::kRowBytes)));
-                    const uint4 vf = make_uint4(lo.x, lo.y, hi.x, hi.y);
-                    o[d] = E::mfma32(vf, pf, o[d]);
+                    const uint2 lo = lds_transposed(vt[d] + 16 * x * TG::kRowBytes);
+                    const uint2 hi = lds_transposed(vt[d] + (16 * x + 8) * TG::kRowBytes);
+                    o[d] = E::mfma32(make_uint4(lo.x, lo.y, hi.x, hi.y), pf, o[d]);
                 }
             }
             if (masked && *poison) {
@@ -833,7 +875,7 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
 #pragma unroll
             for (int r = 0; r < 16; ++r) store_partial(dst + 32 * d + 8 * (r >> 2) + (r & 3), o[d][r]);
     }
-    if (!split_last_arrival(a.flags, (uint32_t)wg_tile, nsplit, &word)) return;
+    if (!split_last_arrival(a.flags, (uint32_t)wg_tile, nsplit, &ctrl[2])) return;
     join_splits<E, D>(a, rq, h, row0, rows, 2 * kTileRows, wg_tile, nsplit, reinterpret_cast<float*>(smem_tile), row_m, row_l);
 }
 
