@@ -10,12 +10,22 @@
 //
 // A prefix of the ranking is a cut: a logit (as an order-preserving 32-bit
 // key) and how many of the tokens with that logit are in, lowest index first.
-// The cuts are found by radix selection on the keys with histograms of counts
-// and weights, no sort.  A kept set hangs on comparisons of weight sums, so
+// Cuts are found by radix selection on the keys with histograms of counts and
+// weights, no sort.  A kept set hangs on comparisons of weight sums, so
 // weights are computed in fp64 and summed as 64-bit fixed point: such sums do
 // not depend on their order, so atomics and any split of the row give the same
 // bits, and their error (2^-44 of the largest weight each) is far below any
 // token's share.
+//
+// One workgroup a row.  What it costs is the passes over the row and the
+// exponentials, so the selection runs on a short list in LDS wherever one
+// holds every token that can be kept (sample_kernel tells which):
+//  * top-k with k <= 1024: the k-th largest of the 1024 threads' own maxima is
+//    a logit that at least k tokens reach, and not many more do;
+//  * min-p: the tokens of at least min_p;
+//  * top-p alone: the tokens of one of 2048 even steps of the logits, the one
+//    in which the weights pass top_p of their total.
+// A list that overflows leaves the selection to passes over the row.
 
 #include <math.h>
 
@@ -29,16 +39,17 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
 constexpr int kBins = 2048;
+constexpr int kList = 4096;  // tokens of a list
 
 struct LogitF32 {
-    static constexpr int VEC = 4;
+    static constexpr int VEC = 4, FLIGHT = 8;  // FLIGHT: vectors a thread reads at a time
     typedef uint32_t raw;
     static __device__ __forceinline__ float value(const uint32_t (&w)[4], int i) { return __uint_as_float(w[i]); }
     static __device__ __forceinline__ float one(const void* row, int64_t i) { return static_cast<const float*>(row)[i]; }
 };
 template <class E>
 struct Logit16 {
-    static constexpr int VEC = 8;
+    static constexpr int VEC = 8, FLIGHT = 4;
     typedef uint16_t raw;
     static __device__ __forceinline__ float value(const uint32_t (&w)[4], int i) {
         return E::to_f32((uint16_t)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]));
@@ -78,6 +89,54 @@ __device__ __forceinline__ void load_keys(const void* row, int i, int V, uint32_
     }
 }
 
+// The logits x of a row for which pre(x) holds, as f(x, index), U vectors a
+// thread in flight.  Vectors past the end are read from the last whole one and
+// their values dropped.
+template <class L, int U, class P, class F>
+__device__ __forceinline__ void each_logit(const void* row, int V, P pre, F f) {
+    constexpr int VEC = L::VEC, STEP = kThreads * VEC;
+    const typename L::raw* x = static_cast<const typename L::raw*>(row);
+    if (V < VEC) {
+        if ((int)threadIdx.x < V && pre(L::one(row, threadIdx.x))) f(L::one(row, threadIdx.x), (int)threadIdx.x);
+        return;
+    }
+    struct __attribute__((packed, aligned(sizeof(typename L::raw)))) Vec {
+        uint32_t w[4];
+    };
+    for (int base = (int)threadIdx.x * VEC; base < V; base += U * STEP) {
+        Vec v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const Vec*>(x + min(base + u * STEP, V - VEC));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = base + u * STEP, at = min(i, V - VEC);
+            const uint32_t w[4] = {v[u].w[0], v[u].w[1], v[u].w[2], v[u].w[3]};
+            if (i + VEC <= V) {
+                bool any = false;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) any |= pre(L::value(w, e));
+                if (any)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        if (pre(L::value(w, e))) f(L::value(w, e), i + e);
+            } else if (i < V) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    if (at + e >= i && pre(L::value(w, e))) f(L::value(w, e), at + e);
+            }
+        }
+    }
+}
+
+// The largest logit of this thread's share of a row (-inf without one).
+template <class L>
+__device__ __forceinline__ float largest(const void* row, int V) {
+    float m = -INFINITY;
+    // every value updates the maximum in `pre`: two instructions each
+    each_logit<L, L::FLIGHT>(row, V, [&](float x) { m = x > m ? x : m; return false; }, [](float, int) {});
+    return m;
+}
+
 struct Row {
     double max, inv_t;  // largest logit, 1 / T
     uint32_t kmax;
@@ -88,6 +147,15 @@ struct Row {
         return exp(((double)logit_of(key) - max) * inv_t);
     }
     __device__ __forceinline__ uint64_t fixed(double w) const { return (uint64_t)(w * fix + 0.5); }
+    // Even steps of the logits below the largest, as bins that rise with the
+    // logit: 2048 over the 32 T in which a weight can add to a sum, or over 64
+    // where that is less.  Rounding keeps the order, so equal logits share a
+    // bin and larger ones never have a lower one.
+    __device__ __forceinline__ float step(float T) const { return (float)kBins / fminf(32.0f * T, 64.0f); }
+    __device__ __forceinline__ int bin(uint32_t key, float step) const {
+        if (key == kmax) return kBins - 1;  // also +inf
+        return kBins - 1 - (int)fminf((logit_of(kmax) - logit_of(key)) * step, (float)(kBins - 1));
+    }
 };
 
 __device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
@@ -104,11 +172,18 @@ struct Shared {
     // results of a search
     uint32_t bin, found, before_c;
     unsigned long long before_w, total_w;
-    unsigned long long best;
-    uint32_t first;
+    uint32_t best, first;
     int seg;
     uint32_t seg_ties;
     unsigned long long seg_before;
+    uint64_t votes[2][kWaves];
+    uint32_t n;  // tokens of the list, also past its end
+};
+
+// The list: keys (0: dropped) and indexes, behind which the segments of a
+// drawing over the row lie where there is no list.
+struct List {
+    uint32_t key[kList], idx[kList];
 };
 
 // Exclusive prefix sums over the workgroup's threads of (c, w), in thread order; the totals go to *tc, *tw.
@@ -230,43 +305,215 @@ __device__ __forceinline__ bool search(Shared& sh, Cut& cut, int digit, bool by_
     return true;
 }
 
+// The same over the first n tokens of the list.
+__device__ __forceinline__ void histogram_list(Shared& sh, const List& list, int n, const Row& r, const Cut& cut, int digit,
+                                               uint32_t floor_key) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += kThreads) {
+        sh.count[i] = 0;
+        sh.weight[i] = 0;
+    }
+    __syncthreads();
+    const int shift = 32 - cut.bits - digit;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint32_t key = list.key[i];
+        if (key == 0 || key < floor_key || (cut.bits && (key >> (32 - cut.bits)) != cut.prefix)) continue;
+        const uint32_t b = (key >> shift) & ((1u << digit) - 1);
+        atomicAdd(&sh.count[b], 1u);
+        atomicAdd(&sh.weight[b], (unsigned long long)r.fixed(r.weight(key)));
+    }
+    __syncthreads();
+}
+
+// How many of the tokens with the cut's logit are in, by weight.
+__device__ __forceinline__ uint32_t ties_in(const Row& r, const Cut& cut, double limit) {
+    const uint64_t one = r.fixed(r.weight(cut.prefix));
+    const double n = one ? ceil((limit - (double)cut.w) / (double)one) : 1.0;
+    return n < 1.0 ? 1u : n > 2147483647.0 ? 0x7FFFFFFFu : (uint32_t)n;
+}
+
+__device__ __forceinline__ void append(Shared& sh, List& list, uint32_t key, int i) {
+    const uint32_t at = atomicAdd(&sh.n, 1u);
+    if (at < (uint32_t)kList) {
+        list.key[at] = key;
+        list.idx[at] = (uint32_t)i;
+    }
+}
+
+// The upper 16 bits of the k-th largest of the threads' values, 1 <= k <= 1024:
+// at least k of them reach it.  Two bits a round: how many reach each of the
+// three values that they can make larger.
+__device__ __forceinline__ uint32_t kth_of_threads(Shared& sh, uint32_t mine, uint32_t k) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    uint32_t prefix = 0;
+#pragma unroll 1
+    for (int bit = 30; bit >= 16; bit -= 2) {
+        uint64_t votes = 0;
+#pragma unroll
+        for (uint32_t d = 1; d < 4; ++d)
+            votes |= (uint64_t)__popcll(__ballot(mine >= (prefix | (d << bit)))) << (16 * d);
+        uint64_t* slot = sh.votes[(bit >> 1) & 1];
+        if (lane == 0) slot[wave] = votes;
+        __syncthreads();
+        votes = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) votes += slot[w];
+        uint32_t best = 0;
+#pragma unroll
+        for (uint32_t d = 1; d < 4; ++d)
+            if ((uint32_t)(votes >> (16 * d) & 0xFFFFu) >= k) best = d;
+        prefix |= best << bit;
+    }
+    return prefix;
+}
+
+// A logit that every token of weight min_p or more reaches, by a margin that
+// covers the roundings of fp64 and of the logarithm many times over.
+__device__ __forceinline__ uint32_t floor_of(const Row& r, double T, double min_p) {
+    const double d = T * log(min_p), x = r.max + d;
+    const double low = x - 1e-9 * (fabs(r.max) + fabs(d) + T);
+    if (!(low > -3.0e38)) return 0x00800000u;  // every finite logit
+    float f = (float)low;
+    f -= fabsf(f) * 1e-6f + 1e-37f;
+    return f > -3.0e38f ? key_of(f) : 0x00800000u;
+}
+
+// Cuts and the drawing where the list holds every token that can be kept.
+__device__ __forceinline__ void draw_from_list(Shared& sh, List& list, int n, const Row& r, double min_w, int k, bool by_k,
+                                               float p, float u, int V, int32_t* token, float* logprob) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int digits[3] = {11, 11, 10};
+    // tokens without weight, or below min_p, are out; what is left and its weight
+    uint32_t c = 0, bc, left;
+    uint64_t w = 0, bw, total;
+    for (int i = tid; i < n; i += kThreads) {
+        const double x = r.weight(list.key[i]);
+        if (!(x > 0.0) || x < min_w) list.key[i] = 0;
+        else ++c, w += r.fixed(x);
+    }
+    block_scan(sh, c, w, &bc, &bw, &left, &total);
+    // the cut, as in sample_kernel; `ties`: how many tokens have its logit
+    uint32_t ckey = 0, cties = 0, ties = 0;
+    if (by_k && (uint32_t)k < left) {
+        Cut cut{0, 0, 0, 0};
+        for (int d = 0; d < 3; ++d) {
+            histogram_list(sh, list, n, r, cut, digits[d], 0);
+            search(sh, cut, digits[d], true, (uint32_t)k, 0.0, nullptr);
+        }
+        ckey = cut.prefix;
+        cties = (uint32_t)k - cut.c;
+        ties = sh.count[sh.bin];
+        total = cut.w + cties * r.fixed(r.weight(ckey));
+    }
+    if (p < 1.0f) {
+        const double limit = (double)p * (double)total;
+        Cut cut{0, 0, 0, 0};
+        bool in = true;
+        for (int d = 0; d < 3 && in; ++d) {
+            histogram_list(sh, list, n, r, cut, digits[d], ckey);
+            in = search(sh, cut, digits[d], false, 0, limit, nullptr);
+        }
+        if (in) {
+            uint32_t t = ties_in(r, cut, limit);
+            if (cut.prefix == ckey && t > cties) t = cties;
+            ckey = cut.prefix;
+            cties = t;
+            ties = sh.count[sh.bin];
+        }
+    }
+    // what the cut leaves, by steps of the row's index: kBins at most
+    __syncthreads();
+    for (int i = tid; i < kBins; i += kThreads) sh.weight[i] = 0;
+    __syncthreads();
+    int shift = 0;
+    while ((V - 1) >> shift >= kBins) ++shift;
+    uint32_t first = 0xFFFFFFFFu;
+    uint32_t gone = 0;  // bit e: this thread's e-th token is a tie past the cut
+    for (int i = tid, e = 0; i < n; i += kThreads, ++e) {
+        const uint32_t key = list.key[i], at = list.idx[i];
+        if (key == 0) continue;
+        bool out = key < ckey;
+        if (key == ckey && ties > cties) {  // the lowest indexes of a tie are in
+            uint32_t before = 0;
+            for (int j = 0; j < n; ++j) before += list.key[j] == ckey && list.idx[j] < at;
+            out = before >= cties;
+        }
+        if (out) {
+            gone |= 1u << e;
+            continue;
+        }
+        first = min(first, at);
+        atomicAdd(&sh.weight[at >> shift], (unsigned long long)r.fixed(r.weight(key)));
+    }
+    for (int d = 32; d > 0; d >>= 1) first = min(first, (uint32_t)__shfl_xor((int)first, d, 64));
+    if (lane == 0 && first != 0xFFFFFFFFu) atomicMin(&sh.first, first);
+    __syncthreads();
+    for (int i = tid, e = 0; i < n; i += kThreads, ++e)
+        if (gone >> e & 1) list.key[i] = 0;
+    constexpr int PER = kBins / kThreads;
+    uint64_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) mine += sh.weight[tid * PER + i];
+    block_scan(sh, 0, mine, &bc, &bw, &left, &total);
+    const double target = (double)u * (double)total;
+    uint64_t before = bw;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const uint64_t next = before + sh.weight[tid * PER + i];
+        if (!((double)before > target) && (double)next > target) {
+            sh.seg = tid * PER + i;
+            sh.seg_before = before;
+        }
+        before = next;
+    }
+    __syncthreads();
+    // the token inside its step; u = 0 takes the first one that is kept
+    const uint32_t seg = (uint32_t)sh.seg;
+    for (int i = tid; i < n; i += kThreads) {
+        const uint32_t key = list.key[i], at = list.idx[i];
+        if (key == 0) continue;
+        const double x = r.weight(key);
+        bool here = at == sh.first;
+        if (u > 0.0f) {
+            if (at >> shift != seg) continue;
+            uint64_t b = sh.seg_before;
+            for (int j = 0; j < n; ++j)
+                if (list.key[j] != 0 && list.idx[j] >> shift == seg && list.idx[j] < at) b += r.fixed(r.weight(list.key[j]));
+            here = !((double)b > target) && (double)(b + r.fixed(x)) > target;
+        }
+        if (here) {
+            *token = (int32_t)at;
+            if (logprob) *logprob = (float)log(x / ((double)total / r.fix));
+        }
+    }
+}
+
 template <class L>
 __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
     __shared__ Shared sh;
-    extern __shared__ unsigned long long seg_mem[];  // per segment: weight, then ties
+    extern __shared__ unsigned long long seg_mem[];  // the list, or per segment of the row: weight, then ties
+    List& list = *reinterpret_cast<List*>(seg_mem);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int V = a.V;
     const int64_t b = blockIdx.x;
     const void* row = static_cast<const typename L::raw*>(a.logits) + b * a.row_stride;
     constexpr int VEC = L::VEC, SEG = 64 * VEC;
 
-    // largest logit, lowest index
+    // largest logit
     if (tid == 0) {
         sh.best = 0;
         sh.first = 0xFFFFFFFFu;
+        sh.n = 0;
     }
     __syncthreads();
-    unsigned long long best = 0;
-    for (int i = tid * VEC; i < V; i += kThreads * VEC) {
-        uint32_t key[VEC];
-        load_keys<L>(row, i, V, key);
+    const uint32_t my_key = key_of(largest<L>(row, V));
+    uint32_t best = my_key;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const unsigned long long x = ((unsigned long long)key[e] << 32) | (uint32_t)~(i + e);
-            best = key[e] && x > best ? x : best;
-        }
-    }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-        const unsigned long long o = __shfl_xor(best, d, 64);
-        best = o > best ? o : best;
-    }
+    for (int d = 32; d > 0; d >>= 1) best = max(best, (uint32_t)__shfl_xor((int)best, d, 64));
     if (lane == 0) atomicMax(&sh.best, best);
     __syncthreads();
-    best = sh.best;
     Row r;
-    r.kmax = (uint32_t)(best >> 32);
-    const int top = (int)~(uint32_t)best;
+    r.kmax = sh.best;
     if (r.kmax <= 0x007FFFFFu) {  // every logit is -inf or NaN
         if (tid == 0) {
             a.tokens[b] = -1;
@@ -282,8 +529,14 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
     float u = a.u[b];
     u = u > 0.0f ? fminf(u, 0.99999994f) : 0.0f;
     if (!(T > 0.0f) || k == 1 || !(p > 0.0f) || !(min_p <= 1.0f)) {  // the best token alone is kept
+        const float x0 = logit_of(r.kmax);
+        uint32_t at = 0xFFFFFFFFu;
+        if (my_key == r.kmax)
+            each_logit<L, L::FLIGHT>(row, V, [&](float x) { return x == x0; }, [&](float, int i) { at = min(at, (uint32_t)i); });
+        if (at != 0xFFFFFFFFu) atomicMin(&sh.first, at);
+        __syncthreads();
         if (tid == 0) {
-            a.tokens[b] = top;
+            a.tokens[b] = (int32_t)sh.first;
             if (a.logprobs) a.logprobs[b] = 0.0f;
         }
         return;
@@ -296,10 +549,87 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
     const double min_w = min_p > 0.0f ? (double)min_p : 0.0;
     uint32_t ckey = 0, cties = 0;
     const bool by_k = k < V, by_p = p < 1.0f;
-    if (by_k || by_p) {
+    const int digits[3] = {11, 11, 10};
+
+    // A list of every token that can be kept, where a bound of their logits is
+    // known: the whole of a short row, the best k, the ones of min_p
+    uint32_t bound = 0;
+    if (V <= kList) {
+        bound = 0x00800000u;
+    } else {
+        if (min_w > 0.0) bound = floor_of(r, (double)T, min_w);
+        if (by_k && k <= kThreads) bound = max(bound, max(kth_of_threads(sh, my_key, (uint32_t)k), 0x00800000u));
+    }
+    bool listed = false;
+    if (bound) {
+        const float x0 = logit_of(bound);
+        each_logit<L, L::FLIGHT>(row, V, [&](float x) { return x >= x0; }, [&](float x, int i) { append(sh, list, key_of(x), i); });
+        __syncthreads();
+        listed = sh.n <= (uint32_t)kList;
+    }
+    if (listed) {
+        draw_from_list(sh, list, (int)sh.n, r, min_w, k, by_k, p, u, V, a.tokens + b, a.logprobs ? a.logprobs + b : nullptr);
+        return;
+    }
+
+    bool cut_found = false;
+    if (by_p && !by_k) {
+        // the step of the logits in which the cut lies, then its tokens as a list
+        const float step = r.step(T);
+        __syncthreads();
+        for (int i = tid; i < kBins; i += kThreads) {
+            sh.count[i] = 0;
+            sh.weight[i] = 0;
+        }
+        if (tid == 0) sh.n = 0;
+        __syncthreads();
+        each_logit<L, 2>(row, V, [](float) { return true; }, [&](float x, int) {
+            const uint32_t key = key_of(x);
+            const double w = r.weight(key);
+            const uint64_t f = r.fixed(w);
+            if (f == 0 || w < min_w) return;  // adds nothing to any sum
+            const int bin = r.bin(key, step);
+            atomicAdd(&sh.count[bin], 1u);
+            atomicAdd(&sh.weight[bin], (unsigned long long)f);
+        });
+        __syncthreads();
+        Cut none{0, 0, 0, 0}, cut{0, 0, 0, 0};
+        uint64_t total = 0;
+        search(sh, none, 0, true, 0xFFFFFFFFu, 0.0, &total);
+        const double limit = (double)p * (double)total;
+        __syncthreads();
+        if (search(sh, cut, 0, false, 0, limit, nullptr)) {
+            const int bin = (int)sh.bin;
+            const Cut above{0, 0, sh.before_c, sh.before_w};
+            auto in_step = [&](float x) {
+                const uint32_t key = key_of(x);
+                return key > 0x007FFFFFu && r.bin(key, step) == bin;
+            };
+            each_logit<L, L::FLIGHT>(row, V, in_step, [&](float x, int i) {
+                const double w = r.weight(key_of(x));
+                if (w >= min_w && r.fixed(w) != 0) append(sh, list, key_of(x), i);
+            });
+            __syncthreads();
+            if (sh.n <= (uint32_t)kList) {
+                const int n = (int)sh.n;
+                cut = above;
+                bool in = true;
+                for (int d = 0; d < 3 && in; ++d) {
+                    histogram_list(sh, list, n, r, cut, digits[d], 0);
+                    in = search(sh, cut, digits[d], false, 0, limit, nullptr);
+                }
+                cut_found = in;
+                if (in) {
+                    ckey = cut.prefix;
+                    cties = ties_in(r, cut, limit);
+                }
+            }
+        }
+        __syncthreads();  // the list's memory is the segments' from here on
+    }
+    if (!cut_found && (by_k || by_p)) {
         Cut root{0, 0, 0, 0};
         uint64_t total = 0;
-        const int digits[3] = {11, 11, 10};
         if (by_k) {
             Cut cut = root;
             bool in = true;
@@ -333,9 +663,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
                 in = search(sh, cut, digits[d], false, 0, limit, nullptr);
             }
             if (in) {
-                const uint64_t one = r.fixed(r.weight(cut.prefix));
-                const double n = one ? ceil((limit - (double)cut.w) / (double)one) : 1.0;
-                uint32_t ties = n < 1.0 ? 1u : n > 2147483647.0 ? 0x7FFFFFFFu : (uint32_t)n;
+                uint32_t ties = ties_in(r, cut, limit);
                 if (cut.prefix == ckey && ties > cties) ties = cties;
                 ckey = cut.prefix;
                 cties = ties;
@@ -463,9 +791,11 @@ hipError_t launch_sample(const SampleArgs& args, hipStream_t s) {
     while (((int64_t)1 << bits) < a.V) ++bits;
     a.fix = ldexp(1.0, 62 - bits);
     const int seg = a.dtype == 2 ? 64 * LogitF32::VEC : 64 * 8;
-    const size_t lds = (size_t)((a.V + seg - 1) / seg) * 12 + 8;
+    size_t lds = (size_t)((a.V + seg - 1) / seg) * 12 + 8;
+    if (lds < sizeof(List)) lds = sizeof(List);
     static DeviceFlags r32, rh, rb;
-    const int most = (int)(kSampleMaxVocab / 256) * 12 + 8;
+    const int most = (int)(kSampleMaxVocab / 256) * 12 + 8;  // more than a list
+    static_assert((kSampleMaxVocab / 256) * 12 + 8 >= sizeof(List), "the raised limit covers the list");
     hipError_t e = hipSuccess;
     const dim3 grid((unsigned)a.B), block(kThreads);
     if (a.dtype == 2) {
