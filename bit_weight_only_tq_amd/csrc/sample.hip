@@ -137,6 +137,28 @@ __device__ __forceinline__ float largest(const void* row, int V) {
     return m;
 }
 
+// e^y for y <= 0: 2^n times the series of e^f, f = y - n ln 2, |f| <= ln 2 / 2.
+// The first term left out is f^13 / 13!, at most 2^-52.4 of the sum.
+__device__ __forceinline__ double exp_negative(double y) {
+    const double n = rint(y * 1.4426950408889634);
+    // ln 2 in two parts, the first with 32 bits: n times it is exact
+    const double f = fma(n, -1.9082149292705877e-10, fma(n, -0.69314718036912382, y));
+    double s = 1.0 / 479001600.0;
+    s = fma(s, f, 1.0 / 39916800.0);
+    s = fma(s, f, 1.0 / 3628800.0);
+    s = fma(s, f, 1.0 / 362880.0);
+    s = fma(s, f, 1.0 / 40320.0);
+    s = fma(s, f, 1.0 / 5040.0);
+    s = fma(s, f, 1.0 / 720.0);
+    s = fma(s, f, 1.0 / 120.0);
+    s = fma(s, f, 1.0 / 24.0);
+    s = fma(s, f, 1.0 / 6.0);
+    s = fma(s, f, 0.5);
+    s = fma(s, f, 1.0);
+    s = fma(s, f, 1.0);
+    return y < -746.0 ? 0.0 : ldexp(s, (int)fmax(n, -1100.0));
+}
+
 struct Row {
     double max, inv_t;  // largest logit, 1 / T
     uint32_t kmax;
@@ -144,7 +166,7 @@ struct Row {
     __device__ __forceinline__ double weight(uint32_t key) const {
         if (key == kmax) return 1.0;             // also +inf
         if (key <= 0x007FFFFFu) return 0.0;      // -inf or no token
-        return exp(((double)logit_of(key) - max) * inv_t);
+        return exp_negative(((double)logit_of(key) - max) * inv_t);
     }
     __device__ __forceinline__ uint64_t fixed(double w) const { return (uint64_t)(w * fix + 0.5); }
     // Even steps of the logits below the largest, as bins that rise with the
@@ -158,10 +180,29 @@ struct Row {
     }
 };
 
-__device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor((unsigned long long)v, d, 64);
+// Inclusive prefix sums over the 64 lanes, by lane shifts within rows of 16 and
+// two broadcasts between rows: no LDS.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t from_lane(uint32_t v) {  // 0 where there is none
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t from_lane(uint64_t v) {
+    return (uint64_t)from_lane<CTRL, ROWS>((uint32_t)v) | (uint64_t)from_lane<CTRL, ROWS>((uint32_t)(v >> 32)) << 32;
+}
+template <class N>
+__device__ __forceinline__ N wave_scan(N v) {
+    v += from_lane<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+    v += from_lane<0x112, 0xF>(v);
+    v += from_lane<0x114, 0xF>(v);
+    v += from_lane<0x118, 0xF>(v);
+    v += from_lane<0x142, 0xA>(v);  // last lane of rows 0 and 2 to rows 1 and 3
+    v += from_lane<0x143, 0xC>(v);  // lane 31 to rows 2 and 3
     return v;
+}
+__device__ __forceinline__ uint32_t lane_of(uint32_t v, int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)v, lane); }
+__device__ __forceinline__ uint64_t lane_of(uint64_t v, int lane) {
+    return (uint64_t)lane_of((uint32_t)v, lane) | (uint64_t)lane_of((uint32_t)(v >> 32), lane) << 32;
 }
 
 struct Shared {
@@ -176,7 +217,7 @@ struct Shared {
     int seg;
     uint32_t seg_ties;
     unsigned long long seg_before;
-    uint64_t votes[2][kWaves];
+    unsigned long long votes[8];
     uint32_t n;  // tokens of the list, also past its end
 };
 
@@ -190,37 +231,23 @@ struct List {
 __device__ __forceinline__ void block_scan(Shared& sh, uint32_t c, uint64_t w, uint32_t* bc, uint64_t* bw, uint32_t* tc,
                                            uint64_t* tw) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t ic = c;
-    unsigned long long iw = w;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint32_t oc = __shfl_up(ic, d, 64);
-        const unsigned long long ow = __shfl_up(iw, d, 64);
-        if (lane >= d) {
-            ic += oc;
-            iw += ow;
-        }
-    }
+    const uint32_t ic = wave_scan(c);
+    const uint64_t iw = wave_scan(w);
     __syncthreads();
     if (lane == 63) {
         sh.scan_c[wave] = ic;
         sh.scan_w[wave] = iw;
     }
     __syncthreads();
-    uint32_t pc = 0, sc = 0;
-    uint64_t pw = 0, sw = 0;
-    for (int i = 0; i < kWaves; ++i) {
-        if (i == wave) {
-            pc = sc;
-            pw = sw;
-        }
-        sc += sh.scan_c[i];
-        sw += sh.scan_w[i];
-    }
-    *bc = pc + ic - c;
-    *bw = pw + iw - w;
-    *tc = sc;
-    *tw = sw;
+    // every wave scans the sums of the waves in its first lanes
+    static_assert(kWaves == 16, "one row of lanes");
+    const uint32_t sc = wave_scan(lane < kWaves ? sh.scan_c[lane] : 0u);
+    const uint64_t sw = wave_scan(lane < kWaves ? (uint64_t)sh.scan_w[lane] : (uint64_t)0);
+    const int before = __builtin_amdgcn_readfirstlane(wave) - 1;
+    *bc = (before < 0 ? 0u : lane_of(sc, before)) + ic - c;
+    *bw = (before < 0 ? 0ull : lane_of(sw, before)) + iw - w;
+    *tc = lane_of(sc, kWaves - 1);
+    *tw = lane_of(sw, kWaves - 1);
 }
 
 // A cut of the ranking being refined, digit by digit: the keys whose top bits
@@ -267,13 +294,13 @@ __device__ __forceinline__ bool search(Shared& sh, Cut& cut, int digit, bool by_
                                        uint64_t* total) {
     if (threadIdx.x == 0) sh.found = 0;
     constexpr int PER = kBins / kThreads;
-    uint32_t c = 0;
-    uint64_t w = 0;
+    uint32_t c = 0, cs[PER];
+    uint64_t w = 0, ws[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int b = kBins - 1 - (threadIdx.x * PER + i);
-        c += sh.count[b];
-        w += sh.weight[b];
+        c += cs[i] = sh.count[b];
+        w += ws[i] = sh.weight[b];
     }
     uint32_t bc, tc;
     uint64_t bw, tw;
@@ -282,13 +309,12 @@ __device__ __forceinline__ bool search(Shared& sh, Cut& cut, int digit, bool by_
     bw += cut.w;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int b = kBins - 1 - (threadIdx.x * PER + i);
-        const uint32_t nc = bc + sh.count[b];
-        const uint64_t nw = bw + sh.weight[b];
-        const bool here = sh.count[b] && (by_count ? (bc < k && k <= nc) : ((double)bw < limit && !((double)nw < limit)));
+        const uint32_t nc = bc + cs[i];
+        const uint64_t nw = bw + ws[i];
+        const bool here = cs[i] && (by_count ? (bc < k && k <= nc) : ((double)bw < limit && !((double)nw < limit)));
         if (here) {
             sh.found = 1;
-            sh.bin = b;
+            sh.bin = kBins - 1 - (threadIdx.x * PER + i);
             sh.before_c = bc;
             sh.before_w = bw;
         }
@@ -344,7 +370,6 @@ __device__ __forceinline__ void append(Shared& sh, List& list, uint32_t key, int
 // at least k of them reach it.  Two bits a round: how many reach each of the
 // three values that they can make larger.
 __device__ __forceinline__ uint32_t kth_of_threads(Shared& sh, uint32_t mine, uint32_t k) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     uint32_t prefix = 0;
 #pragma unroll 1
     for (int bit = 30; bit >= 16; bit -= 2) {
@@ -352,12 +377,10 @@ __device__ __forceinline__ uint32_t kth_of_threads(Shared& sh, uint32_t mine, ui
 #pragma unroll
         for (uint32_t d = 1; d < 4; ++d)
             votes |= (uint64_t)__popcll(__ballot(mine >= (prefix | (d << bit)))) << (16 * d);
-        uint64_t* slot = sh.votes[(bit >> 1) & 1];
-        if (lane == 0) slot[wave] = votes;
+        unsigned long long* sum = sh.votes + (30 - bit) / 2;  // one a round, zero before
+        if ((threadIdx.x & 63) == 0) atomicAdd(sum, (unsigned long long)votes);
         __syncthreads();
-        votes = 0;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) votes += slot[w];
+        votes = *sum;
         uint32_t best = 0;
 #pragma unroll
         for (uint32_t d = 1; d < 4; ++d)
@@ -376,6 +399,112 @@ __device__ __forceinline__ uint32_t floor_of(const Row& r, double T, double min_
     float f = (float)low;
     f -= fabsf(f) * 1e-6f + 1e-37f;
     return f > -3.0e38f ? key_of(f) : 0x00800000u;
+}
+
+// Sorts 64 R values, element 64 r + lane in v[r] of the lane, the largest first,
+// in one wave: a bitonic network, its steps of 64 and more between registers.
+template <class N>
+__device__ __forceinline__ N from_xor(N v, int d) {
+    if constexpr (sizeof(N) == 8) return (N)__shfl_xor((unsigned long long)v, d, 64);
+    else return (N)__shfl_xor((int)v, d, 64);
+}
+template <int R, int SIZE, class N>
+__device__ __forceinline__ void sort_runs(N (&v)[R]) {
+    const int lane = threadIdx.x & 63;
+    if constexpr (SIZE > 2) sort_runs<R, SIZE / 2>(v);
+#pragma unroll
+    for (int s = SIZE / 128; s > 0; s >>= 1)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (!(r & s)) {
+                const bool down = !((64 * r) & SIZE);
+                const N x = v[r], y = v[r | s];
+                const N hi = x > y ? x : y, lo = x > y ? y : x;
+                v[r] = down ? hi : lo;
+                v[r | s] = down ? lo : hi;
+            }
+#pragma unroll 1
+    for (int s = SIZE > 64 ? 32 : SIZE / 2; s > 0; s >>= 1) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool down = !((64 * r + lane) & SIZE);
+            const N x = v[r], y = from_xor(x, s);
+            const bool larger = down == !(lane & s);  // keeps the larger of the two
+            v[r] = (x > y) == larger ? x : y;
+        }
+    }
+}
+template <int R, class N>
+__device__ __forceinline__ void sort_wave(N (&v)[R]) {
+    sort_runs<R, 64 * R>(v);
+}
+
+// Cuts and the drawing in one wave, where the list holds every token that can
+// be kept and they are 64 R at most: the tokens are sorted by rank, their
+// weights summed in that order and cut, and what is left sorted by index.
+// A workgroup's barriers and LDS traffic cost more than so few tokens do.
+template <int R>
+__device__ __forceinline__ void draw_in_wave(Shared& sh, const List& list, int n, const Row& r, double min_w, int k, float p,
+                                             float u, int32_t* token, float* logprob) {
+    const int lane = threadIdx.x & 63;
+    uint64_t v[R];
+#pragma unroll
+    for (int e = 0; e < R; ++e) {
+        const int i = 64 * e + lane;
+        v[e] = i < n ? (uint64_t)list.key[i] << 32 | (uint32_t)~list.idx[i] : 0ull;
+    }
+    sort_wave(v);
+    // weights by rank, of the first k that are of min_p
+    uint64_t w[R], before[R], total = 0;
+    bool in[R];
+#pragma unroll
+    for (int e = 0; e < R; ++e) {
+        const double x = r.weight((uint32_t)(v[e] >> 32));
+        in[e] = v[e] != 0 && 64 * e + lane < k && x > 0.0 && !(x < min_w);
+        w[e] = in[e] ? r.fixed(x) : 0ull;
+        const uint64_t sum = wave_scan(w[e]);
+        before[e] = total + sum - w[e];
+        total += lane_of(sum, 63);
+    }
+    if (p < 1.0f) {
+        const double limit = (double)p * (double)total;
+        total = 0;
+#pragma unroll
+        for (int e = 0; e < R; ++e) {
+            in[e] = in[e] && (double)before[e] < limit;
+            if (!in[e]) w[e] = 0;
+            total += lane_of(wave_scan(w[e]), 63);
+        }
+    }
+    // by index: the largest first of (2^20 - index, rank); 0 for what is out
+    static_assert(kSampleMaxVocab <= 1 << 20 && 64 * R <= 1 << 10, "index and rank share 32 bits");
+    uint32_t at[R];
+#pragma unroll
+    for (int e = 0; e < R; ++e) {
+        const int rank = 64 * e + lane;
+        sh.count[rank] = (uint32_t)(v[e] >> 32);
+        sh.weight[rank] = w[e];
+        at[e] = in[e] ? ((1u << 20) - (uint32_t)~v[e]) << 10 | (uint32_t)rank : 0u;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    sort_wave(at);
+    const double target = (double)u * (double)total;
+    uint64_t past = 0;
+#pragma unroll
+    for (int e = 0; e < R; ++e) {
+        const uint32_t rank = at[e] & 1023u;
+        const uint64_t one = at[e] ? sh.weight[rank] : 0ull;
+        const uint64_t sum = wave_scan(one), b = past + sum - one;
+        past += lane_of(sum, 63);
+        // u = 0 takes the first token that is kept
+        const bool here = u > 0.0f ? (!((double)b > target) && (double)(b + one) > target) : (e == 0 && lane == 0);
+        if (here && at[e]) {
+            *token = (int32_t)((1u << 20) - (at[e] >> 10));
+            if (logprob) *logprob = (float)log(r.weight(sh.count[rank]) / ((double)total / r.fix));
+        }
+    }
 }
 
 // Cuts and the drawing where the list holds every token that can be kept.
@@ -505,6 +634,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         sh.first = 0xFFFFFFFFu;
         sh.n = 0;
     }
+    if (tid < 8) sh.votes[tid] = 0;
     __syncthreads();
     const uint32_t my_key = key_of(largest<L>(row, V));
     uint32_t best = my_key;
@@ -567,6 +697,15 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         __syncthreads();
         listed = sh.n <= (uint32_t)kList;
     }
+    if (listed && sh.n <= 1024u) {
+        if (wave != 0) return;
+        const int n = (int)sh.n;
+        float* logprob = a.logprobs ? a.logprobs + b : nullptr;
+        if (n <= 64) draw_in_wave<1>(sh, list, n, r, min_w, k, p, u, a.tokens + b, logprob);
+        else if (n <= 256) draw_in_wave<4>(sh, list, n, r, min_w, k, p, u, a.tokens + b, logprob);
+        else draw_in_wave<16>(sh, list, n, r, min_w, k, p, u, a.tokens + b, logprob);
+        return;
+    }
     if (listed) {
         draw_from_list(sh, list, (int)sh.n, r, min_w, k, by_k, p, u, V, a.tokens + b, a.logprobs ? a.logprobs + b : nullptr);
         return;
@@ -583,31 +722,46 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         }
         if (tid == 0) sh.n = 0;
         __syncthreads();
+        // Tokens of less than (1 - p) / V of the total (at least 1, the best
+        // token's weight) add up to less than 1 - p of it: they lie past the
+        // cut, and only count in the total.
+        const uint64_t small = r.fixed((1.0 - (double)p) / (double)V * 0.999);
+        uint64_t rest = 0;
         each_logit<L, 2>(row, V, [](float) { return true; }, [&](float x, int) {
             const uint32_t key = key_of(x);
             const double w = r.weight(key);
             const uint64_t f = r.fixed(w);
-            if (f == 0 || w < min_w) return;  // adds nothing to any sum
+            if (w < min_w) return;
+            if (f < small || f == 0) {
+                rest += f;
+                return;
+            }
             const int bin = r.bin(key, step);
             atomicAdd(&sh.count[bin], 1u);
             atomicAdd(&sh.weight[bin], (unsigned long long)f);
         });
+        uint32_t none_c, all_c;
+        uint64_t none_w, all_rest;
+        block_scan(sh, 0u, rest, &none_c, &none_w, &all_c, &all_rest);
         __syncthreads();
         Cut none{0, 0, 0, 0}, cut{0, 0, 0, 0};
         uint64_t total = 0;
         search(sh, none, 0, true, 0xFFFFFFFFu, 0.0, &total);
-        const double limit = (double)p * (double)total;
+        const double limit = (double)p * (double)(total + all_rest);
         __syncthreads();
         if (search(sh, cut, 0, false, 0, limit, nullptr)) {
             const int bin = (int)sh.bin;
             const Cut above{0, 0, sh.before_c, sh.before_w};
-            auto in_step = [&](float x) {
+            // the step's ends, a little wider than their rounding
+            const float top = logit_of(r.kmax), wide = fabsf(top) * 1e-6f + 64.0f * 1e-6f;
+            const float hi = top - (float)(kBins - 1 - bin) / step + wide;
+            const float lo = bin == 0 ? -INFINITY : top - (float)(kBins - bin) / step - wide;
+            each_logit<L, L::FLIGHT>(row, V, [&](float x) { return x >= lo && x <= hi; }, [&](float x, int i) {
                 const uint32_t key = key_of(x);
-                return key > 0x007FFFFFu && r.bin(key, step) == bin;
-            };
-            each_logit<L, L::FLIGHT>(row, V, in_step, [&](float x, int i) {
-                const double w = r.weight(key_of(x));
-                if (w >= min_w && r.fixed(w) != 0) append(sh, list, key_of(x), i);
+                if (key <= 0x007FFFFFu || r.bin(key, step) != bin) return;
+                const double w = r.weight(key);
+                const uint64_t f = r.fixed(w);
+                if (w >= min_w && f >= small && f != 0) append(sh, list, key, i);
             });
             __syncthreads();
             if (sh.n <= (uint32_t)kList) {
@@ -691,9 +845,9 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
             if (key[e] == ckey) ++ties;
             else w += r.fixed(x);
         }
-        w = wave_sum_u64(w);
-        for (int d = 32; d > 0; d >>= 1) ties += __shfl_xor(ties, d, 64);
-        if (lane == 0) {
+        w = wave_scan(w);
+        if (__any(ties != 0)) ties = wave_scan(ties);
+        if (lane == 63) {
             seg_w[s] = w;
             seg_t[s] = ties;
         }
