@@ -20,8 +20,9 @@
 // One workgroup a row.  What it costs is the passes over the row and the
 // exponentials, so the selection runs on a short list in LDS wherever one
 // holds every token that can be kept (sample_kernel tells which):
-//  * top-k with k <= 1024: the k-th largest of the 1024 threads' own maxima is
-//    a logit that at least k tokens reach, and not many more do;
+//  * top-k with k <= 1024: the k-th largest of 2048 maxima, two of each
+//    thread's share, is a logit that at least k tokens reach, and not many
+//    more do;
 //  * min-p: the tokens of at least min_p;
 //  * top-p alone: the tokens of one of 2048 even steps of the logits, the one
 //    in which the weights pass top_p of their total.
@@ -89,7 +90,8 @@ __device__ __forceinline__ void load_keys(const void* row, int i, int V, uint32_
     }
 }
 
-// The logits x of a row for which pre(x) holds, as f(x, index), U vectors a
+// The logits x of a row for which pre(x, place in its vector)
+// holds, as f(x, index), U vectors a
 // thread in flight.  Vectors past the end are read from the last whole one and
 // their values dropped.
 template <class L, int U, class P, class F>
@@ -97,7 +99,7 @@ __device__ __forceinline__ void each_logit(const void* row, int V, P pre, F f) {
     constexpr int VEC = L::VEC, STEP = kThreads * VEC;
     const typename L::raw* x = static_cast<const typename L::raw*>(row);
     if (V < VEC) {
-        if ((int)threadIdx.x < V && pre(L::one(row, threadIdx.x))) f(L::one(row, threadIdx.x), (int)threadIdx.x);
+        if ((int)threadIdx.x < V && pre(L::one(row, threadIdx.x), 0)) f(L::one(row, threadIdx.x), (int)threadIdx.x);
         return;
     }
     struct __attribute__((packed, aligned(sizeof(typename L::raw)))) Vec {
@@ -114,66 +116,85 @@ __device__ __forceinline__ void each_logit(const void* row, int V, P pre, F f) {
             if (i + VEC <= V) {
                 bool any = false;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) any |= pre(L::value(w, e));
+                for (int e = 0; e < VEC; ++e) any |= pre(L::value(w, e), e);
                 if (any)
 #pragma unroll
                     for (int e = 0; e < VEC; ++e)
-                        if (pre(L::value(w, e))) f(L::value(w, e), i + e);
+                        if (pre(L::value(w, e), e)) f(L::value(w, e), i + e);
             } else if (i < V) {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
-                    if (at + e >= i && pre(L::value(w, e))) f(L::value(w, e), at + e);
+                    if (at + e >= i && pre(L::value(w, e), e)) f(L::value(w, e), at + e);
             }
         }
     }
 }
 
-// The largest logit of this thread's share of a row (-inf without one).
+// The largest logits of two halves of this thread's share of a row (-inf
+// without one).
 template <class L>
-__device__ __forceinline__ float largest(const void* row, int V) {
-    float m = -INFINITY;
-    // every value updates the maximum in `pre`: two instructions each
-    each_logit<L, L::FLIGHT>(row, V, [&](float x) { m = x > m ? x : m; return false; }, [](float, int) {});
-    return m;
+__device__ __forceinline__ void largest(const void* row, int V, float (&most)[2]) {
+    float m0 = -INFINITY, m1 = -INFINITY;
+    // every value updates a maximum in `pre`: two instructions each
+    each_logit<L, L::FLIGHT>(row, V, [&](float x, int e) {
+        float& m = e & 1 ? m1 : m0;
+        m = x > m ? x : m;
+        return false;
+    }, [](float, int) {});
+    most[0] = m0;
+    most[1] = m1;
 }
 
-// e^y for y <= 0: 2^n times the series of e^f, f = y - n ln 2, |f| <= ln 2 / 2.
-// The first term left out is f^13 / 13!, at most 2^-52.4 of the sum.
-__device__ __forceinline__ double exp_negative(double y) {
-    const double n = rint(y * 1.4426950408889634);
-    // ln 2 in two parts, the first with 32 bits: n times it is exact
-    const double f = fma(n, -1.9082149292705877e-10, fma(n, -0.69314718036912382, y));
-    double s = 1.0 / 479001600.0;
-    s = fma(s, f, 1.0 / 39916800.0);
-    s = fma(s, f, 1.0 / 3628800.0);
-    s = fma(s, f, 1.0 / 362880.0);
-    s = fma(s, f, 1.0 / 40320.0);
-    s = fma(s, f, 1.0 / 5040.0);
-    s = fma(s, f, 1.0 / 720.0);
-    s = fma(s, f, 1.0 / 120.0);
-    s = fma(s, f, 1.0 / 24.0);
-    s = fma(s, f, 1.0 / 6.0);
-    s = fma(s, f, 0.5);
-    s = fma(s, f, 1.0);
-    s = fma(s, f, 1.0);
-    return y < -746.0 ? 0.0 : ldexp(s, (int)fmax(n, -1100.0));
+// 2^f for |f| <= 1/2 by its series: the first term left out is
+// (f ln 2)^13 / 13!, at most 2^-52 of the sum.
+__device__ __forceinline__ double exp2_series(double f) {
+    constexpr double L = 0.69314718055994531, L2 = L * L, L3 = L2 * L, L4 = L2 * L2;
+    double s = L4 * L4 * L4 / 479001600.0;
+    s = fma(s, f, L4 * L4 * L3 / 39916800.0);
+    s = fma(s, f, L4 * L4 * L2 / 3628800.0);
+    s = fma(s, f, L4 * L4 * L / 362880.0);
+    s = fma(s, f, L4 * L4 / 40320.0);
+    s = fma(s, f, L4 * L3 / 5040.0);
+    s = fma(s, f, L4 * L2 / 720.0);
+    s = fma(s, f, L4 * L / 120.0);
+    s = fma(s, f, L4 / 24.0);
+    s = fma(s, f, L3 / 6.0);
+    s = fma(s, f, L2 / 2.0);
+    s = fma(s, f, L);
+    return fma(s, f, 1.0);
 }
 
 struct Row {
-    double max, inv_t;  // largest logit, 1 / T
+    double max, per_t;  // largest logit, log2(e) / T
     uint32_t kmax;
-    double fix;         // 2^S: fixed-point unit of the weights
-    __device__ __forceinline__ double weight(uint32_t key) const {
-        if (key == kmax) return 1.0;             // also +inf
-        if (key <= 0x007FFFFFu) return 0.0;      // -inf or no token
-        return exp_negative(((double)logit_of(key) - max) * inv_t);
+    int fix;            // weights are summed in units of 2^-fix, fix <= 52
+    // weight * 2^shift
+    __device__ __forceinline__ double scaled(uint32_t key, int shift) const {
+        if (key <= 0x007FFFFFu) return 0.0;  // -inf or no token
+        // also of the largest, +inf and overflow: the maximum of the fp64
+        // exponent's -1100 and NaN is -1100
+        const double y = key == kmax ? 0.0 : fmax(((double)logit_of(key) - max) * per_t, -1100.0);
+        const double n = rint(y);
+        return ldexp(exp2_series(y - n), (int)n + shift);
     }
-    __device__ __forceinline__ uint64_t fixed(double w) const { return (uint64_t)(w * fix + 0.5); }
+    __device__ __forceinline__ double weight(uint32_t key) const { return scaled(key, 0); }
+    // The weight in units of 2^-fix, to the nearest: the low bits of 2^52 plus it.
+    __device__ __forceinline__ uint64_t fixed(uint32_t key) const { return units(scaled(key, fix)); }
+    __device__ __forceinline__ uint64_t fixed(double weight) const { return units(ldexp(weight, fix)); }
+    static __device__ __forceinline__ uint64_t units(double x) {
+        return (uint64_t)__double_as_longlong(x + 4503599627370496.0) - 0x4330000000000000ull;
+    }
+    __device__ __forceinline__ double of_units(uint64_t x) const { return ldexp((double)x, -fix); }
     // Even steps of the logits below the largest, as bins that rise with the
     // logit: 2048 over the 32 T in which a weight can add to a sum, or over 64
     // where that is less.  Rounding keeps the order, so equal logits share a
     // bin and larger ones never have a lower one.
     __device__ __forceinline__ float step(float T) const { return (float)kBins / fminf(32.0f * T, 64.0f); }
+    // The lower end of a bin (above 0), less a margin that covers the roundings.
+    __device__ __forceinline__ float step_end(int bin, float step) const {
+        return top() - (float)(kBins - bin) / step - (fabsf(top()) + 64.0f) * 1e-6f;
+    }
+    __device__ __forceinline__ float top() const { return logit_of(kmax); }
     __device__ __forceinline__ int bin(uint32_t key, float step) const {
         if (key == kmax) return kBins - 1;  // also +inf
         return kBins - 1 - (int)fminf((logit_of(kmax) - logit_of(key)) * step, (float)(kBins - 1));
@@ -217,7 +238,6 @@ struct Shared {
     int seg;
     uint32_t seg_ties;
     unsigned long long seg_before;
-    unsigned long long votes[8];
     uint32_t n;  // tokens of the list, also past its end
 };
 
@@ -346,14 +366,14 @@ __device__ __forceinline__ void histogram_list(Shared& sh, const List& list, int
         if (key == 0 || key < floor_key || (cut.bits && (key >> (32 - cut.bits)) != cut.prefix)) continue;
         const uint32_t b = (key >> shift) & ((1u << digit) - 1);
         atomicAdd(&sh.count[b], 1u);
-        atomicAdd(&sh.weight[b], (unsigned long long)r.fixed(r.weight(key)));
+        atomicAdd(&sh.weight[b], (unsigned long long)r.fixed(key));
     }
     __syncthreads();
 }
 
 // How many of the tokens with the cut's logit are in, by weight.
 __device__ __forceinline__ uint32_t ties_in(const Row& r, const Cut& cut, double limit) {
-    const uint64_t one = r.fixed(r.weight(cut.prefix));
+    const uint64_t one = r.fixed(cut.prefix);
     const double n = one ? ceil((limit - (double)cut.w) / (double)one) : 1.0;
     return n < 1.0 ? 1u : n > 2147483647.0 ? 0x7FFFFFFFu : (uint32_t)n;
 }
@@ -366,28 +386,23 @@ __device__ __forceinline__ void append(Shared& sh, List& list, uint32_t key, int
     }
 }
 
-// The upper 16 bits of the k-th largest of the threads' values, 1 <= k <= 1024:
-// at least k of them reach it.  Two bits a round: how many reach each of the
-// three values that they can make larger.
-__device__ __forceinline__ uint32_t kth_of_threads(Shared& sh, uint32_t mine, uint32_t k) {
-    uint32_t prefix = 0;
-#pragma unroll 1
-    for (int bit = 30; bit >= 16; bit -= 2) {
-        uint64_t votes = 0;
-#pragma unroll
-        for (uint32_t d = 1; d < 4; ++d)
-            votes |= (uint64_t)__popcll(__ballot(mine >= (prefix | (d << bit)))) << (16 * d);
-        unsigned long long* sum = sh.votes + (30 - bit) / 2;  // one a round, zero before
-        if ((threadIdx.x & 63) == 0) atomicAdd(sum, (unsigned long long)votes);
-        __syncthreads();
-        votes = *sum;
-        uint32_t best = 0;
-#pragma unroll
-        for (uint32_t d = 1; d < 4; ++d)
-            if ((uint32_t)(votes >> (16 * d) & 0xFFFFu) >= k) best = d;
-        prefix |= best << bit;
+// A logit that at least k tokens reach: the lower end of the step that holds
+// the k-th largest of the threads' 2 * kThreads maxima, which are logits of
+// different tokens.  The lowest finite one if there is no such step.
+__device__ __forceinline__ uint32_t floor_of_best(Shared& sh, const Row& r, const float (&most)[2], uint32_t k) {
+    const float step = (float)kBins / 64.0f;
+    for (int i = threadIdx.x; i < kBins; i += kThreads) {
+        sh.count[i] = 0;
+        sh.weight[i] = 0;
     }
-    return prefix;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (most[i] > -INFINITY) atomicAdd(&sh.count[r.bin(key_of(most[i]), step)], 1u);
+    __syncthreads();
+    Cut cut{0, 0, 0, 0};
+    if (!search(sh, cut, 0, true, k, 0.0, nullptr) || sh.bin == 0) return 0x00800000u;
+    return max(key_of(r.step_end((int)sh.bin, step)), 0x00800000u);
 }
 
 // A logit that every token of weight min_p or more reaches, by a margin that
@@ -502,7 +517,7 @@ __device__ __forceinline__ void draw_in_wave(Shared& sh, const List& list, int n
         const bool here = u > 0.0f ? (!((double)b > target) && (double)(b + one) > target) : (e == 0 && lane == 0);
         if (here && at[e]) {
             *token = (int32_t)((1u << 20) - (at[e] >> 10));
-            if (logprob) *logprob = (float)log(r.weight(sh.count[rank]) / ((double)total / r.fix));
+            if (logprob) *logprob = (float)log(r.weight(sh.count[rank]) / r.of_units(total));
         }
     }
 }
@@ -532,7 +547,7 @@ __device__ __forceinline__ void draw_from_list(Shared& sh, List& list, int n, co
         ckey = cut.prefix;
         cties = (uint32_t)k - cut.c;
         ties = sh.count[sh.bin];
-        total = cut.w + cties * r.fixed(r.weight(ckey));
+        total = cut.w + cties * r.fixed(ckey);
     }
     if (p < 1.0f) {
         const double limit = (double)p * (double)total;
@@ -553,6 +568,7 @@ __device__ __forceinline__ void draw_from_list(Shared& sh, List& list, int n, co
     // what the cut leaves, by steps of the row's index: kBins at most
     __syncthreads();
     for (int i = tid; i < kBins; i += kThreads) sh.weight[i] = 0;
+    if (tid == 0) sh.n = 0;
     __syncthreads();
     int shift = 0;
     while ((V - 1) >> shift >= kBins) ++shift;
@@ -572,7 +588,7 @@ __device__ __forceinline__ void draw_from_list(Shared& sh, List& list, int n, co
             continue;
         }
         first = min(first, at);
-        atomicAdd(&sh.weight[at >> shift], (unsigned long long)r.fixed(r.weight(key)));
+        atomicAdd(&sh.weight[at >> shift], (unsigned long long)r.fixed(key));
     }
     for (int d = 32; d > 0; d >>= 1) first = min(first, (uint32_t)__shfl_xor((int)first, d, 64));
     if (lane == 0 && first != 0xFFFFFFFFu) atomicMin(&sh.first, first);
@@ -596,25 +612,27 @@ __device__ __forceinline__ void draw_from_list(Shared& sh, List& list, int n, co
         before = next;
     }
     __syncthreads();
-    // the token inside its step; u = 0 takes the first one that is kept
+    // the token inside its step, of whose tokens (V / kBins at most) one
+    // thread each sums the ones before; u = 0 takes the first that is kept
+    static_assert(kSampleMaxVocab / kBins <= kThreads, "a thread for every token of a step");
     const uint32_t seg = (uint32_t)sh.seg;
     for (int i = tid; i < n; i += kThreads) {
         const uint32_t key = list.key[i], at = list.idx[i];
-        if (key == 0) continue;
-        const double x = r.weight(key);
-        bool here = at == sh.first;
-        if (u > 0.0f) {
-            if (at >> shift != seg) continue;
-            uint64_t b = sh.seg_before;
-            for (int j = 0; j < n; ++j)
-                if (list.key[j] != 0 && list.idx[j] >> shift == seg && list.idx[j] < at) b += r.fixed(r.weight(list.key[j]));
-            here = !((double)b > target) && (double)(b + r.fixed(x)) > target;
-        }
-        if (here) {
-            *token = (int32_t)at;
-            if (logprob) *logprob = (float)log(x / ((double)total / r.fix));
-        }
+        if (key == 0 || (u > 0.0f ? at >> shift != seg : at != sh.first)) continue;
+        const uint32_t place = atomicAdd(&sh.n, 1u);
+        sh.count[place] = (uint32_t)i;
+        sh.weight[place] = (unsigned long long)r.fixed(key);
     }
+    __syncthreads();
+    const int m = (int)sh.n;
+    if (tid >= m) return;
+    const uint32_t key = list.key[sh.count[tid]], at = list.idx[sh.count[tid]];
+    uint64_t past = sh.seg_before;
+    for (int j = 0; j < m; ++j)
+        if (list.idx[sh.count[j]] < at) past += sh.weight[j];
+    if (u > 0.0f && ((double)past > target || !((double)(past + sh.weight[tid]) > target))) return;
+    *token = (int32_t)at;
+    if (logprob) *logprob = (float)log(r.weight(key) / r.of_units(total));
 }
 
 template <class L>
@@ -634,9 +652,10 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         sh.first = 0xFFFFFFFFu;
         sh.n = 0;
     }
-    if (tid < 8) sh.votes[tid] = 0;
     __syncthreads();
-    const uint32_t my_key = key_of(largest<L>(row, V));
+    float most[2];
+    largest<L>(row, V, most);
+    const uint32_t my_key = key_of(fmaxf(most[0], most[1]));
     uint32_t best = my_key;
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) best = max(best, (uint32_t)__shfl_xor((int)best, d, 64));
@@ -662,7 +681,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         const float x0 = logit_of(r.kmax);
         uint32_t at = 0xFFFFFFFFu;
         if (my_key == r.kmax)
-            each_logit<L, L::FLIGHT>(row, V, [&](float x) { return x == x0; }, [&](float, int i) { at = min(at, (uint32_t)i); });
+            each_logit<L, L::FLIGHT>(row, V, [&](float x, int) { return x == x0; }, [&](float, int i) { at = min(at, (uint32_t)i); });
         if (at != 0xFFFFFFFFu) atomicMin(&sh.first, at);
         __syncthreads();
         if (tid == 0) {
@@ -672,7 +691,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         return;
     }
     r.max = (double)logit_of(r.kmax);
-    r.inv_t = 1.0 / (double)T;
+    r.per_t = 1.4426950408889634 / (double)T;
     r.fix = a.fix;
 
     // the cut: tokens with keys above `ckey`, and the first `cties` with it
@@ -688,12 +707,12 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         bound = 0x00800000u;
     } else {
         if (min_w > 0.0) bound = floor_of(r, (double)T, min_w);
-        if (by_k && k <= kThreads) bound = max(bound, max(kth_of_threads(sh, my_key, (uint32_t)k), 0x00800000u));
+        if (by_k && k <= kThreads) bound = max(bound, floor_of_best(sh, r, most, (uint32_t)k));
     }
     bool listed = false;
     if (bound) {
         const float x0 = logit_of(bound);
-        each_logit<L, L::FLIGHT>(row, V, [&](float x) { return x >= x0; }, [&](float x, int i) { append(sh, list, key_of(x), i); });
+        each_logit<L, L::FLIGHT>(row, V, [&](float x, int) { return x >= x0; }, [&](float x, int i) { append(sh, list, key_of(x), i); });
         __syncthreads();
         listed = sh.n <= (uint32_t)kList;
     }
@@ -727,7 +746,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         // cut, and only count in the total.
         const uint64_t small = r.fixed((1.0 - (double)p) / (double)V * 0.999);
         uint64_t rest = 0;
-        each_logit<L, 2>(row, V, [](float) { return true; }, [&](float x, int) {
+        each_logit<L, 2>(row, V, [](float, int) { return true; }, [&](float x, int) {
             const uint32_t key = key_of(x);
             const double w = r.weight(key);
             const uint64_t f = r.fixed(w);
@@ -753,10 +772,9 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
             const int bin = (int)sh.bin;
             const Cut above{0, 0, sh.before_c, sh.before_w};
             // the step's ends, a little wider than their rounding
-            const float top = logit_of(r.kmax), wide = fabsf(top) * 1e-6f + 64.0f * 1e-6f;
-            const float hi = top - (float)(kBins - 1 - bin) / step + wide;
-            const float lo = bin == 0 ? -INFINITY : top - (float)(kBins - bin) / step - wide;
-            each_logit<L, L::FLIGHT>(row, V, [&](float x) { return x >= lo && x <= hi; }, [&](float x, int i) {
+            const float lo = bin == 0 ? -INFINITY : r.step_end(bin, step);
+            const float hi = bin == kBins - 1 ? INFINITY : r.step_end(bin + 1, step) + (fabsf(r.top()) + 64.0f) * 2e-6f;
+            each_logit<L, L::FLIGHT>(row, V, [&](float x, int) { return x >= lo && x <= hi; }, [&](float x, int i) {
                 const uint32_t key = key_of(x);
                 if (key <= 0x007FFFFFu || r.bin(key, step) != bin) return;
                 const double w = r.weight(key);
@@ -794,7 +812,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
             if (in) {  // otherwise fewer than k tokens are left, and `total` is their weight
                 ckey = cut.prefix;
                 cties = (uint32_t)k - cut.c;
-                total = cut.w + cties * r.fixed(r.weight(ckey));
+                total = cut.w + cties * r.fixed(ckey);
             }
         }
         if (by_p) {
@@ -855,7 +873,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
     for (int d = 32; d > 0; d >>= 1) first = min(first, (uint32_t)__shfl_xor((int)first, d, 64));
     if (lane == 0) atomicMin(&sh.first, first);
     __syncthreads();
-    const uint64_t one = ckey ? r.fixed(r.weight(ckey)) : 0;
+    const uint64_t one = ckey ? r.fixed(ckey) : 0;
     const int per = (segs + kThreads - 1) / kThreads;
     const int s0 = min(segs, tid * per), s1 = min(segs, s0 + per);
     uint32_t tc = 0, bt, all_t;
@@ -926,14 +944,14 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         const bool here = u > 0.0f ? (!((double)before > target) && (double)next > target) : false;
         if (here) {
             a.tokens[b] = i + e;
-            if (a.logprobs) a.logprobs[b] = (float)log(r.weight(key[e]) / ((double)all_w / r.fix));
+            if (a.logprobs) a.logprobs[b] = (float)log(r.weight(key[e]) / r.of_units(all_w));
         }
         before = next;
     }
     if (u == 0.0f && lane == 0) {
         const uint32_t f = sh.first;
         a.tokens[b] = (int32_t)f;
-        if (a.logprobs) a.logprobs[b] = (float)log(r.weight(key_of(L::one(row, f))) / ((double)all_w / r.fix));
+        if (a.logprobs) a.logprobs[b] = (float)log(r.weight(key_of(L::one(row, f))) / r.of_units(all_w));
     }
 }
 
@@ -943,7 +961,7 @@ hipError_t launch_sample(const SampleArgs& args, hipStream_t s) {
     SampleArgs a = args;
     int bits = 0;
     while (((int64_t)1 << bits) < a.V) ++bits;
-    a.fix = ldexp(1.0, 62 - bits);
+    a.fix = bits < 10 ? 52 : 62 - bits;  // V weights of 2^fix at most: sums stay below 2^63
     const int seg = a.dtype == 2 ? 64 * LogitF32::VEC : 64 * 8;
     size_t lds = (size_t)((a.V + seg - 1) / seg) * 12 + 8;
     if (lds < sizeof(List)) lds = sizeof(List);

@@ -241,7 +241,7 @@ struct SampleArgs {
     const float *top_p, *min_p;
     int32_t* tokens;
     float* logprobs;
-    double fix = 0;  // set by the launcher: fixed-point unit of the weights
+    int fix = 0;  // set by the launcher: weights are summed in units of 2^-fix
 };
 hipError_t launch_sample(const SampleArgs& a, hipStream_t s);
 
