@@ -93,19 +93,20 @@ __device__ __forceinline__ void load_keys(const void* row, int i, int V, uint32_
 // The logits x of a row for which pre(x, place in its vector)
 // holds, as f(x, index), U vectors a
 // thread in flight.  Vectors past the end are read from the last whole one and
-// their values dropped.
+// their values dropped.  `from`, `to`: of the row, whole rounds of U vectors a
+// thread, without either the whole row.
 template <class L, int U, class P, class F>
-__device__ __forceinline__ void each_logit(const void* row, int V, P pre, F f) {
+__device__ __forceinline__ void each_logit(const void* row, int V, P pre, F f, int from = 0, int to = INT32_MAX) {
     constexpr int VEC = L::VEC, STEP = kThreads * VEC;
     const typename L::raw* x = static_cast<const typename L::raw*>(row);
     if (V < VEC) {
-        if ((int)threadIdx.x < V && pre(L::one(row, threadIdx.x), 0)) f(L::one(row, threadIdx.x), (int)threadIdx.x);
+        if (from == 0 && (int)threadIdx.x < V && pre(L::one(row, threadIdx.x), 0)) f(L::one(row, threadIdx.x), (int)threadIdx.x);
         return;
     }
     struct __attribute__((packed, aligned(sizeof(typename L::raw)))) Vec {
         uint32_t w[4];
     };
-    for (int base = (int)threadIdx.x * VEC; base < V; base += U * STEP) {
+    for (int base = from + (int)threadIdx.x * VEC; base < min(V, to); base += U * STEP) {
         Vec v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) v[u] = *reinterpret_cast<const Vec*>(x + min(base + u * STEP, V - VEC));
@@ -114,13 +115,16 @@ __device__ __forceinline__ void each_logit(const void* row, int V, P pre, F f) {
             const int i = base + u * STEP, at = min(i, V - VEC);
             const uint32_t w[4] = {v[u].w[0], v[u].w[1], v[u].w[2], v[u].w[3]};
             if (i + VEC <= V) {
-                bool any = false;
+                uint32_t hits = 0;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) any |= pre(L::value(w, e), e);
-                if (any)
+                for (int e = 0; e < VEC; ++e) hits |= pre(L::value(w, e), e) ? 1u << e : 0u;
+                for (; hits; hits &= hits - 1) {
+                    const int e = __ffs((int)hits) - 1;
+                    float x = L::value(w, 0);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        if (pre(L::value(w, e), e)) f(L::value(w, e), i + e);
+                    for (int o = 1; o < VEC; ++o) x = e == o ? L::value(w, o) : x;
+                    f(x, i + e);
+                }
             } else if (i < V) {
 #pragma unroll
                 for (int e = 0; e < VEC; ++e)
@@ -128,21 +132,6 @@ __device__ __forceinline__ void each_logit(const void* row, int V, P pre, F f) {
             }
         }
     }
-}
-
-// The largest logits of two halves of this thread's share of a row (-inf
-// without one).
-template <class L>
-__device__ __forceinline__ void largest(const void* row, int V, float (&most)[2]) {
-    float m0 = -INFINITY, m1 = -INFINITY;
-    // every value updates a maximum in `pre`: two instructions each
-    each_logit<L, L::FLIGHT>(row, V, [&](float x, int e) {
-        float& m = e & 1 ? m1 : m0;
-        m = x > m ? x : m;
-        return false;
-    }, [](float, int) {});
-    most[0] = m0;
-    most[1] = m1;
 }
 
 // 2^f for |f| <= 1/2 by its series: the first term left out is
@@ -416,109 +405,90 @@ __device__ __forceinline__ uint32_t floor_of(const Row& r, double T, double min_
     return f > -3.0e38f ? key_of(f) : 0x00800000u;
 }
 
-// Sorts 64 R values, element 64 r + lane in v[r] of the lane, the largest first,
-// in one wave: a bitonic network, its steps of 64 and more between registers.
-template <class N>
-__device__ __forceinline__ N from_xor(N v, int d) {
-    if constexpr (sizeof(N) == 8) return (N)__shfl_xor((unsigned long long)v, d, 64);
-    else return (N)__shfl_xor((int)v, d, 64);
-}
-template <int R, int SIZE, class N>
-__device__ __forceinline__ void sort_runs(N (&v)[R]) {
-    const int lane = threadIdx.x & 63;
-    if constexpr (SIZE > 2) sort_runs<R, SIZE / 2>(v);
-#pragma unroll
-    for (int s = SIZE / 128; s > 0; s >>= 1)
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            if (!(r & s)) {
-                const bool down = !((64 * r) & SIZE);
-                const N x = v[r], y = v[r | s];
-                const N hi = x > y ? x : y, lo = x > y ? y : x;
-                v[r] = down ? hi : lo;
-                v[r | s] = down ? lo : hi;
-            }
-#pragma unroll 1
-    for (int s = SIZE > 64 ? 32 : SIZE / 2; s > 0; s >>= 1) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const bool down = !((64 * r + lane) & SIZE);
-            const N x = v[r], y = from_xor(x, s);
-            const bool larger = down == !(lane & s);  // keeps the larger of the two
-            v[r] = (x > y) == larger ? x : y;
+// Cuts and the drawing where the list holds every token that can be kept, at
+// most kFew.  Every token's place by rank and by index is counted, all pairs
+// spread over the workgroup's threads; then two prefix sums of the weights, in
+// the one order and in the other, give the cut and the token.  Against passes
+// of histograms this is a few short loops: code that runs once is bound by its
+// own fetch and by the workgroup's barriers.
+constexpr int kFew = 512;
+__device__ __forceinline__ void draw_from_few(Shared& sh, const List& list, int n, const Row& r, double min_w, int k, float p,
+                                              float u, int32_t* token, float* logprob) {
+    const int tid = threadIdx.x;
+    struct Few {
+        uint64_t rank[kFew], by_rank[kFew], by_idx[kFew];
+        uint32_t place[kFew];  // by rank, and << 16 by index
+    };
+    static_assert(sizeof(Few) <= sizeof(sh.count) + sizeof(sh.weight), "the bins' memory");
+    Few& few = *reinterpret_cast<Few*>(sh.count);
+    int width = 64;
+    while (width < n) width *= 2;
+    bool in = false;
+    uint32_t key = 0, at = 0xFFFFFFFFu;
+    uint64_t w = 0;
+    double x = 0.0;
+    __syncthreads();
+    if (tid < width) {
+        if (tid < n) {
+            key = list.key[tid];
+            at = list.idx[tid];
+            x = r.weight(key);
+            in = x > 0.0 && !(x < min_w);
+            w = in ? r.fixed(x) : 0ull;
         }
+        // larger: a better rank; the low word falls with the index also where
+        // the token is out (no key), and is 0 past the list
+        few.rank[tid] = (uint64_t)(in ? key : 0u) << 32 | (uint32_t)~at;
+        few.by_rank[tid] = few.by_idx[tid] = 0;
+        few.place[tid] = 0;
     }
-}
-template <int R, class N>
-__device__ __forceinline__ void sort_wave(N (&v)[R]) {
-    sort_runs<R, 64 * R>(v);
-}
-
-// Cuts and the drawing in one wave, where the list holds every token that can
-// be kept and they are 64 R at most: the tokens are sorted by rank, their
-// weights summed in that order and cut, and what is left sorted by index.
-// A workgroup's barriers and LDS traffic cost more than so few tokens do.
-template <int R>
-__device__ __forceinline__ void draw_in_wave(Shared& sh, const List& list, int n, const Row& r, double min_w, int k, float p,
-                                             float u, int32_t* token, float* logprob) {
-    const int lane = threadIdx.x & 63;
-    uint64_t v[R];
+    __syncthreads();
+    {
+        const int mine = tid & (width - 1), part = tid / width, parts = kThreads / width;
+        const int per = ((width / 4 + parts - 1) / parts) * 4, j1 = min(width, (part + 1) * per);
+        const uint64_t rank = few.rank[mine];
+        uint32_t place = 0;
+#pragma unroll 1
+        for (int j = part * per; j < j1; j += 4) {
+            uint64_t other[4];
 #pragma unroll
-    for (int e = 0; e < R; ++e) {
-        const int i = 64 * e + lane;
-        v[e] = i < n ? (uint64_t)list.key[i] << 32 | (uint32_t)~list.idx[i] : 0ull;
+            for (int e = 0; e < 4; ++e) other[e] = few.rank[j + e];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                place += (other[e] > rank ? 1u : 0u) + ((uint32_t)other[e] > (uint32_t)rank ? 0x10000u : 0u);
+        }
+        atomicAdd(&few.place[mine], place);
     }
-    sort_wave(v);
-    // weights by rank, of the first k that are of min_p
-    uint64_t w[R], before[R], total = 0;
-    bool in[R];
-#pragma unroll
-    for (int e = 0; e < R; ++e) {
-        const double x = r.weight((uint32_t)(v[e] >> 32));
-        in[e] = v[e] != 0 && 64 * e + lane < k && x > 0.0 && !(x < min_w);
-        w[e] = in[e] ? r.fixed(x) : 0ull;
-        const uint64_t sum = wave_scan(w[e]);
-        before[e] = total + sum - w[e];
-        total += lane_of(sum, 63);
+    __syncthreads();
+    uint32_t by_rank = 0, by_idx = 0, none_c, all_c;
+    if (tid < n) {
+        by_rank = few.place[tid] & 0xFFFFu;
+        by_idx = few.place[tid] >> 16;
+        in = in && by_rank < (uint32_t)k;
+        if (in) few.by_rank[by_rank] = w;
     }
     if (p < 1.0f) {
-        const double limit = (double)p * (double)total;
-        total = 0;
-#pragma unroll
-        for (int e = 0; e < R; ++e) {
-            in[e] = in[e] && (double)before[e] < limit;
-            if (!in[e]) w[e] = 0;
-            total += lane_of(wave_scan(w[e]), 63);
-        }
+        uint64_t before, total;
+        __syncthreads();
+        block_scan(sh, 0u, tid < width ? few.by_rank[tid] : (uint64_t)0, &none_c, &before, &all_c, &total);
+        if (tid < width) few.by_rank[tid] = before;
+        __syncthreads();
+        in = in && (double)few.by_rank[by_rank] < (double)p * (double)total;
     }
-    // by index: the largest first of (2^20 - index, rank); 0 for what is out
-    static_assert(kSampleMaxVocab <= 1 << 20 && 64 * R <= 1 << 10, "index and rank share 32 bits");
-    uint32_t at[R];
-#pragma unroll
-    for (int e = 0; e < R; ++e) {
-        const int rank = 64 * e + lane;
-        sh.count[rank] = (uint32_t)(v[e] >> 32);
-        sh.weight[rank] = w[e];
-        at[e] = in[e] ? ((1u << 20) - (uint32_t)~v[e]) << 10 | (uint32_t)rank : 0u;
+    if (in) {
+        few.by_idx[by_idx] = w;
+        atomicMin(&sh.first, by_idx);
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    sort_wave(at);
+    __syncthreads();
+    const uint64_t one = tid < width ? few.by_idx[tid] : (uint64_t)0;
+    uint64_t past, total;
+    block_scan(sh, 0u, one, &none_c, &past, &all_c, &total);
     const double target = (double)u * (double)total;
-    uint64_t past = 0;
-#pragma unroll
-    for (int e = 0; e < R; ++e) {
-        const uint32_t rank = at[e] & 1023u;
-        const uint64_t one = at[e] ? sh.weight[rank] : 0ull;
-        const uint64_t sum = wave_scan(one), b = past + sum - one;
-        past += lane_of(sum, 63);
-        // u = 0 takes the first token that is kept
-        const bool here = u > 0.0f ? (!((double)b > target) && (double)(b + one) > target) : (e == 0 && lane == 0);
-        if (here && at[e]) {
-            *token = (int32_t)((1u << 20) - (at[e] >> 10));
-            if (logprob) *logprob = (float)log(r.weight(sh.count[rank]) / r.of_units(total));
-        }
+    if (u > 0.0f && !((double)past > target) && (double)(past + one) > target) sh.first = (uint32_t)tid;
+    __syncthreads();
+    if (in && by_idx == sh.first) {  // u = 0: the first token that is kept
+        *token = (int32_t)at;
+        if (logprob) *logprob = (float)log(x / r.of_units(total));
     }
 }
 
@@ -653,14 +623,44 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         sh.n = 0;
     }
     __syncthreads();
-    float most[2];
-    largest<L>(row, V, most);
-    const uint32_t my_key = key_of(fmaxf(most[0], most[1]));
-    uint32_t best = my_key;
+    // One pass takes the largest logits of two halves of each thread's share
+    // (every value updates a maximum in `pre`, two instructions each).  A long
+    // row with min-p begins its list in the same pass: the tokens that pass
+    // min-p pass it against the largest logit of the row's first round too.
+    float most[2] = {-INFINITY, -INFINITY};
+    const auto largest = [&](float x, int e) {
+        float& m = most[e & 1];
+        m = x > m ? x : m;
+        return false;
+    };
+    const auto workgroup_best = [&] {
+        uint32_t best = key_of(fmaxf(most[0], most[1]));
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) best = max(best, (uint32_t)__shfl_xor((int)best, d, 64));
-    if (lane == 0) atomicMax(&sh.best, best);
-    __syncthreads();
+        for (int d = 32; d > 0; d >>= 1) best = max(best, (uint32_t)__shfl_xor((int)best, d, 64));
+        if (lane == 0) atomicMax(&sh.best, best);
+        __syncthreads();
+        return sh.best;
+    };
+    constexpr int ROUND = L::FLIGHT * VEC * kThreads;
+    const float T = a.temperature ? a.temperature[b] : 1.0f;
+    const float min_p = a.min_p ? a.min_p[b] : 0.0f;
+    const double min_w = min_p > 0.0f ? (double)min_p : 0.0;
+    const bool early = V > 2 * ROUND && T > 0.0f && min_p > 0.0f && min_p <= 1.0f;
+    if (early) {
+        each_logit<L, L::FLIGHT>(row, V, largest, [](float, int) {}, 0, ROUND);
+        Row first;
+        first.kmax = workgroup_best();
+        first.max = (double)logit_of(first.kmax);
+        const float x0 = first.kmax > 0x007FFFFFu ? logit_of(floor_of(first, (double)T, min_w)) : -3.0e38f;
+        each_logit<L, L::FLIGHT>(row, V, [&](float x, int e) {
+            largest(x, e);
+            return x >= x0;
+        }, [&](float x, int i) { append(sh, list, key_of(x), i); }, ROUND);
+    } else {
+        each_logit<L, L::FLIGHT>(row, V, largest, [](float, int) {});
+    }
+    workgroup_best();
+    const uint32_t my_key = key_of(fmaxf(most[0], most[1]));
     Row r;
     r.kmax = sh.best;
     if (r.kmax <= 0x007FFFFFu) {  // every logit is -inf or NaN
@@ -670,9 +670,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         }
         return;
     }
-    const float T = a.temperature ? a.temperature[b] : 1.0f;
     const float p = a.top_p ? a.top_p[b] : 1.0f;
-    const float min_p = a.min_p ? a.min_p[b] : 0.0f;
     int k = a.top_k ? a.top_k[b] : 0;
     if (k <= 0 || k > V) k = V;
     float u = a.u[b];
@@ -695,7 +693,6 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
     r.fix = a.fix;
 
     // the cut: tokens with keys above `ckey`, and the first `cties` with it
-    const double min_w = min_p > 0.0f ? (double)min_p : 0.0;
     uint32_t ckey = 0, cties = 0;
     const bool by_k = k < V, by_p = p < 1.0f;
     const int digits[3] = {11, 11, 10};
@@ -712,17 +709,37 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
     bool listed = false;
     if (bound) {
         const float x0 = logit_of(bound);
-        each_logit<L, L::FLIGHT>(row, V, [&](float x, int) { return x >= x0; }, [&](float x, int i) { append(sh, list, key_of(x), i); });
+        // of the list begun above, what the first round adds; otherwise, or if it overflowed, all of it
+        const bool begun = early && sh.n <= (uint32_t)kList;
+        __syncthreads();
+        if (!begun && tid == 0) sh.n = 0;
+        __syncthreads();
+        each_logit<L, L::FLIGHT>(row, V, [&](float x, int) { return x >= x0; },
+                                 [&](float x, int i) { append(sh, list, key_of(x), i); }, 0, begun ? ROUND : INT32_MAX);
         __syncthreads();
         listed = sh.n <= (uint32_t)kList;
+        if (begun && listed && sh.n > 64u) {
+            // the list was begun with a lower bound: what this one leaves of it
+            constexpr int PER = kList / kThreads;
+            uint32_t keys[PER], at[PER];
+            const int n = (int)sh.n;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                const int i = tid + e * kThreads;
+                keys[e] = i < n ? list.key[i] : 0u;
+                at[e] = i < n ? list.idx[i] : 0u;
+            }
+            __syncthreads();
+            if (tid == 0) sh.n = 0;
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < PER; ++e)
+                if (keys[e] >= bound) append(sh, list, keys[e], (int)at[e]);
+            __syncthreads();
+        }
     }
-    if (listed && sh.n <= 1024u) {
-        if (wave != 0) return;
-        const int n = (int)sh.n;
-        float* logprob = a.logprobs ? a.logprobs + b : nullptr;
-        if (n <= 64) draw_in_wave<1>(sh, list, n, r, min_w, k, p, u, a.tokens + b, logprob);
-        else if (n <= 256) draw_in_wave<4>(sh, list, n, r, min_w, k, p, u, a.tokens + b, logprob);
-        else draw_in_wave<16>(sh, list, n, r, min_w, k, p, u, a.tokens + b, logprob);
+    if (listed && sh.n <= (uint32_t)kFew) {
+        draw_from_few(sh, list, (int)sh.n, r, min_w, k, p, u, a.tokens + b, a.logprobs ? a.logprobs + b : nullptr);
         return;
     }
     if (listed) {
