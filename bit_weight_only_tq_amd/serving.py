@@ -10,37 +10,73 @@ call (the C ABI takes bare pointers), and there is no CPU fallback.
 from typing import NamedTuple
 
 from . import _lib
-from ._lib import TQ_BF16, TQ_F16, TQ_F32, _check, _dtype_enum, _ptr, _stream
+from ._lib import TQ_BF16, TQ_F16, TQ_F32, _check
 
-_LOGITS = {"torch.float16": TQ_F16, "torch.bfloat16": TQ_BF16, "torch.float32": TQ_F32}
+# A serving step calls these once a layer, often on a few rows: what a call
+# costs is then the host's time, so a check is a comparison or two, pointers
+# are passed as the integers they are, and only a failed check pays for words.
+
+
+class _Torch:
+    """torch's types and its current stream, looked up at the first call."""
+
+    def __init__(self):
+        import torch
+        self.i32, self.i64, self.f32 = torch.int32, torch.int64, torch.float32
+        self.cache = {torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}
+        self.logits = {**self.cache, torch.float32: TQ_F32}
+        # the stream's handle without a Stream object around it (2 us less), where torch has it
+        self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+_torch = None
+
+
+def _types():
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
 
 
 def _tensor(name, t, dtype, dim, shape=None):
-    if t.dtype != dtype or t.dim() != dim:
+    if t.dtype is not dtype or t.dim() != dim:
         raise TypeError(f"{name} must be a {dim}-D {dtype} tensor, got {t.dim()}-D {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
 
+def _vector(name, t, dtype, n=None):
+    """A contiguous vector (of n entries); -> its address."""
+    if t.dtype is not dtype or t.dim() != 1:
+        raise TypeError(f"{name} must be a 1-D {dtype} tensor, got {t.dim()}-D {t.dtype}")
+    if n is not None and t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
 def _on_device(*ts):
-    """All tensors are device tensors of one device."""
-    dev = None
+    """All tensors are device tensors of one device; -> its index."""
+    index = None
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
+        i = t.get_device()  # -1: host memory
+        if i < 0:
             raise ValueError("tensors must be device tensors")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors must live on one device, got {dev} and {t.device}")
-    return dev
+        if i != index:
+            if index is not None:
+                raise ValueError(f"tensors must live on one device, got {index} and {i}")
+            index = i
+    return index
 
 
-def _contiguous(**ts):
-    for name, t in ts.items():
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+def _contiguous(name, t):
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def _table_stride(page_table):
@@ -55,30 +91,34 @@ def _table_stride(page_table):
 
 
 def _cache(k_cache, v_cache):
-    """Checks the caches [pages, Hkv, page_size, D]; -> elements between pages."""
-    import torch
-    if k_cache.dim() != 4 or k_cache.dtype not in (torch.float16, torch.bfloat16):
+    """Checks the caches [pages, Hkv, page_size, D]; -> (tq_dtype, elements between pages)."""
+    dt = _types().cache.get(k_cache.dtype)
+    if k_cache.dim() != 4 or dt is None:
         raise TypeError("k_cache must be a 4-D float16 or bfloat16 tensor [pages, heads, page_size, D]")
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or v_cache.stride() != k_cache.stride():
+    if v_cache.shape != k_cache.shape or v_cache.dtype is not k_cache.dtype or v_cache.stride() != k_cache.stride():
         raise ValueError("k_cache and v_cache must be alike in shape, type and strides")
     pages, H, page, D = k_cache.shape
+    if k_cache.is_contiguous():
+        return dt, H * page * D
     if not k_cache[:1].is_contiguous():
         raise ValueError("the pages of a cache must be contiguous")
     stride = k_cache.stride(0) if pages > 1 else H * page * D
     if stride < H * page * D:
         raise ValueError("the pages of a cache must not overlap")
-    return stride
+    return dt, stride
 
 
 def _heads(name, t, dtype, T, D):
     """Checks a [T, heads, D] tensor whose last dimension is contiguous; -> (heads, token stride, head stride)."""
-    if t.dim() != 3 or t.dtype != dtype:
+    if t.dim() != 3 or t.dtype is not dtype:
         raise TypeError(f"{name} must be a 3-D {dtype} tensor, got {t.dim()}-D {t.dtype}")
-    if t.shape[0] != T or t.shape[2] != D:
+    n, heads, d = t.shape
+    if n != T or d != D:
         raise ValueError(f"{name} must be [{T}, heads, {D}], got {tuple(t.shape)}")
-    if D > 1 and t.stride(2) != 1:
+    token, head, one = t.stride()
+    if one != 1 and D > 1:
         raise ValueError(f"the heads of {name} must be contiguous")
-    return t.shape[1], t.stride(0), t.stride(1)
+    return heads, token, head
 
 
 # --------------------------------------------------------------------- plan
@@ -101,35 +141,36 @@ def tq_paged_plan(ctx_lens, new_lens, page_table, free_pages, free_head, tokens:
     read only: the head after the step is state[0]; tokens: entries of
     positions and slots, at least new_lens' sum (a larger number pads with
     slot -1).  out: a plan to write into, for steps replayed from a graph."""
-    import torch
-    i32 = torch.int32
-    _tensor("ctx_lens", ctx_lens, i32, 1)
+    ty = _types()
+    i32 = ty.i32
+    ctx = _vector("ctx_lens", ctx_lens, i32)
     B = ctx_lens.shape[0]
-    _tensor("new_lens", new_lens, i32, 1, (B,))
+    new = _vector("new_lens", new_lens, i32, B)
     _tensor("page_table", page_table, i32, 2)
-    _tensor("free_pages", free_pages, i32, 1)
-    _tensor("free_head", free_head, i32, 1, (1,))
+    free = _vector("free_pages", free_pages, i32)
+    head = _vector("free_head", free_head, i32, 1)
     if page_table.shape[0] != B:
         raise ValueError(f"page_table must have {B} rows, got {page_table.shape[0]}")
     if tokens < 0:
         raise ValueError("tokens must not be negative")
     stride = _table_stride(page_table)
-    _contiguous(ctx_lens=ctx_lens, new_lens=new_lens, free_pages=free_pages)
     if out is not None:
-        _tensor("out.cu_q", out.cu_q, i32, 1, (B + 1,))
-        _tensor("out.kv_lens", out.kv_lens, i32, 1, (B,))
-        _tensor("out.positions", out.positions, i32, 1, (tokens,))
-        _tensor("out.slots", out.slots, torch.int64, 1, (tokens,))
-        _tensor("out.state", out.state, i32, 1, (2,))
-        _contiguous(cu_q=out.cu_q, kv_lens=out.kv_lens, positions=out.positions, slots=out.slots, state=out.state)
+        _vector("out.cu_q", out.cu_q, i32, B + 1)
+        _vector("out.kv_lens", out.kv_lens, i32, B)
+        _vector("out.positions", out.positions, i32, tokens)
+        _vector("out.slots", out.slots, ty.i64, tokens)
+        _vector("out.state", out.state, i32, 2)
     dev = _on_device(ctx_lens, new_lens, page_table, free_pages, free_head, *(out or ()))
-    if out is None:
-        new = ctx_lens.new_empty
-        out = PagedPlan(new((B + 1,)), new((B,)), new((tokens,)), new((tokens,), dtype=torch.int64), new((2,)))
-    _check("tq_paged_plan", _lib.load().tq_paged_plan(
-        _ptr(ctx_lens), _ptr(new_lens), _ptr(page_table), stride, _ptr(free_pages), _ptr(free_head), B,
-        page_table.shape[1], free_pages.shape[0], tokens, page_size, _ptr(out.cu_q), _ptr(out.kv_lens),
-        _ptr(out.positions), _ptr(out.slots), _ptr(out.state), _stream(dev)))
+    if out is None:  # one allocation, the slots first: they are 8 bytes each
+        slots, cu_q, kv_lens, positions, state = ctx_lens.new_empty((2 * B + 3 * tokens + 3,)).split_with_sizes(
+            (2 * tokens, B + 1, B, tokens, 2))
+        out = PagedPlan(cu_q, kv_lens, positions, slots.view(ty.i64), state)
+    cu_q, kv_lens, positions, slots, state = out
+    status = _lib.load().tq_paged_plan(
+        ctx, new, page_table.data_ptr(), stride, free, head, B, page_table.shape[1], free_pages.shape[0], tokens, page_size,
+        cu_q.data_ptr(), kv_lens.data_ptr(), positions.data_ptr(), slots.data_ptr(), state.data_ptr(), ty.stream(dev))
+    if status:
+        _check("tq_paged_plan", status)
     return out
 
 
@@ -143,42 +184,46 @@ def tq_kv_append(q, k, v, k_cache, v_cache, slots, positions=None, rope=None, in
     positions int32 [T] and rope fp32 [rows, rot] (rot / 2 cosines, then
     rot / 2 sines) together, or neither: then nothing is rotated and the
     result is a copy of q.  out: where the rotated queries go, contiguous."""
-    import torch
-    stride = _cache(k_cache, v_cache)
+    ty = _types()
+    dt, stride = _cache(k_cache, v_cache)
     pages, Hkv, page, D = k_cache.shape
-    dt = k_cache.dtype
+    dtype = k_cache.dtype
     if k.dim() != 3:
         raise TypeError(f"k must be 3-D [T, {Hkv}, {D}], got {k.dim()}-D")
     T = k.shape[0]
-    kh, k_tok, k_head = _heads("k", k, dt, T, D)
-    vh, v_tok, v_head = _heads("v", v, dt, T, D)
+    kh, k_tok, k_head = _heads("k", k, dtype, T, D)
+    vh, v_tok, v_head = _heads("v", v, dtype, T, D)
     if kh != Hkv or vh != Hkv:
         raise ValueError(f"k and v must have the cache's {Hkv} heads, got {kh} and {vh}")
     Hq = q_tok = q_head = 0
     if q is not None:
-        Hq, q_tok, q_head = _heads("q", q, dt, T, D)
-    _tensor("slots", slots, torch.int64, 1, (T,))
+        Hq, q_tok, q_head = _heads("q", q, dtype, T, D)
+    at = _vector("slots", slots, ty.i64, T)
     if (rope is None) != (positions is None):
         raise ValueError("rope and positions come together")
-    rot = rows = 0
+    rot = rows = pos = angles = None
     if rope is not None:
-        _tensor("rope", rope, torch.float32, 2)
-        _tensor("positions", positions, torch.int32, 1, (T,))
+        _tensor("rope", rope, ty.f32, 2)
+        _contiguous("rope", rope)
+        pos = _vector("positions", positions, ty.i32, T)
+        angles = rope.data_ptr()
         rows, rot = rope.shape
         if rot > D or rot % 2:
             raise ValueError(f"rope must have an even number of columns, at most {D}, got {rot}")
     if out is not None:
         if q is None:
             raise ValueError("out needs q")
-        _tensor("out", out, dt, 3, (T, Hq, D))
-    _contiguous(slots=slots, positions=positions, rope=rope, out=out)
+        _tensor("out", out, dtype, 3, (T, Hq, D))
+        _contiguous("out", out)
     dev = _on_device(q, k, v, k_cache, v_cache, slots, positions, rope, out)
     if out is None and q is not None:
         out = q.new_empty((T, Hq, D))
-    _check("tq_kv_append", _lib.load().tq_kv_append(
-        _ptr(q), q_tok, q_head, _ptr(k), k_tok, k_head, _ptr(v), v_tok, v_head, _dtype_enum(k_cache), T, Hq, Hkv, D,
-        _ptr(k_cache), _ptr(v_cache), pages, page, stride, _ptr(slots), _ptr(positions), _ptr(rope), rows, rot,
-        1 if interleaved else 0, _ptr(out), _stream(dev)))
+    status = _lib.load().tq_kv_append(
+        None if q is None else q.data_ptr(), q_tok, q_head, k.data_ptr(), k_tok, k_head, v.data_ptr(), v_tok, v_head, dt, T,
+        Hq, Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(), pages, page, stride, at, pos, angles, rows or 0, rot or 0,
+        1 if interleaved else 0, None if out is None else out.data_ptr(), ty.stream(dev))
+    if status:
+        _check("tq_kv_append", status)
     return out
 
 
@@ -201,40 +246,41 @@ def tq_paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q: in
     scale: 1 / sqrt(D) by default; window, sinks: a token sees its last
     `window` keys (0: all) and the first `sinks`.  Causal in each request.
     workspace: as for tq_gemm ("auto", None or a contiguous device tensor)."""
-    import torch
-    stride = _cache(k_cache, v_cache)
+    ty = _types()
+    dt, stride = _cache(k_cache, v_cache)
     pages, Hkv, page, D = k_cache.shape
     if q.dim() != 3:
         raise TypeError(f"q must be 3-D [T, heads, {D}], got {q.dim()}-D")
     T = q.shape[0]
     Hq, q_tok, q_head = _heads("q", q, k_cache.dtype, T, D)
-    i32 = torch.int32
+    i32 = ty.i32
     _tensor("page_table", page_table, i32, 2)
     B, width = page_table.shape
-    _tensor("cu_q", cu_q, i32, 1, (B + 1,))
-    _tensor("kv_lens", kv_lens, i32, 1, (B,))
+    cu = _vector("cu_q", cu_q, i32, B + 1)
+    kv = _vector("kv_lens", kv_lens, i32, B)
     tab = _table_stride(page_table)
     if out is not None:
         _tensor("out", out, q.dtype, 3, (T, Hq, D))
-    _contiguous(cu_q=cu_q, kv_lens=kv_lens, out=out)
+        _contiguous("out", out)
     dev = _on_device(q, k_cache, v_cache, page_table, cu_q, kv_lens, out)
     lib = _lib.load()
     if out is None:
         out = q.new_empty((T, Hq, D))
-    lse = q.new_empty((T, Hq), dtype=torch.float32) if return_lse else None
+    lse = q.new_empty((T, Hq), dtype=ty.f32) if return_lse else None
     if isinstance(workspace, str):
         workspace = _lib.new_workspace(lib.tq_paged_attention_workspace_bytes(T, Hq, Hkv, D, B, max_q, max_kv, window,
-                                                                              sinks), dev)
-    nbytes = 0
+                                                                              sinks), q.device)
+    room = nbytes = 0
     if workspace is not None:
         _on_device(q, workspace)
-        _contiguous(workspace=workspace)
-        nbytes = workspace.numel() * workspace.element_size()
-    _check("tq_paged_attention", lib.tq_paged_attention(
-        _ptr(q), q_tok, q_head if Hq > 1 else 0, _dtype_enum(q), T, Hq, Hkv, D, _ptr(k_cache), _ptr(v_cache), pages, page, stride,
-        _ptr(page_table), tab, width, _ptr(cu_q), _ptr(kv_lens), B, max_q, max_kv,
-        D ** -0.5 if scale is None else scale, window, sinks, _ptr(out), _ptr(lse), _ptr(workspace), nbytes,
-        _stream(dev)))
+        _contiguous("workspace", workspace)
+        room, nbytes = workspace.data_ptr(), workspace.nbytes
+    status = lib.tq_paged_attention(
+        q.data_ptr(), q_tok, q_head if Hq > 1 else 0, dt, T, Hq, Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(), pages, page,
+        stride, page_table.data_ptr(), tab, width, cu, kv, B, max_q, max_kv, D ** -0.5 if scale is None else scale, window,
+        sinks, out.data_ptr(), None if lse is None else lse.data_ptr(), room, nbytes, ty.stream(dev))
+    if status:
+        _check("tq_paged_attention", status)
     return (out, lse) if return_lse else out
 
 
@@ -248,32 +294,33 @@ def tq_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, o
     for 1, 1, 0 and 0 (no cut); temperature 0 takes the best token.  A row
     without a logit above -inf gives token -1.  out: (tokens, logprobs) to
     write into."""
-    import torch
-    f32 = torch.float32
+    ty = _types()
+    f32 = ty.f32
     if logits.dim() != 2:
         raise TypeError(f"logits must be 2-D [B, V], got {logits.dim()}-D")
-    dt = _LOGITS.get(str(logits.dtype))
+    dt = ty.logits.get(logits.dtype)
     if dt is None:
         raise TypeError(f"logits must be float16, bfloat16 or float32, got {logits.dtype}")
     B, V = logits.shape
-    if V > 1 and logits.stride(1) != 1:
+    stride, one = logits.stride()
+    if one != 1 and V > 1:
         raise ValueError("the rows of logits must be contiguous")
-    stride = logits.stride(0) if B > 1 else V
+    if B <= 1:
+        stride = V
     if stride < V:
         raise ValueError("the rows of logits must not overlap")
-    _tensor("u", u, f32, 1, (B,))
-    for name, t, want in (("temperature", temperature, f32), ("top_k", top_k, torch.int32), ("top_p", top_p, f32),
-                          ("min_p", min_p, f32)):
-        if t is not None:
-            _tensor(name, t, want, 1, (B,))
+    at = _vector("u", u, f32, B)
+    t = None if temperature is None else _vector("temperature", temperature, f32, B)
+    k = None if top_k is None else _vector("top_k", top_k, ty.i32, B)
+    p = None if top_p is None else _vector("top_p", top_p, f32, B)
+    m = None if min_p is None else _vector("min_p", min_p, f32, B)
     if out is not None:
-        _tensor("tokens", out[0], torch.int32, 1, (B,))
-        _tensor("logprobs", out[1], f32, 1, (B,))
-        _contiguous(tokens=out[0], logprobs=out[1])
-    _contiguous(u=u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p)
+        _vector("tokens", out[0], ty.i32, B)
+        _vector("logprobs", out[1], f32, B)
     dev = _on_device(logits, u, temperature, top_k, top_p, min_p, *(out or ()))
-    tokens, logprobs = out or (u.new_empty((B,), dtype=torch.int32), u.new_empty((B,)))
-    _check("tq_sample", _lib.load().tq_sample(
-        _ptr(logits), dt, B, V, stride, _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
-        _ptr(tokens), _ptr(logprobs), _stream(dev)))
+    tokens, logprobs = out or (u.new_empty((B,), dtype=ty.i32), u.new_empty((B,)))
+    status = _lib.load().tq_sample(logits.data_ptr(), dt, B, V, stride, at, t, k, p, m, tokens.data_ptr(),
+                                   logprobs.data_ptr(), ty.stream(dev))
+    if status:
+        _check("tq_sample", status)
     return tokens, logprobs
