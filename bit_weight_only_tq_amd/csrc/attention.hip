@@ -62,6 +62,10 @@ __device__ __forceinline__ uint32_t nonfinite(uint32_t w) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// Page tables are read as constant memory, through the scalar cache: such loads
+// wait for no vector load or DMA in flight.
+typedef const __attribute__((address_space(4))) int32_t* const_i32;
+
 // One request as the kernels see it: its new tokens and the keys in reach of
 // its table.  A request whose offsets do not lie in [0, T] has no tokens.
 struct Request {
@@ -267,31 +271,49 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
     float m = -INFINITY, l = 0.f;
 
     const int i0 = split * per, i1 = min(bl.count, i0 + per);
-    const int32_t* trow = a.table + (int64_t)b * a.table_stride;
+    const const_i32 trow = (const_i32)(uintptr_t)(a.table + (int64_t)b * a.table_stride);
     const int last_key = rq.keys - 1;
+    const int page_mask = (1 << a.shift) - 1;
     const int kperm = 8 * (c >> 2) + (c & 3);  // key of tile t's row c: kperm + 4 t
-    if (tile_ok) {
-        for (int i = i0 + ks; i < i1; i += KS) {
-            const int key0 = bl.at(i) * kBlockKeys;
-            if (key0 > tile_p1) continue;
-            // pages: this lane's K rows lie in one page, its V rows in one page
-            const int kk = min(key0 + 8 * (c >> 2), last_key), kv = min(key0 + 8 * g, last_key);
-            const int idk = trow[kk >> a.shift], idv = trow[kv >> a.shift];
-            const bool okk = (uint32_t)idk < (uint32_t)a.pages, okv = (uint32_t)idv < (uint32_t)a.pages;
-            const int page_mask = (1 << a.shift) - 1;
-            const uint16_t* kbase = a.k + (int64_t)(okk ? idk : 0) * a.page_stride + ((int64_t)h << a.shift) * D + 8 * g;
-            const uint16_t* vbase = a.v + (int64_t)(okv ? idv : 0) * a.page_stride + ((int64_t)h << a.shift) * D + DV * c;
-            uint4 kf[2][ST];
+    // A block's two runs of 16 keys lie in a page each.  Page ids come through
+    // the scalar cache one block ahead; the K of the next block is loaded into
+    // the registers of this one's as soon as its scores are there, and V after
+    // the products, so that loads are in flight all the time.
+    struct Pages {
+        int lo, hi;
+    };
+    auto pages_at = [&](int i) {
+        const int key0 = bl.at(i < i1 ? i : i1 - 1) * kBlockKeys;
+        return Pages{trow[min(key0, last_key) >> a.shift], trow[min(key0 + 16, last_key) >> a.shift]};
+    };
+    auto there = [&](int id) { return (uint32_t)id < (uint32_t)a.pages; };
+    auto base_of = [&](int id) { return (int64_t)(there(id) ? id : 0) * a.page_stride + ((int64_t)h << a.shift) * D; };
+    uint4 kf[2][ST];
+    VRow<VD> vr[8];
+    auto load_k = [&](int key0, const Pages& pg) {
+        const uint16_t* kbase = a.k + (c >= 8 ? base_of(pg.hi) : base_of(pg.lo)) + 8 * g;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const uint16_t* p = kbase + (int64_t)((key0 + kperm + 4 * t) & page_mask) * D;
+        for (int t = 0; t < 2; ++t) {
+            const uint16_t* p = kbase + (uint32_t)(((key0 + kperm + 4 * t) & page_mask) * D);
 #pragma unroll
-                for (int s = 0; s < ST; ++s) kf[t][s] = *reinterpret_cast<const uint4*>(p + 32 * s);
-            }
-            VRow<VD> vr[8];
+            for (int s = 0; s < ST; ++s) kf[t][s] = *reinterpret_cast<const uint4*>(p + 32 * s);
+        }
+    };
+    auto load_v = [&](int key0, const Pages& pg) {
+        const uint16_t* vbase = a.v + (g >= 2 ? base_of(pg.hi) : base_of(pg.lo)) + DV * c + (uint32_t)(((key0 + 8 * g) & page_mask) * D);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) vr[e] = load_vrow<VD>(vbase + (int64_t)((key0 + 8 * g + e) & page_mask) * D);
-
+        for (int e = 0; e < 8; ++e) vr[e] = load_vrow<VD>(vbase + e * D);
+    };
+    if (tile_ok && i0 + ks < i1) {
+        int i = i0 + ks, key0 = bl.at(i) * kBlockKeys;
+        Pages now = pages_at(i);
+        load_k(key0, now);
+        load_v(key0, now);
+        Pages next = pages_at(i + KS);
+        for (;;) {
+            const bool more = i + KS < i1;
+            const int key1 = more ? bl.at(i + KS) * kBlockKeys : key0;
+            const bool okv = there(g >= 2 ? now.hi : now.lo);
             float t8[8];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -301,20 +323,21 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) t8[4 * t + r] = s4[r] * a.scale_log2;
             }
+            if (more) load_k(key1, next);
             // blocks that every row of the tile sees whole need no mask
             bool whole = key0 + kBlockKeys - 1 <= min(tile_p0, last_key);
             if (a.window > 0) whole = whole && (tile_p1 - key0 < a.window || key0 + kBlockKeys <= a.sinks);
-            const bool masked = !whole || __any(!okv);
+            const bool masked = !whole || !there(now.lo) || !there(now.hi);
             bool poisoned = false;
             if (masked) {
                 uint32_t bad = 0;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int j = key0 + 8 * g + e;
-                    const bool there = okv && j <= last_key;
-                    if (!there || !sees(a, my_pos, j)) t8[e] = -INFINITY;
+                    const bool held = okv && j <= last_key;
+                    if (!held || !sees(a, my_pos, j)) t8[e] = -INFINITY;
                     // a key that no row of the tile sees may hold anything
-                    const bool hidden = !there || j > tile_p1 ||
+                    const bool hidden = !held || j > tile_p1 ||
                                         (a.window > 0 && tile_p0 - j >= a.window && j >= a.sinks);
 #pragma unroll
                     for (int w = 0; w < VD; ++w) {
@@ -367,7 +390,7 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
                 // Lane (g, c) owns row c, values D / 4 g .. of V.
                 for (int gg = 0; gg < 4; ++gg) {
                     const int src = gg * 16;
-                    const int pid = __shfl(okv ? idv : -1, src, 64);
+                    const int pid = gg >= 2 ? now.hi : now.lo;
                     for (int e = 0; e < 8; ++e) {
                         const int j = key0 + 8 * gg + e;
                         float p = 0.f;
@@ -377,7 +400,7 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
                             const float got = __shfl(px, src + c, 64);
                             if (x == e) p = got;
                         }
-                        if (pid < 0 || j > last_key || !sees(a, my_pos, j)) continue;
+                        if (!there(pid) || j > last_key || !sees(a, my_pos, j)) continue;
                         const uint16_t* vp = a.v + (int64_t)pid * a.page_stride +
                                              (((int64_t)h << a.shift) + (j & page_mask)) * D + 4 * DV * g;
 #pragma unroll
@@ -390,6 +413,12 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
                     }
                 }
             }
+            if (!more) break;
+            load_v(key1, next);
+            i += KS;
+            key0 = key1;
+            now = next;
+            next = pages_at(i + KS);
         }
         l += __shfl_xor(l, 16, 64);
         l += __shfl_xor(l, 32, 64);
@@ -477,7 +506,6 @@ constexpr int kTileKeys = 64;
 constexpr int kTileRows = 128;
 constexpr int kTileThreads = 256;
 
-typedef const __attribute__((address_space(4))) int32_t* const_i32;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) char lds_char;
@@ -601,8 +629,6 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
     float m = -INFINITY, l = 0.f;
 
     const int i0 = split * per, i1 = min(bl.count, i0 + per);
-    // the table as constant memory: page ids come through the scalar cache and
-    // wait for no DMA in flight
     const const_i32 trow = (const_i32)(uintptr_t)(a.table + (int64_t)b * a.table_stride);
     const int last_key = rq.keys - 1;
     const int page_mask = (1 << a.shift) - 1;
@@ -900,11 +926,15 @@ constexpr int64_t kRowsMost = 64;
 namespace {
 
 // Splits of `blocks` key blocks: `per` blocks each, at least `least`, such
-// that `tiles` tiles make about `want` workgroups; at most `most` splits.
-int64_t split_keys(int64_t tiles, int64_t blocks, int64_t want, int64_t least, int64_t most, int64_t* per_out) {
+// that `tiles` tiles make about `want` workgroups, but no shorter than `full`
+// while there are more than `resident` of them; at most `most` splits.
+int64_t split_keys(int64_t tiles, int64_t blocks, int64_t want, int64_t resident, int64_t least, int64_t full, int64_t most,
+                   int64_t* per_out) {
     *per_out = blocks > 0 ? blocks : 1;
     if (tiles > kMaxFlags || blocks <= least) return 1;
     int64_t per = (tiles * blocks + want - 1) / want;
+    const int64_t one_round = (tiles * blocks + resident - 1) / resident;
+    if (per < full) per = one_round < full ? one_round : full;
     if (per < least) per = least;
     int64_t s = (blocks + per - 1) / per;
     if (s > most) s = most;
@@ -932,7 +962,8 @@ AttnPlan attn_plan(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int
         p.rows_most = B > 1 ? kRowsMost : 0;
         p.tiles = T * G / kTileRows + B;
         const int64_t blocks = (reach(kTileRows) + kTileKeys - 1) / kTileKeys;
-        p.tile_splits = split_keys(p.tiles * Hkv, blocks, compute_units * 4, 8, D == 128 ? 128 : 64, &p.tile_split_blocks);
+        p.tile_splits = split_keys(p.tiles * Hkv, blocks, compute_units * 4, compute_units * 2, 8, 16, D == 128 ? 128 : 64,
+                                   &p.tile_split_blocks);
         p.tile_slab = kTileRows * (D + 2);
         if (p.tile_splits > 1) bytes = (size_t)(p.tiles * Hkv * p.tile_splits * p.tile_slab) * 4;
         rows = kRowsMost;
@@ -945,7 +976,7 @@ AttnPlan attn_plan(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int
         const int64_t tiles = B * p.row_groups * Hkv;
         const int64_t blocks = (reach(16 * p.R) + kBlockKeys - 1) / kBlockKeys;
         // the join's weights: splits * rows <= 4096 floats of LDS
-        p.splits = split_keys(tiles, blocks, compute_units * 8, 8, 256 / p.R, &p.split_blocks);
+        p.splits = split_keys(tiles, blocks, compute_units * 16, compute_units * 2, 8, 32, 256 / p.R, &p.split_blocks);
         p.slab = (rows < 16 * p.R ? rows : 16 * p.R) * (D + 2);
         if (p.splits > 1) {
             const size_t need = (size_t)(tiles * p.splits * p.slab) * 4;
