@@ -1,4 +1,6 @@
-"""Build libtq.so (the HIP kernels and the C ABI) in-tree for gfx950.
+"""Build libtq.so (the HIP kernels and the C ABI) in-tree for gfx950, and
+_serving.so, the Python entry of its serving operators (host code only, built
+against the installed torch).
 
 Usage: python -m bit_weight_only_tq_amd.build  (or call ``build()``).
 
@@ -21,6 +23,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libtq.so")
+BINDING = os.path.join(HERE, "_serving.so")
 ARCH = "gfx950"
 
 SOURCES = {
@@ -41,6 +44,27 @@ def _hipcc():
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("hipcc not found (set HIPCC or install ROCm)")
+
+
+def _build_binding():
+    """Compile and link _serving.so beside libtq.so, which it needs."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"]]
+    for path in cpp_extension.include_paths() + [os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include")]:
+        cmd += ["-isystem", path]
+    tmp = BINDING + ".tmp"
+    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", HERE, "-l:libtq.so", "-L", lib, "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if r.returncode != 0:
+        raise RuntimeError(f"_serving build failed: {' '.join(cmd)}\n" + r.stdout.decode(errors="replace"))
+    os.replace(tmp, BINDING)
 
 
 def build(verbose: bool = False, jobs: int = 4) -> str:
@@ -76,6 +100,7 @@ def build(verbose: bool = False, jobs: int = 4) -> str:
         if r.returncode != 0:
             raise RuntimeError("libtq link failed:\n" + r.stdout.decode(errors="replace"))
         os.replace(tmp_lib, LIB)
+    _build_binding()
     return LIB
 
 
