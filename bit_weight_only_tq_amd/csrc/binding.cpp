@@ -144,6 +144,17 @@ Tensor fresh(at::IntArrayRef sizes, const Tensor& like, at::ScalarType type) {
     return at::empty(sizes, like.options().dtype(type));
 }
 
+// A vector of n entries at an offset of a buffer's storage: several outputs of
+// one allocation (an allocation costs 0.8 us, this 0.1).
+Tensor part_of(const Tensor& buffer, int64_t bytes_in, at::ScalarType type, int64_t n) {
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buffer.storage()), buffer.key_set(),
+                                                        c10::scalarTypeToTypeMeta(type));
+    const int64_t step = 1;
+    t.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef(&n, 1), at::IntArrayRef(&step, 1),
+                                                   bytes_in / (int64_t)c10::elementSize(type));
+    return t;
+}
+
 // A call's status as Python sees it: 0, or what _lib._check raises from.
 PyObject* with_status(tq_status st, PyObject* result) {
     if (st == TQ_OK) return result;
@@ -195,13 +206,17 @@ PyObject* paged_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
     }
     for (const Tensor* t : {&ctx, &fresh_lens, &table, &free, &head}) dev.take(*t);
-    for (int i = 0; i < 5; ++i) {
-        if (given) {
-            dev.take(out[i]);
-            continue;
+    if (given) {
+        for (const Tensor& t : out) dev.take(t);
+    } else {  // the slots first: they are 8 bytes each
+        const Tensor buffer = fresh({2 * B + 3 * tokens + 3}, ctx, at::kInt);
+        int64_t at = 0;
+        for (const int i : {3, 0, 1, 2, 4}) {
+            const at::ScalarType type = i == 3 ? at::kLong : at::kInt;
+            out[i] = part_of(buffer, at, type, sizes[i]);
+            p[i] = out[i].data_ptr();
+            at += sizes[i] * (int64_t)c10::elementSize(type);
         }
-        out[i] = fresh({sizes[i]}, ctx, i == 3 ? at::kLong : at::kInt);
-        p[i] = out[i].data_ptr();
     }
     const hipStream_t s = dev.stream();
     const tq_status st = call([&] {

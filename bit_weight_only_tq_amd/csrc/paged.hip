@@ -40,9 +40,9 @@ __device__ __forceinline__ int last_at_most(const int* a, int n, int x) {
 //
 // One launch.  Every workgroup scans all B requests by itself (2048 requests
 // are 16 KiB out of L2) rather than waiting for a scan kernel: a step this
-// small is bound by launches, not by bytes.  Workgroup 0 also writes the
+// small is bound by launches, not by bytes.  Workgroup 0 writes the
 // per-request outputs and counts the tokens left without a slot, by ranges of
-// tokens instead of token by token.
+// tokens instead of token by token; the others take the tokens.
 __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs a) {
     extern __shared__ int lds[];
     int* cu = lds;               // [B + 1]
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs a) {
     const int page = 1 << shift, T = a.T;
     // tokens: positions, slots, and the table entries of the pages they begin
     const int64_t span = max(T, total);
-    for (int64_t t64 = (int64_t)blockIdx.x * nthr + tid; t64 < span; t64 += (int64_t)gridDim.x * nthr) {
+    for (int64_t t64 = (int64_t)(blockIdx.x - 1) * nthr + tid; blockIdx.x > 0 && t64 < span; t64 += (int64_t)(gridDim.x - 1) * nthr) {
         const int t = (int)t64;
         int pos = 0;
         int64_t slot = -1;
@@ -359,7 +359,7 @@ hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t s) {
     // a small step is one small workgroup: its waves start and meet sooner
     const int threads = a.B <= 256 && a.T <= 256 ? 256 : 1024;
     const int64_t groups = ((int64_t)a.T + threads - 1) / threads;
-    const unsigned grid = (unsigned)(groups < 1 ? 1 : groups > 512 ? 512 : groups);
+    const unsigned grid = 1u + (unsigned)(groups < 1 ? 1 : groups > 512 ? 512 : groups);
     plan_kernel<<<dim3(grid), dim3(threads), lds, s>>>(a);
     return hipGetLastError();
 }
