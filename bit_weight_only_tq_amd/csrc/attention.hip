@@ -121,8 +121,9 @@ __device__ __forceinline__ bool sees(const AttnArgs& a, int p, int j) {
 //
 // Decode is bound by the read of the cache, so the waves of a workgroup take
 // different key blocks (R = 1), or different rows of the same keys (R = 2, 4
-// for requests with more rows), and the key axis is cut into `a.splits`
-// workgroups; the last one to finish joins the partial results in order.
+// for requests with more rows), and the blocks of all requests are dealt to
+// the workgroups in even shares; the last one to finish a request joins the
+// partial results in order.
 constexpr int kRowsThreads = 256;
 constexpr int kBlockKeys = 32;
 
@@ -154,24 +155,28 @@ __device__ __forceinline__ VRow<VD> load_vrow(const uint16_t* p) {
 // Joins the partial results of a workgroup tile's splits, in split order, by
 // the last workgroup to arrive (256 threads): weights of the splits from their
 // row statistics ([row][2] at the front of each slab), then the weighted sum
-// of their outputs ([row][D] from `out_at` on).  `wgt` has room for
-// rows * nsplit floats.
+// of their outputs ([row][D] from `out_at` on).  Split s lies at slabs.at(s).
+// `wgt` has room for rows * nsplit floats.
+struct Slabs {
+    const float *first, *base;
+    int64_t stride;
+    __device__ __forceinline__ const float* at(int s) const { return s == 0 ? first : base + s * stride; }
+};
 template <class E, int D>
 __device__ __forceinline__ void join_splits(const AttnArgs& a, const Request& rq, int h, int64_t row0, int rows, int out_at,
-                                            int64_t wg_tile, int nsplit, float* wgt, float* row_m, float* row_l) {
+                                            const Slabs& slabs, int nsplit, float* wgt, float* row_m, float* row_l) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, G = a.G;
-    const float* slabs = a.partials + wg_tile * a.splits * a.slab;
     for (int row = wave; row < rows; row += 4) {
         float M = -INFINITY;
         for (int s = lane; s < nsplit; s += 64)
-            M = fmaxf(M, __hip_atomic_load(slabs + s * a.slab + 2 * row, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+            M = fmaxf(M, __hip_atomic_load(slabs.at(s) + 2 * row, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
 #pragma unroll
         for (int x = 32; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor(M, x, 64));
         const float ms = M == -INFINITY ? 0.f : M;
         float L = 0.f;
         for (int s = lane; s < nsplit; s += 64) {
-            const float ps = __hip_atomic_load(slabs + s * a.slab + 2 * row, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            const float pl = __hip_atomic_load(slabs + s * a.slab + 2 * row + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            const float ps = __hip_atomic_load(slabs.at(s) + 2 * row, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            const float pl = __hip_atomic_load(slabs.at(s) + 2 * row + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             const float f = exp2_fast(ps - ms);
             wgt[row * nsplit + s] = f;
             L += f * pl;
@@ -186,13 +191,13 @@ __device__ __forceinline__ void join_splits(const AttnArgs& a, const Request& rq
     for (int u = tid; u < rows * (D / 2); u += kRowsThreads) {
         const int row = u / (D / 2), d = (u - row * (D / 2)) * 2;
         float x0 = 0.f, x1 = 0.f;
-        const float* base = slabs + out_at + row * D + d;
+        const int at_d = out_at + row * D + d;
         constexpr int RS = 8;  // splits in flight
         for (int s0 = 0; s0 < nsplit; s0 += RS) {
             uint64_t v[RS];
 #pragma unroll
             for (int s = 0; s < RS; ++s)
-                v[s] = __hip_atomic_load(reinterpret_cast<const uint64_t*>(base + (int64_t)min(s0 + s, nsplit - 1) * a.slab),
+                v[s] = __hip_atomic_load(reinterpret_cast<const uint64_t*>(slabs.at(min(s0 + s, nsplit - 1)) + at_d),
                                          __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
             for (int s = 0; s < RS; ++s)
@@ -212,6 +217,70 @@ __device__ __forceinline__ void join_splits(const AttnArgs& a, const Request& rq
     }
 }
 
+// Even shares: the requests' blocks lie one after another (start[b], start[B]
+// in all), and every workgroup of a KV head takes as many of them, so that one
+// round of workgroups ends together whatever the lengths.  -> blocks of a
+// share: kShareBlocks (one a wave) at least, and so many that no request has more than
+// a.split_most shares.  All threads of the workgroup.
+constexpr int kShareRequests = 1024;
+constexpr int kShareBlocks = 4;
+constexpr int kSplitBlocks = 8;  // calls whose requests have no more blocks are not shared out
+// x / y for x >= 0, y > 0; 64-bit division is a long loop, and seldom needed.
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
+    return (x | y) >> 32 == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
+template <class F>
+__device__ __forceinline__ int64_t even_shares(const AttnArgs& a, int64_t* start, int64_t* word, F blocks) {
+    __shared__ int64_t sums[4], most_of[4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const auto share_of = [&](int64_t total, int64_t most) {
+        const int64_t share = divide(total + a.workers - 1, a.workers);
+        return max(max(share, divide(most + a.split_most - 2, a.split_most - 1)), (int64_t)kShareBlocks);
+    };
+    if (a.B == 1) {  // nothing to add up
+        const int64_t n = blocks(0);
+        if (tid == 0) {
+            start[0] = 0;
+            start[1] = n;
+        }
+        __syncthreads();
+        return share_of(n, n);
+    }
+    const int per = (a.B + kRowsThreads - 1) / kRowsThreads, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    int64_t sum = 0, most = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int n = blocks(b);
+        start[b] = sum;  // from this thread's first on
+        sum += n;
+        most = max(most, (int64_t)n);
+    }
+    int64_t upto = sum;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int64_t o = __shfl_up((long long)upto, d, 64), x = __shfl_xor((long long)most, d, 64);
+        if (lane >= d) upto += o;
+        most = max(most, x);
+    }
+    if (lane == 63) {
+        sums[wave] = upto;
+        most_of[wave] = most;
+    }
+    __syncthreads();
+    int64_t before = upto - sum, total = 0;
+    for (int w = 0; w < 4; ++w) {
+        if (w < wave) before += sums[w];
+        total += sums[w];
+        most = max(most, most_of[w]);
+    }
+    for (int b = b0; b < b1; ++b) start[b] += before;
+    if (tid == 0) {
+        start[a.B] = total;
+        *word = share_of(total, most);
+    }
+    __syncthreads();
+    return *word;
+}
+
 template <class E, int D>
 __global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
     constexpr int ST = D / 32, DV = D / 16, VD = DV / 2;
@@ -220,266 +289,297 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
     __shared__ float lds_ml[4 * 16 * 2];
     __shared__ float row_m[64], row_l[64];
     __shared__ uint32_t word;
+    __shared__ int64_t start[kShareRequests + 1], share_word;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, c = lane & 15;
-    // workgroup -> KV head (fastest), split, row group, request
-    int64_t id = blockIdx.x;
-    const int h = (int)(id % a.Hkv);
-    id /= a.Hkv;
-    const int split = (int)(id % a.splits);
-    id /= a.splits;
-    const int rg = (int)(id % a.row_groups);
-    const int b = (int)(id / a.row_groups);
-    const Request rq = request_of(a, b);
     const int R = a.R, G = a.G;
-    const int64_t rows_all = (int64_t)min(rq.n, a.max_q) * G;
-    const int64_t row0 = (int64_t)rg * 16 * R;
-    if (row0 >= rows_all || rows_all > a.rows_most) return;
-    const int rows = (int)(rows_all - row0 < 16 * R ? rows_all - row0 : 16 * R);  // of this workgroup
-    // the keys any of its rows sees, cut into splits
-    const Blocks bl = blocks_of<5>(a, rq, rq.first + (int)(row0 / G), rq.first + (int)((row0 + rows - 1) / G));
-    int per = a.split_blocks;
-    if ((int64_t)per * a.splits < bl.count) per = (bl.count + a.splits - 1) / a.splits;
-    const int nsplit = bl.count > per ? (bl.count + per - 1) / per : 1;
-    if (split >= nsplit) return;
+    const int h = (int)(blockIdx.x % (unsigned)a.Hkv), worker = (int)(blockIdx.x / (unsigned)a.Hkv);
 
-    const int tile = wave % R, ks = wave / R, KS = 4 / R;
-    const int64_t my_row = row0 + tile * 16 + c;
-    const bool row_ok = my_row < rows_all;
-    const int my_tok = (int)((row_ok ? my_row : row0) / G);
-    const int my_head = h * G + (int)((row_ok ? my_row : row0) - (int64_t)my_tok * G);
-    const int my_pos = row_ok ? rq.first + my_tok : INT32_MIN;
-    // positions of the tile's first and last row
-    const int64_t last_row = row0 + tile * 16 + 15 < rows_all ? row0 + tile * 16 + 15 : rows_all - 1;
-    const int tile_p0 = rq.first + (int)((row0 + tile * 16) / G);
-    const int tile_p1 = rq.first + (int)(last_row / G);
-    const bool tile_ok = tile * 16 < rows;
+    // What request b asks of a KV head: its rows and the key blocks they see.
+    auto rows_of = [&](const Request& rq) {
+        const int64_t all = (int64_t)min(rq.n, a.max_q) * G;
+        return all > a.rows_most ? 0 : (int)all;  // the tile kernel's
+    };
+    auto seen_by = [&](const Request& rq, int rows) { return blocks_of<5>(a, rq, rq.first, rq.first + (rows - 1) / G); };
 
-    uint4 qf[ST];
-    {
-        const uint16_t* src = a.q + (int64_t)(rq.t0 + my_tok) * a.q_stride + my_head * a.q_head + 8 * g;
-#pragma unroll
-        for (int s = 0; s < ST; ++s) {
-            qf[s] = *reinterpret_cast<const uint4*>(src + 32 * s);
-            if (!row_ok) qf[s] = make_uint4(0, 0, 0, 0);
+    // This workgroup's run of blocks of all the requests' together, or all of one request's
+    int b = worker;
+    int64_t r0 = 0, r1 = 0, share = 1;
+    if (a.workers > 0) {
+        share = even_shares(a, start, &share_word, [&](int i) {
+            const Request rq = request_of(a, i);
+            const int rows = rows_of(rq);
+            return rows > 0 ? max(seen_by(rq, rows).count, 1) : 0;
+        });
+        r0 = worker * share;
+        r1 = min(start[a.B], r0 + share);
+        if (r0 >= r1) return;
+        int lo = 0, hi = a.B;  // the last request that begins at or before r0
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (start[mid] <= r0) lo = mid;
+            else hi = mid;
         }
+        b = lo;
     }
-    f32x4 o[DV];
-#pragma unroll
-    for (int j = 0; j < DV; ++j) o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, l = 0.f;
-
-    const int i0 = split * per, i1 = min(bl.count, i0 + per);
-    const const_i32 trow = (const_i32)(uintptr_t)(a.table + (int64_t)b * a.table_stride);
-    const int last_key = rq.keys - 1;
-    const int page_mask = (1 << a.shift) - 1;
-    const int kperm = 8 * (c >> 2) + (c & 3);  // key of tile t's row c: kperm + 4 t
-    // A block's two runs of 16 keys lie in a page each.  Page ids come through
-    // the scalar cache one block ahead; the K of the next block is loaded into
-    // the registers of this one's as soon as its scores are there, and V after
-    // the products, so that loads are in flight all the time.
-    struct Pages {
-        int lo, hi;
-    };
-    auto pages_at = [&](int i) {
-        const int key0 = bl.at(i < i1 ? i : i1 - 1) * kBlockKeys;
-        return Pages{trow[min(key0, last_key) >> a.shift], trow[min(key0 + 16, last_key) >> a.shift]};
-    };
-    auto there = [&](int id) { return (uint32_t)id < (uint32_t)a.pages; };
-    auto base_of = [&](int id) { return (int64_t)(there(id) ? id : 0) * a.page_stride + ((int64_t)h << a.shift) * D; };
-    uint4 kf[2][ST];
-    VRow<VD> vr[8];
-    auto load_k = [&](int key0, const Pages& pg) {
-        const uint16_t* kbase = a.k + (c >= 8 ? base_of(pg.hi) : base_of(pg.lo)) + 8 * g;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const uint16_t* p = kbase + (uint32_t)(((key0 + kperm + 4 * t) & page_mask) * D);
-#pragma unroll
-            for (int s = 0; s < ST; ++s) kf[t][s] = *reinterpret_cast<const uint4*>(p + 32 * s);
+    for (;; ++b) {
+        if (a.workers > 0 && (b >= a.B || start[b] >= r1)) return;
+        const Request rq = request_of(a, b);
+        const int rows = rows_of(rq);
+        if (rows == 0) {
+            if (a.workers > 0) continue;
+            return;
         }
-    };
-    auto load_v = [&](int key0, const Pages& pg) {
-        const uint16_t* vbase = a.v + (g >= 2 ? base_of(pg.hi) : base_of(pg.lo)) + DV * c + (uint32_t)(((key0 + 8 * g) & page_mask) * D);
+        const Blocks bl = seen_by(rq, rows);
+        int i0 = 0, i1 = bl.count, nsplit = 1;
+        float* slab = nullptr;  // this split's partial result: [rows][2], then [rows][D]
+        Slabs slabs{nullptr, nullptr, 0};
+        if (a.workers > 0) {
+            // A workgroup has at most two partial results: of the request its
+            // run begins in, and of the one it ends in.
+            const int64_t s0 = start[b], s1 = start[b + 1];
+            i0 = (int)(max(r0, s0) - s0);
+            i1 = min(bl.count, (int)(min(r1, s1) - s0));
+            const int first = (int)divide(s0, share);
+            nsplit = (int)divide(s1 - 1, share) - first + 1;
+            auto slab_of = [&](int w, int which) { return a.partials + (((int64_t)w * a.Hkv + h) * 2 + which) * a.slab; };
+            slab = slab_of(worker, s0 <= r0 ? 0 : 1);
+            slabs = Slabs{slab_of(first, s0 > first * share ? 1 : 0), slab_of(first, 0), (int64_t)a.Hkv * 2 * a.slab};
+        }
+
+        const int tile = wave % R, ks = wave / R, KS = 4 / R;
+        const int my_row = tile * 16 + c;
+        const bool row_ok = my_row < rows;
+        const int my_tok = (row_ok ? my_row : 0) / G;
+        const int my_head = h * G + (row_ok ? my_row : 0) - my_tok * G;
+        const int my_pos = row_ok ? rq.first + my_tok : INT32_MIN;
+        // positions of the tile's first and last row
+        const int tile_p0 = rq.first + tile * 16 / G;
+        const int tile_p1 = rq.first + min(tile * 16 + 15, rows - 1) / G;
+        const bool tile_ok = tile * 16 < rows;
+
+        uint4 qf[ST];
+        {
+            const uint16_t* src = a.q + (int64_t)(rq.t0 + my_tok) * a.q_stride + my_head * a.q_head + 8 * g;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) vr[e] = load_vrow<VD>(vbase + e * D);
-    };
-    if (tile_ok && i0 + ks < i1) {
-        int i = i0 + ks, key0 = bl.at(i) * kBlockKeys;
-        Pages now = pages_at(i);
-        load_k(key0, now);
-        load_v(key0, now);
-        Pages next = pages_at(i + KS);
-        for (;;) {
-            const bool more = i + KS < i1;
-            const int key1 = more ? bl.at(i + KS) * kBlockKeys : key0;
-            const bool okv = there(g >= 2 ? now.hi : now.lo);
-            float t8[8];
+            for (int s = 0; s < ST; ++s) {
+                qf[s] = *reinterpret_cast<const uint4*>(src + 32 * s);
+                if (!row_ok) qf[s] = make_uint4(0, 0, 0, 0);
+            }
+        }
+        f32x4 o[DV];
+#pragma unroll
+        for (int j = 0; j < DV; ++j) o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        float m = -INFINITY, l = 0.f;
+
+        const const_i32 trow = (const_i32)(uintptr_t)(a.table + (int64_t)b * a.table_stride);
+        const int last_key = rq.keys - 1;
+        const int page_mask = (1 << a.shift) - 1;
+        const int kperm = 8 * (c >> 2) + (c & 3);  // key of tile t's row c: kperm + 4 t
+        // A block's two runs of 16 keys lie in a page each.  Page ids come through
+        // the scalar cache one block ahead; the K of the next block is loaded into
+        // the registers of this one's as soon as its scores are there, and V after
+        // the products, so that loads are in flight all the time.
+        struct Pages {
+            int lo, hi;
+        };
+        auto pages_at = [&](int i) {
+            const int key0 = bl.at(i < i1 ? i : i1 - 1) * kBlockKeys;
+            return Pages{trow[min(key0, last_key) >> a.shift], trow[min(key0 + 16, last_key) >> a.shift]};
+        };
+        auto there = [&](int id) { return (uint32_t)id < (uint32_t)a.pages; };
+        auto base_of = [&](int id) { return (int64_t)(there(id) ? id : 0) * a.page_stride + ((int64_t)h << a.shift) * D; };
+        uint4 kf[2][ST];
+        VRow<VD> vr[8];
+        auto load_k = [&](int key0, const Pages& pg) {
+            const uint16_t* kbase = a.k + (c >= 8 ? base_of(pg.hi) : base_of(pg.lo)) + 8 * g;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                f32x4 s4 = f32x4{0.f, 0.f, 0.f, 0.f};
+                const uint16_t* p = kbase + (uint32_t)(((key0 + kperm + 4 * t) & page_mask) * D);
 #pragma unroll
-                for (int s = 0; s < ST; ++s) s4 = E::mfma16(kf[t][s], qf[s], s4);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) t8[4 * t + r] = s4[r] * a.scale_log2;
+                for (int s = 0; s < ST; ++s) kf[t][s] = *reinterpret_cast<const uint4*>(p + 32 * s);
             }
-            if (more) load_k(key1, next);
-            // blocks that every row of the tile sees whole need no mask
-            bool whole = key0 + kBlockKeys - 1 <= min(tile_p0, last_key);
-            if (a.window > 0) whole = whole && (tile_p1 - key0 < a.window || key0 + kBlockKeys <= a.sinks);
-            const bool masked = !whole || !there(now.lo) || !there(now.hi);
-            bool poisoned = false;
-            if (masked) {
-                uint32_t bad = 0;
+        };
+        auto load_v = [&](int key0, const Pages& pg) {
+            const uint16_t* vbase = a.v + (g >= 2 ? base_of(pg.hi) : base_of(pg.lo)) + DV * c + (uint32_t)(((key0 + 8 * g) & page_mask) * D);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int j = key0 + 8 * g + e;
-                    const bool held = okv && j <= last_key;
-                    if (!held || !sees(a, my_pos, j)) t8[e] = -INFINITY;
-                    // a key that no row of the tile sees may hold anything
-                    const bool hidden = !held || j > tile_p1 ||
-                                        (a.window > 0 && tile_p0 - j >= a.window && j >= a.sinks);
+            for (int e = 0; e < 8; ++e) vr[e] = load_vrow<VD>(vbase + e * D);
+        };
+        if (tile_ok && i0 + ks < i1) {
+            int i = i0 + ks, key0 = bl.at(i) * kBlockKeys;
+            Pages now = pages_at(i);
+            load_k(key0, now);
+            load_v(key0, now);
+            Pages next = pages_at(i + KS);
+            for (;;) {
+                const bool more = i + KS < i1;
+                const int key1 = more ? bl.at(i + KS) * kBlockKeys : key0;
+                const bool okv = there(g >= 2 ? now.hi : now.lo);
+                float t8[8];
 #pragma unroll
-                    for (int w = 0; w < VD; ++w) {
-                        if (hidden) vr[e].w[w] = 0;
-                        bad |= nonfinite<E>(vr[e].w[w]);
+                for (int t = 0; t < 2; ++t) {
+                    f32x4 s4 = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int s = 0; s < ST; ++s) s4 = E::mfma16(kf[t][s], qf[s], s4);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) t8[4 * t + r] = s4[r] * a.scale_log2;
+                }
+                if (more) load_k(key1, next);
+                // blocks that every row of the tile sees whole need no mask
+                bool whole = key0 + kBlockKeys - 1 <= min(tile_p0, last_key);
+                if (a.window > 0) whole = whole && (tile_p1 - key0 < a.window || key0 + kBlockKeys <= a.sinks);
+                const bool masked = !whole || !there(now.lo) || !there(now.hi);
+                bool poisoned = false;
+                if (masked) {
+                    uint32_t bad = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int j = key0 + 8 * g + e;
+                        const bool held = okv && j <= last_key;
+                        if (!held || !sees(a, my_pos, j)) t8[e] = -INFINITY;
+                        // a key that no row of the tile sees may hold anything
+                        const bool hidden = !held || j > tile_p1 ||
+                                            (a.window > 0 && tile_p0 - j >= a.window && j >= a.sinks);
+#pragma unroll
+                        for (int w = 0; w < VD; ++w) {
+                            if (hidden) vr[e].w[w] = 0;
+                            bad |= nonfinite<E>(vr[e].w[w]);
+                        }
+                    }
+                    poisoned = __any(bad != 0);
+                }
+                // running maximum, shared by the four lanes of a row; raised only
+                // when a score passes it by more than 2^8, so that most blocks
+                // rescale nothing (weights up to 256 fit both 16-bit types)
+                float mx = t8[0];
+#pragma unroll
+                for (int e = 1; e < 8; ++e) mx = fmaxf(mx, t8[e]);
+                if (__any(mx > m + 8.f)) {
+                    mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+                    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+                    const float mn = fmaxf(m, mx);
+                    const float f = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
+                    m = mn;
+                    l *= f;
+#pragma unroll
+                    for (int j = 0; j < DV; ++j) o[j] *= f;
+                }
+                const float ms = m == -INFINITY ? 0.f : m;
+                uint32_t pw[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float p0 = exp2_fast(t8[2 * e] - ms), p1 = exp2_fast(t8[2 * e + 1] - ms);
+                    l += p0 + p1;
+                    pw[e] = E::pack2(p0, p1);
+                }
+                if (!poisoned) {
+                    const uint4 pf = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+#pragma unroll
+                    for (int j = 0; j < DV; ++j) {
+                        const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
+                        uint4 vf;
+                        vf.x = __builtin_amdgcn_perm(vr[1].w[j / 2], vr[0].w[j / 2], sel);
+                        vf.y = __builtin_amdgcn_perm(vr[3].w[j / 2], vr[2].w[j / 2], sel);
+                        vf.z = __builtin_amdgcn_perm(vr[5].w[j / 2], vr[4].w[j / 2], sel);
+                        vf.w = __builtin_amdgcn_perm(vr[7].w[j / 2], vr[6].w[j / 2], sel);
+                        o[j] = E::mfma16(vf, pf, o[j]);
+                    }
+                } else {
+                    // A value that some rows see and others do not is not finite:
+                    // 0 times it would spoil the rows it is hidden from, so the
+                    // block is added key by key, to the rows that see each.
+                    // Lane (g, c) owns row c, values D / 4 g .. of V.
+                    for (int gg = 0; gg < 4; ++gg) {
+                        const int src = gg * 16;
+                        const int pid = gg >= 2 ? now.hi : now.lo;
+                        for (int e = 0; e < 8; ++e) {
+                            const int j = key0 + 8 * gg + e;
+                            float p = 0.f;
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {
+                                const float px = (x & 1) ? E::hi(pw[x / 2]) : E::lo(pw[x / 2]);
+                                const float got = __shfl(px, src + c, 64);
+                                if (x == e) p = got;
+                            }
+                            if (!there(pid) || j > last_key || !sees(a, my_pos, j)) continue;
+                            const uint16_t* vp = a.v + (int64_t)pid * a.page_stride +
+                                                 (((int64_t)h << a.shift) + (j & page_mask)) * D + 4 * DV * g;
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                                for (int jj = 0; jj < DV; ++jj) {
+                                    const uint32_t w = vp[DV * r + jj];
+                                    o[jj][r] = fmaf(p, E::lo(w), o[jj][r]);
+                                }
+                        }
                     }
                 }
-                poisoned = __any(bad != 0);
+                if (!more) break;
+                load_v(key1, next);
+                i += KS;
+                key0 = key1;
+                now = next;
+                next = pages_at(i + KS);
             }
-            // running maximum, shared by the four lanes of a row; raised only
-            // when a score passes it by more than 2^8, so that most blocks
-            // rescale nothing (weights up to 256 fit both 16-bit types)
-            float mx = t8[0];
+            l += __shfl_xor(l, 16, 64);
+            l += __shfl_xor(l, 32, 64);
+        }
+
+        // join the waves of each tile
+        {
+            float* dst = lds_o + (wave * 16 + c) * LD + 4 * DV * g;
 #pragma unroll
-            for (int e = 1; e < 8; ++e) mx = fmaxf(mx, t8[e]);
-            if (__any(mx > m + 8.f)) {
-                mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-                mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-                const float mn = fmaxf(m, mx);
-                const float f = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
-                m = mn;
-                l *= f;
+            for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int j = 0; j < DV; ++j) o[j] *= f;
+                for (int j = 0; j < DV; j += 4)
+                    *reinterpret_cast<float4*>(dst + DV * r + j) = make_float4(o[j][r], o[j + 1][r], o[j + 2][r], o[j + 3][r]);
+            if (g == 0) {
+                lds_ml[(wave * 16 + c) * 2] = m;
+                lds_ml[(wave * 16 + c) * 2 + 1] = l;
             }
-            const float ms = m == -INFINITY ? 0.f : m;
-            uint32_t pw[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float p0 = exp2_fast(t8[2 * e] - ms), p1 = exp2_fast(t8[2 * e + 1] - ms);
-                l += p0 + p1;
-                pw[e] = E::pack2(p0, p1);
+        }
+        __syncthreads();
+        const bool parts = nsplit > 1;
+        constexpr int EPT = 4;                                             // values a thread joins at a time
+        for (int u = tid; u < rows * (D / EPT); u += kRowsThreads) {
+            const int row = u / (D / EPT), d = (u - row * (D / EPT)) * EPT;
+            const int tl = row >> 4, rr = row & 15;
+            float M = -INFINITY, L = 0.f;
+            for (int w = 0; w < KS; ++w) M = fmaxf(M, lds_ml[((w * R + tl) * 16 + rr) * 2]);
+            const float ms = M == -INFINITY ? 0.f : M;
+            float acc[EPT] = {0.f, 0.f, 0.f, 0.f};
+            for (int w = 0; w < KS; ++w) {
+                const int base = (w * R + tl) * 16 + rr;
+                const float f = exp2_fast(lds_ml[base * 2] - ms);
+                L += f * lds_ml[base * 2 + 1];
+                const float4 x = *reinterpret_cast<const float4*>(lds_o + base * LD + d);
+                acc[0] += f * x.x;
+                acc[1] += f * x.y;
+                acc[2] += f * x.z;
+                acc[3] += f * x.w;
             }
-            if (!poisoned) {
-                const uint4 pf = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+            if (parts) {
 #pragma unroll
-                for (int j = 0; j < DV; ++j) {
-                    const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
-                    uint4 vf;
-                    vf.x = __builtin_amdgcn_perm(vr[1].w[j / 2], vr[0].w[j / 2], sel);
-                    vf.y = __builtin_amdgcn_perm(vr[3].w[j / 2], vr[2].w[j / 2], sel);
-                    vf.z = __builtin_amdgcn_perm(vr[5].w[j / 2], vr[4].w[j / 2], sel);
-                    vf.w = __builtin_amdgcn_perm(vr[7].w[j / 2], vr[6].w[j / 2], sel);
-                    o[j] = E::mfma16(vf, pf, o[j]);
+                for (int e = 0; e < EPT; ++e) store_partial(slab + 2 * rows + row * D + d + e, acc[e]);
+                if (d == 0) {
+                    store_partial(slab + 2 * row, M);
+                    store_partial(slab + 2 * row + 1, L);
                 }
             } else {
-                // A value that some rows see and others do not is not finite:
-                // 0 times it would spoil the rows it is hidden from, so the
-                // block is added key by key, to the rows that see each.
-                // Lane (g, c) owns row c, values D / 4 g .. of V.
-                for (int gg = 0; gg < 4; ++gg) {
-                    const int src = gg * 16;
-                    const int pid = gg >= 2 ? now.hi : now.lo;
-                    for (int e = 0; e < 8; ++e) {
-                        const int j = key0 + 8 * gg + e;
-                        float p = 0.f;
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            const float px = (x & 1) ? E::hi(pw[x / 2]) : E::lo(pw[x / 2]);
-                            const float got = __shfl(px, src + c, 64);
-                            if (x == e) p = got;
-                        }
-                        if (!there(pid) || j > last_key || !sees(a, my_pos, j)) continue;
-                        const uint16_t* vp = a.v + (int64_t)pid * a.page_stride +
-                                             (((int64_t)h << a.shift) + (j & page_mask)) * D + 4 * DV * g;
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-#pragma unroll
-                            for (int jj = 0; jj < DV; ++jj) {
-                                const uint32_t w = vp[DV * r + jj];
-                                o[jj][r] = fmaf(p, E::lo(w), o[jj][r]);
-                            }
-                    }
-                }
+                const int tok = row / G;
+                const int64_t at = (int64_t)(rq.t0 + tok) * a.Hq + h * G + row - tok * G;
+                const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN);
+                *reinterpret_cast<uint2*>(a.out + at * D + d) =
+                    make_uint2(E::pack2(acc[0] * inv, acc[1] * inv), E::pack2(acc[2] * inv, acc[3] * inv));
+                if (d == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : kLn2 * (M + log2f(L));
             }
-            if (!more) break;
-            load_v(key1, next);
-            i += KS;
-            key0 = key1;
-            now = next;
-            next = pages_at(i + KS);
         }
-        l += __shfl_xor(l, 16, 64);
-        l += __shfl_xor(l, 32, 64);
+        if (parts && split_last_arrival(a.flags, (uint32_t)(b * a.Hkv + h), nsplit, &word))
+            join_splits<E, D>(a, rq, h, 0, rows, 2 * rows, slabs, nsplit, lds_o, row_m, row_l);
+        if (a.workers == 0) return;
+        __syncthreads();  // LDS is the next request's
     }
-
-    // join the waves of each tile
-    {
-        float* dst = lds_o + (wave * 16 + c) * LD + 4 * DV * g;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int j = 0; j < DV; j += 4)
-                *reinterpret_cast<float4*>(dst + DV * r + j) = make_float4(o[j][r], o[j + 1][r], o[j + 2][r], o[j + 3][r]);
-        if (g == 0) {
-            lds_ml[(wave * 16 + c) * 2] = m;
-            lds_ml[(wave * 16 + c) * 2 + 1] = l;
-        }
-    }
-    __syncthreads();
-    const bool parts = nsplit > 1;
-    const int64_t wg_tile = ((int64_t)b * a.row_groups + rg) * a.Hkv + h;
-    float* slab = a.partials + (wg_tile * a.splits + split) * a.slab;  // [rows][2], then [rows][D]
-    constexpr int EPT = 4;                                             // values a thread joins at a time
-    for (int u = tid; u < rows * (D / EPT); u += kRowsThreads) {
-        const int row = u / (D / EPT), d = (u - row * (D / EPT)) * EPT;
-        const int tl = row >> 4, rr = row & 15;
-        float M = -INFINITY, L = 0.f;
-        for (int w = 0; w < KS; ++w) M = fmaxf(M, lds_ml[((w * R + tl) * 16 + rr) * 2]);
-        const float ms = M == -INFINITY ? 0.f : M;
-        float acc[EPT] = {0.f, 0.f, 0.f, 0.f};
-        for (int w = 0; w < KS; ++w) {
-            const int base = (w * R + tl) * 16 + rr;
-            const float f = exp2_fast(lds_ml[base * 2] - ms);
-            L += f * lds_ml[base * 2 + 1];
-            const float4 x = *reinterpret_cast<const float4*>(lds_o + base * LD + d);
-            acc[0] += f * x.x;
-            acc[1] += f * x.y;
-            acc[2] += f * x.z;
-            acc[3] += f * x.w;
-        }
-        if (parts) {
-#pragma unroll
-            for (int e = 0; e < EPT; ++e) store_partial(slab + 2 * rows + row * D + d + e, acc[e]);
-            if (d == 0) {
-                store_partial(slab + 2 * row, M);
-                store_partial(slab + 2 * row + 1, L);
-            }
-        } else {
-            const int64_t r = row0 + row;
-            const int tok = (int)(r / G);
-            const int64_t at = (int64_t)(rq.t0 + tok) * a.Hq + h * G + (int)(r - (int64_t)tok * G);
-            const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN);
-            *reinterpret_cast<uint2*>(a.out + at * D + d) =
-                make_uint2(E::pack2(acc[0] * inv, acc[1] * inv), E::pack2(acc[2] * inv, acc[3] * inv));
-            if (d == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : kLn2 * (M + log2f(L));
-        }
-    }
-    if (!parts) return;
-    if (!split_last_arrival(a.flags, (uint32_t)wg_tile, nsplit, &word)) return;
-
-    join_splits<E, D>(a, rq, h, row0, rows, 2 * rows, wg_tile, nsplit, lds_o, row_m, row_l);
 }
 
 // ---- tile kernel: 32 rows a wave, 128 a workgroup, keys in tiles of 64.
@@ -902,7 +1002,9 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
             for (int r = 0; r < 16; ++r) store_partial(dst + 32 * d + 8 * (r >> 2) + (r & 3), o[d][r]);
     }
     if (!split_last_arrival(a.flags, (uint32_t)wg_tile, nsplit, &ctrl[2])) return;
-    join_splits<E, D>(a, rq, h, row0, rows, 2 * kTileRows, wg_tile, nsplit, reinterpret_cast<float*>(smem_tile), row_m, row_l);
+    const float* slabs = a.partials + wg_tile * a.splits * a.slab;
+    join_splits<E, D>(a, rq, h, row0, rows, 2 * kTileRows, Slabs{slabs, slabs, a.slab}, nsplit,
+                      reinterpret_cast<float*>(smem_tile), row_m, row_l);
 }
 
 }  // namespace
@@ -914,10 +1016,10 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
 // may be of both kinds launches both, one request alone the one it needs.
 //
 // Rows kernel: row tiles a workgroup holds: as many as its largest request
-// needs, up to 4 (its waves then share the keys).  The key axis is split
-// until the grid has about 8 workgroups a compute unit (lengths are ragged,
-// and short splits even them out), but no split is shorter than 8 blocks:
-// below that its partial results cost more than its keys.
+// needs, up to 4 (its waves then share the keys).  With a workspace, the two
+// workgroups a compute unit holds take even shares of all blocks, 4 at least (a
+// block a wave).  Without one, or where
+// the requests are more than the counters, a request is one workgroup's.
 //
 // Tile kernel: split until the grid has about 4 workgroups a compute unit (two
 // are resident), no split shorter than 8 tiles.
@@ -972,14 +1074,14 @@ AttnPlan attn_plan(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int
     }
     if (p.rows_most > 0) {
         p.R = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-        p.row_groups = (rows + 16 * p.R - 1) / (16 * p.R);
-        const int64_t tiles = B * p.row_groups * Hkv;
-        const int64_t blocks = (reach(16 * p.R) + kBlockKeys - 1) / kBlockKeys;
-        // the join's weights: splits * rows <= 4096 floats of LDS
-        p.splits = split_keys(tiles, blocks, compute_units * 16, compute_units * 2, 8, 32, 256 / p.R, &p.split_blocks);
-        p.slab = (rows < 16 * p.R ? rows : 16 * p.R) * (D + 2);
-        if (p.splits > 1) {
-            const size_t need = (size_t)(tiles * p.splits * p.slab) * 4;
+        p.slab = rows * (D + 2);
+        const int64_t blocks = (reach(rows) + kBlockKeys - 1) / kBlockKeys;
+        p.split_most = 4096 / (16 * p.R);  // the join's weights: splits * rows <= 4096 floats of LDS
+        int64_t w = B * blocks / kShareBlocks + 1;
+        if (w > 2 * compute_units / Hkv) w = 2 * compute_units / Hkv;
+        if (w > 1 && blocks > kSplitBlocks && B <= kShareRequests && B * Hkv <= kMaxFlags) {
+            p.workers = w;
+            const size_t need = (size_t)(w * Hkv * 2 * p.slab) * 4;
             if (need > bytes) bytes = need;
         }
     }
@@ -1023,11 +1125,10 @@ hipError_t launch_attention(const AttnArgs& args, const AttnPlan& plan, hipStrea
     }
     if (plan.rows_most == 0) return hipSuccess;
     a.R = plan.R;
-    a.row_groups = (int)plan.row_groups;
-    a.splits = a.partials ? (int)plan.splits : 1;
-    a.split_blocks = (int)plan.split_blocks;
+    a.workers = a.partials ? (int)plan.workers : 0;
+    a.split_most = (int)plan.split_most;
     a.slab = plan.slab;
-    const int64_t grid = (int64_t)a.B * plan.row_groups * a.splits * a.Hkv;
+    const int64_t grid = (a.workers > 0 ? a.workers : (int64_t)a.B) * a.Hkv;
     if (grid <= 0 || grid > 0x7FFFFFFF) return hipErrorInvalidValue;
     const unsigned gd = (unsigned)grid;
     if (a.bf16) return a.D == 64 ? launch_rows<AttnBF16, 64>(a, gd, s) : launch_rows<AttnBF16, 128>(a, gd, s);

@@ -206,7 +206,8 @@ struct AttnArgs {
     uint32_t* flags;
     int64_t rows_most;  // requests of more rows are the tile kernel's
     int64_t tiles;      // of the tile kernel, with room for every request's last
-    int R, row_groups, splits, split_blocks;
+    int splits, split_blocks;  // tile kernel
+    int R, workers, split_most;  // rows kernel
     int64_t slab;
 };
 struct AttnPlan {
@@ -218,10 +219,9 @@ struct AttnPlan {
     // rows kernel
     int64_t rows_most;    // 0: not launched
     int R;                // 16-row tiles a workgroup holds
-    int64_t row_groups;   // workgroups over the rows of the largest request
-    int64_t splits;       // workgroups over its keys
-    int64_t split_blocks; // key blocks of a split
-    int64_t slab;         // floats of one split's partial result
+    int64_t workers;      // workgroups of a KV head that take even shares (0: one a request)
+    int64_t split_most;   // shares of one request, at most
+    int64_t slab;         // floats of a partial result
     size_t data_bytes;    // partial results of the call
 };
 AttnPlan attn_plan(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q, int64_t max_kv, int64_t window,
