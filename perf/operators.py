@@ -238,8 +238,8 @@ def _own(s, op):
         return {"table": s["table"], "cu_q": r.cu_q, "kv_lens": r.kv_lens, "positions": r.positions, "slots": r.slots,
                 "state": r.state}
     if op == "append":
-        q = tq.tq_kv_append(s["q"], s["k"], s["v"], s["kc"], s["vc"], s["slots"], positions=s["pos"], rope=s["rope"],
-                            interleaved=s["interleaved"])
+        q = tq.tq_kv_append(s["q"], s["k"], s["v"], s["kc"], s["vc"], s["slots"], rope=s["rope"],
+                            positions=None if s["rope"] is None else s["pos"], interleaved=s["interleaved"])
         return {"q": q, "k_cache": s["kc"], "v_cache": s["vc"]}
     if op == "attend":
         out, lse = tq.tq_paged_attention(s["q"], s["kc"], s["vc"], s["table"], s["cu"], s["kv"], max(s["qn"]),
