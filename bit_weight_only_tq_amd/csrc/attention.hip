@@ -14,6 +14,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "tq_device.h"
 #include "tq_internal.h"
 
@@ -120,11 +122,15 @@ __device__ __forceinline__ bool sees(const AttnArgs& a, int p, int j) {
 // Row statistics and outputs of a row stay in the lanes of that row.
 //
 // Decode is bound by the read of the cache, so the waves of a workgroup take
-// different key blocks (R = 1), or different rows of the same keys (R = 2, 4
-// for requests with more rows), and the blocks of all requests are dealt to
-// the workgroups in even shares; the last one to finish a request joins the
-// partial results in order.
+// different key blocks, and the blocks of all requests are dealt to the
+// workgroups in even shares; the last one to finish a request joins the partial
+// results in order.  64 requests of 33 to 8191 keys with 64 + 8 heads of 128:
+// 200 us, 5.4 TB/s of cache; two of 100001 and 131071 keys with 32 + 8 heads:
+// 170 us, 5.6 TB/s (a streaming read reaches as much).  The same with splits of
+// a fixed length, whose workgroups came in rounds: 226 and 187 us.
 constexpr int kRowsThreads = 256;
+constexpr int kWaves = kRowsThreads / 64;
+constexpr int kRowsMost = 16;  // rows (new tokens times the group's heads) of a request that the rows kernel takes
 constexpr int kBlockKeys = 32;
 
 // Dword t of a lane's V values of one key.
@@ -150,6 +156,12 @@ __device__ __forceinline__ VRow<VD> load_vrow(const uint16_t* p) {
         }
     }
     return r;
+}
+
+// Two values of a partial result (see store_partial), 8-byte aligned.
+__device__ __forceinline__ void store_pair(float* p, float x, float y) {
+    __hip_atomic_store(reinterpret_cast<uint64_t*>(p), (uint64_t)__float_as_uint(x) | (uint64_t)__float_as_uint(y) << 32,
+                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // Joins the partial results of a workgroup tile's splits, in split order, by
@@ -188,40 +200,69 @@ __device__ __forceinline__ void join_splits(const AttnArgs& a, const Request& rq
         }
     }
     __syncthreads();
-    for (int u = tid; u < rows * (D / 2); u += kRowsThreads) {
-        const int row = u / (D / 2), d = (u - row * (D / 2)) * 2;
-        float x0 = 0.f, x1 = 0.f;
-        const int at_d = out_at + row * D + d;
-        constexpr int RS = 8;  // splits in flight
-        for (int s0 = 0; s0 < nsplit; s0 += RS) {
-            uint64_t v[RS];
+    // Pairs of values, U pairs of RS splits in flight a thread: these loads go
+    // past the L2 and take a microsecond or two each, so a join is bound by how
+    // many of them wait at once.  Many rows fill that with pairs, few with splits.
+    const int pairs = rows * (D / 2);
+    const auto join = [&](auto units, auto round) {
+        constexpr int U = decltype(units)::value, RS = decltype(round)::value;
+        for (int u0 = tid; u0 < pairs; u0 += U * kRowsThreads) {
+            float x0[U], x1[U];
+            int rw[U], at_d[U];
 #pragma unroll
-            for (int s = 0; s < RS; ++s)
-                v[s] = __hip_atomic_load(reinterpret_cast<const uint64_t*>(slabs.at(min(s0 + s, nsplit - 1)) + at_d),
-                                         __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            for (int u = 0; u < U; ++u) {
+                const int p = min(u0 + u * kRowsThreads, pairs - 1);
+                rw[u] = p / (D / 2);
+                at_d[u] = out_at + 2 * p;
+                x0[u] = x1[u] = 0.f;
+            }
+            for (int s0 = 0; s0 < nsplit; s0 += RS) {
+                uint64_t v[RS][U];
 #pragma unroll
-            for (int s = 0; s < RS; ++s)
-                if (s0 + s < nsplit) {
-                    const float f = wgt[row * nsplit + s0 + s];
-                    x0 += f * __uint_as_float((uint32_t)v[s]);
-                    x1 += f * __uint_as_float((uint32_t)(v[s] >> 32));
-                }
+                for (int s = 0; s < RS; ++s)
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        v[s][u] = __hip_atomic_load(reinterpret_cast<const uint64_t*>(slabs.at(min(s0 + s, nsplit - 1)) + at_d[u]),
+                                                    __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+                for (int s = 0; s < RS; ++s)
+                    if (s0 + s < nsplit) {
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            const float f = wgt[rw[u] * nsplit + s0 + s];
+                            x0[u] += f * __uint_as_float((uint32_t)v[s][u]);
+                            x1[u] += f * __uint_as_float((uint32_t)(v[s][u] >> 32));
+                        }
+                    }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (u0 + u * kRowsThreads >= pairs) break;
+                const float L = row_l[rw[u]];
+                const int64_t r = row0 + rw[u];
+                const int tok = (int)(r / G), d = at_d[u] - out_at - rw[u] * D;
+                const int64_t at = (int64_t)(rq.t0 + tok) * a.Hq + h * G + (int)(r - (int64_t)tok * G);
+                const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN);
+                *reinterpret_cast<uint32_t*>(a.out + at * D + d) = E::pack2(x0[u] * inv, x1[u] * inv);
+                if (d == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : kLn2 * (row_m[rw[u]] + log2f(L));
+            }
         }
-        const float L = row_l[row];
-        const int64_t r = row0 + row;
-        const int tok = (int)(r / G);
-        const int64_t at = (int64_t)(rq.t0 + tok) * a.Hq + h * G + (int)(r - (int64_t)tok * G);
-        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN);
-        *reinterpret_cast<uint32_t*>(a.out + at * D + d) = E::pack2(x0 * inv, x1 * inv);
-        if (d == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : kLn2 * (row_m[row] + log2f(L));
-    }
+    };
+    using std::integral_constant;
+    if (pairs > 4 * kRowsThreads) join(integral_constant<int, 8>{}, integral_constant<int, 2>{});
+    else if (pairs > kRowsThreads) join(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+    else join(integral_constant<int, 1>{}, integral_constant<int, 16>{});
 }
 
 // Even shares: the requests' blocks lie one after another (start[b], start[B]
 // in all), and every workgroup of a KV head takes as many of them, so that one
 // round of workgroups ends together whatever the lengths.  -> blocks of a
-// share: kShareBlocks (one a wave) at least, and so many that no request has more than
-// a.split_most shares.  All threads of the workgroup.
+// share: kShareBlocks (one a wave) at least; so many that no request has more
+// than a.split_most shares; and no fewer than where the longest request's join
+// costs what its blocks do.  N blocks in shares of x take 0.3 us x, and the
+// join of N / x partial results, 32 KiB of them in flight for 1.5 us,
+// 1.5 us rows D 4 B / 32 KiB each: x = sqrt(N rows D 6e-4).  All threads of the
+// workgroup.
 constexpr int kShareRequests = 1024;
 constexpr int kShareBlocks = 4;
 constexpr int kSplitBlocks = 8;  // calls whose requests have no more blocks are not shared out
@@ -235,7 +276,8 @@ __device__ __forceinline__ int64_t even_shares(const AttnArgs& a, int64_t* start
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const auto share_of = [&](int64_t total, int64_t most) {
         const int64_t share = divide(total + a.workers - 1, a.workers);
-        return max(max(share, divide(most + a.split_most - 2, a.split_most - 1)), (int64_t)kShareBlocks);
+        const int64_t joined = (int64_t)sqrtf((float)most * a.join_cost);
+        return max(max(share, joined), max(divide(most + a.split_most - 2, a.split_most - 1), (int64_t)kShareBlocks));
     };
     if (a.B == 1) {  // nothing to add up
         const int64_t n = blocks(0);
@@ -282,18 +324,18 @@ __device__ __forceinline__ int64_t even_shares(const AttnArgs& a, int64_t* start
 }
 
 template <class E, int D>
-__global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kRowsThreads, D == 64 ? 3 : 2) void rows_kernel(AttnArgs a) {
     constexpr int ST = D / 32, DV = D / 16, VD = DV / 2;
     constexpr int LD = D + 4;  // LDS row stride (floats): rows of a quad of lanes fall into different banks
     __shared__ float lds_o[4 * 16 * LD];
     __shared__ float lds_ml[4 * 16 * 2];
-    __shared__ float row_m[64], row_l[64];
+    __shared__ float row_m[kRowsMost], row_l[kRowsMost];
     __shared__ uint32_t word;
     __shared__ int64_t start[kShareRequests + 1], share_word;
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, c = lane & 15;
-    const int R = a.R, G = a.G;
+    const int G = a.G;
     const int h = (int)(blockIdx.x % (unsigned)a.Hkv), worker = (int)(blockIdx.x / (unsigned)a.Hkv);
 
     // What request b asks of a KV head: its rows and the key blocks they see.
@@ -348,16 +390,13 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
             slabs = Slabs{slab_of(first, s0 > first * share ? 1 : 0), slab_of(first, 0), (int64_t)a.Hkv * 2 * a.slab};
         }
 
-        const int tile = wave % R, ks = wave / R, KS = 4 / R;
-        const int my_row = tile * 16 + c;
-        const bool row_ok = my_row < rows;
-        const int my_tok = (row_ok ? my_row : 0) / G;
-        const int my_head = h * G + (row_ok ? my_row : 0) - my_tok * G;
+        const bool row_ok = c < rows;
+        const int my_tok = (row_ok ? c : 0) / G;
+        const int my_head = h * G + (row_ok ? c : 0) - my_tok * G;
         const int my_pos = row_ok ? rq.first + my_tok : INT32_MIN;
-        // positions of the tile's first and last row
-        const int tile_p0 = rq.first + tile * 16 / G;
-        const int tile_p1 = rq.first + min(tile * 16 + 15, rows - 1) / G;
-        const bool tile_ok = tile * 16 < rows;
+        // positions of the first and the last row
+        const int tile_p0 = rq.first;
+        const int tile_p1 = rq.first + (rows - 1) / G;
 
         uint4 qf[ST];
         {
@@ -406,15 +445,15 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) vr[e] = load_vrow<VD>(vbase + e * D);
         };
-        if (tile_ok && i0 + ks < i1) {
-            int i = i0 + ks, key0 = bl.at(i) * kBlockKeys;
+        if (i0 + wave < i1) {
+            int i = i0 + wave, key0 = bl.at(i) * kBlockKeys;
             Pages now = pages_at(i);
             load_k(key0, now);
             load_v(key0, now);
-            Pages next = pages_at(i + KS);
+            Pages next = pages_at(i + kWaves);
             for (;;) {
-                const bool more = i + KS < i1;
-                const int key1 = more ? bl.at(i + KS) * kBlockKeys : key0;
+                const bool more = i + kWaves < i1;
+                const int key1 = more ? bl.at(i + kWaves) * kBlockKeys : key0;
                 const bool okv = there(g >= 2 ? now.hi : now.lo);
                 float t8[8];
 #pragma unroll
@@ -517,16 +556,16 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
                 }
                 if (!more) break;
                 load_v(key1, next);
-                i += KS;
+                i += kWaves;
                 key0 = key1;
                 now = next;
-                next = pages_at(i + KS);
+                next = pages_at(i + kWaves);
             }
             l += __shfl_xor(l, 16, 64);
             l += __shfl_xor(l, 32, 64);
         }
 
-        // join the waves of each tile
+        // join the waves
         {
             float* dst = lds_o + (wave * 16 + c) * LD + 4 * DV * g;
 #pragma unroll
@@ -544,13 +583,12 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
         constexpr int EPT = 4;                                             // values a thread joins at a time
         for (int u = tid; u < rows * (D / EPT); u += kRowsThreads) {
             const int row = u / (D / EPT), d = (u - row * (D / EPT)) * EPT;
-            const int tl = row >> 4, rr = row & 15;
             float M = -INFINITY, L = 0.f;
-            for (int w = 0; w < KS; ++w) M = fmaxf(M, lds_ml[((w * R + tl) * 16 + rr) * 2]);
+            for (int w = 0; w < kWaves; ++w) M = fmaxf(M, lds_ml[(w * 16 + row) * 2]);
             const float ms = M == -INFINITY ? 0.f : M;
             float acc[EPT] = {0.f, 0.f, 0.f, 0.f};
-            for (int w = 0; w < KS; ++w) {
-                const int base = (w * R + tl) * 16 + rr;
+            for (int w = 0; w < kWaves; ++w) {
+                const int base = w * 16 + row;
                 const float f = exp2_fast(lds_ml[base * 2] - ms);
                 L += f * lds_ml[base * 2 + 1];
                 const float4 x = *reinterpret_cast<const float4*>(lds_o + base * LD + d);
@@ -561,7 +599,7 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
             }
             if (parts) {
 #pragma unroll
-                for (int e = 0; e < EPT; ++e) store_partial(slab + 2 * rows + row * D + d + e, acc[e]);
+                    for (int e = 0; e < EPT; e += 2) store_pair(slab + 2 * rows + row * D + d + e, acc[e], acc[e + 1]);
                 if (d == 0) {
                     store_partial(slab + 2 * row, M);
                     store_partial(slab + 2 * row + 1, L);
@@ -602,6 +640,11 @@ __global__ __launch_bounds__(kRowsThreads) void rows_kernel(AttnArgs a) {
 // The scores of tile i + 1 are computed in the same run of instructions as the
 // exponentials and the products with V of tile i, so that the matrix cores and
 // the vector unit work at once within a wave: K runs one tile ahead of V.
+//
+// 8192 tokens over 12288 keys, 32 + 8 heads of 128, bf16: 1030 to 1090 us, 1010
+// to 1070 TFLOP/s; without the overlap of scores and weights 1220 us.  The
+// matrix cores are busy 56 % of the cycles, at a clock that the card's power
+// holds at 1.7 GHz under this load.
 constexpr int kTileKeys = 64;
 constexpr int kTileRows = 128;
 constexpr int kTileThreads = 256;
@@ -999,7 +1042,7 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) store_partial(dst + 32 * d + 8 * (r >> 2) + (r & 3), o[d][r]);
+            for (int r = 0; r < 16; r += 2) store_pair(dst + 32 * d + 8 * (r >> 2) + (r & 3), o[d][r], o[d][r + 1]);
     }
     if (!split_last_arrival(a.flags, (uint32_t)wg_tile, nsplit, &ctrl[2])) return;
     const float* slabs = a.partials + wg_tile * a.splits * a.slab;
@@ -1011,41 +1054,19 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
 
 // Schedule of a call.
 //
-// Requests of more than kRowsMost rows (new tokens times the group's heads)
-// go to the tile kernel, the others to the rows kernel; a call whose requests
-// may be of both kinds launches both, one request alone the one it needs.
+// Requests of more than kRowsMost rows go to the tile kernel, the others to the
+// rows kernel.  A call that may hold both kinds launches both; but where the
+// largest request has 64 rows at most, or there is one request, the tile kernel
+// takes them all: a second launch costs 4 us, more than its short tiles do.
 //
-// Rows kernel: row tiles a workgroup holds: as many as its largest request
-// needs, up to 4 (its waves then share the keys).  With a workspace, the two
+// Rows kernel: with a workspace, the two
 // workgroups a compute unit holds take even shares of all blocks, 4 at least (a
 // block a wave).  Without one, or where
 // the requests are more than the counters, a request is one workgroup's.
 //
-// Tile kernel: split until the grid has about 4 workgroups a compute unit (two
-// are resident), no split shorter than 8 tiles.
-constexpr int64_t kRowsMost = 64;
-
-namespace {
-
-// Splits of `blocks` key blocks: `per` blocks each, at least `least`, such
-// that `tiles` tiles make about `want` workgroups, but no shorter than `full`
-// while there are more than `resident` of them; at most `most` splits.
-int64_t split_keys(int64_t tiles, int64_t blocks, int64_t want, int64_t resident, int64_t least, int64_t full, int64_t most,
-                   int64_t* per_out) {
-    *per_out = blocks > 0 ? blocks : 1;
-    if (tiles > kMaxFlags || blocks <= least) return 1;
-    int64_t per = (tiles * blocks + want - 1) / want;
-    const int64_t one_round = (tiles * blocks + resident - 1) / resident;
-    if (per < full) per = one_round < full ? one_round : full;
-    if (per < least) per = least;
-    int64_t s = (blocks + per - 1) / per;
-    if (s > most) s = most;
-    per = (blocks + s - 1) / s;
-    *per_out = per;
-    return (blocks + per - 1) / per;
-}
-
-}  // namespace
+// Tile kernel: keys are split only while that keeps the grid within the two
+// workgroups a compute unit holds, into no less than 8 tiles each.
+constexpr int64_t kTileSplitMost = 64;  // the join's weights: splits * 128 floats of LDS, 32 KiB for D = 64
 
 AttnPlan attn_plan(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q, int64_t max_kv, int64_t window,
                    int64_t sinks, int compute_units) {
@@ -1061,11 +1082,15 @@ AttnPlan attn_plan(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int
     };
     size_t bytes = 0;
     if (large) {
-        p.rows_most = B > 1 ? kRowsMost : 0;
+        p.rows_most = B > 1 && rows > 64 ? kRowsMost : 0;
         p.tiles = T * G / kTileRows + B;
         const int64_t blocks = (reach(kTileRows) + kTileKeys - 1) / kTileKeys;
-        p.tile_splits = split_keys(p.tiles * Hkv, blocks, compute_units * 4, compute_units * 2, 8, 16, D == 128 ? 128 : 64,
-                                   &p.tile_split_blocks);
+        int64_t n = 2 * compute_units / (p.tiles * Hkv);
+        if (n > blocks / 8) n = blocks / 8;
+        if (n > kTileSplitMost) n = kTileSplitMost;
+        if (n < 1 || p.tiles * Hkv > kMaxFlags) n = 1;
+        p.tile_split_blocks = blocks > 0 ? (blocks + n - 1) / n : 1;
+        p.tile_splits = blocks > 0 ? (blocks + p.tile_split_blocks - 1) / p.tile_split_blocks : 1;
         p.tile_slab = kTileRows * (D + 2);
         if (p.tile_splits > 1) bytes = (size_t)(p.tiles * Hkv * p.tile_splits * p.tile_slab) * 4;
         rows = kRowsMost;
@@ -1073,10 +1098,10 @@ AttnPlan attn_plan(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int
         p.rows_most = rows;
     }
     if (p.rows_most > 0) {
-        p.R = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
         p.slab = rows * (D + 2);
         const int64_t blocks = (reach(rows) + kBlockKeys - 1) / kBlockKeys;
-        p.split_most = 4096 / (16 * p.R);  // the join's weights: splits * rows <= 4096 floats of LDS
+        p.split_most = 4096 / rows;  // the join's weights: splits * rows <= 4096 floats of LDS
+        p.join_cost = (float)(rows * D) * 6e-4f;
         int64_t w = B * blocks / kShareBlocks + 1;
         if (w > 2 * compute_units / Hkv) w = 2 * compute_units / Hkv;
         if (w > 1 && blocks > kSplitBlocks && B <= kShareRequests && B * Hkv <= kMaxFlags) {
@@ -1124,9 +1149,9 @@ hipError_t launch_attention(const AttnArgs& args, const AttnPlan& plan, hipStrea
         if (e != hipSuccess) return e;
     }
     if (plan.rows_most == 0) return hipSuccess;
-    a.R = plan.R;
     a.workers = a.partials ? (int)plan.workers : 0;
     a.split_most = (int)plan.split_most;
+    a.join_cost = plan.join_cost;
     a.slab = plan.slab;
     const int64_t grid = (a.workers > 0 ? a.workers : (int64_t)a.B) * a.Hkv;
     if (grid <= 0 || grid > 0x7FFFFFFF) return hipErrorInvalidValue;

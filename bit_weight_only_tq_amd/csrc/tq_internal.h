@@ -207,7 +207,8 @@ struct AttnArgs {
     int64_t rows_most;  // requests of more rows are the tile kernel's
     int64_t tiles;      // of the tile kernel, with room for every request's last
     int splits, split_blocks;  // tile kernel
-    int R, workers, split_most;  // rows kernel
+    int workers, split_most;     // rows kernel
+    float join_cost;
     int64_t slab;
 };
 struct AttnPlan {
@@ -218,9 +219,9 @@ struct AttnPlan {
     int64_t tile_slab;          // floats of one split's partial result
     // rows kernel
     int64_t rows_most;    // 0: not launched
-    int R;                // 16-row tiles a workgroup holds
     int64_t workers;      // workgroups of a KV head that take even shares (0: one a request)
     int64_t split_most;   // shares of one request, at most
+    float join_cost;      // of a partial result against a block of keys
     int64_t slab;         // floats of a partial result
     size_t data_bytes;    // partial results of the call
 };
