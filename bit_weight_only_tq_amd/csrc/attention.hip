@@ -100,7 +100,7 @@ __device__ __forceinline__ Blocks blocks_of(const AttnArgs& a, const Request& r,
     const int end = min(p1, r.keys - 1) + 1;  // first key nobody sees
     const int main1 = end > 0 ? (int)(((uint32_t)end + (1u << LOG) - 1u) >> LOG) : 0;
     int lo = 0;
-    if (a.window > 0) lo = max(p0 - a.window + 1, 0);
+    if (a.window > 0) lo = (int)max((int64_t)p0 - a.window + 1, (int64_t)0);
     k.main0 = min(lo >> LOG, main1);
     k.head = min((int)(((uint32_t)a.sinks + (1u << LOG) - 1u) >> LOG), k.main0);
     k.count = k.head + (main1 - k.main0);
@@ -1055,9 +1055,16 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
 // Schedule of a call.
 //
 // Requests of more than kRowsMost rows go to the tile kernel, the others to the
-// rows kernel.  A call that may hold both kinds launches both; but where the
-// largest request has 64 rows at most, or there is one request, the tile kernel
-// takes them all: a second launch costs 4 us, more than its short tiles do.
+// rows kernel.  A call that may hold both kinds launches both, unless there is
+// one request or none reads more than kShortKeys keys: the tile kernel then
+// takes them all, a decoding row in a tile of 128 costing less than the second
+// launch and its tail (24 decoding requests beside 9 chunks, a window of 2047:
+// 143 us against 165; 44 requests of up to 401 keys, 13 of them chunks of 23
+// tokens at most: 14 against 31; 60 decoding requests of up to 8191 keys beside
+// 4 chunks: 697 against 728).  With one request of 30000 keys among eight, whose
+// tiles have no even shares, it is 335 against 247.  The same holds, at any
+// length, where the largest request has 64 rows at most (64 requests of up to
+// 8191 keys and 3 tokens: 233 against 310).
 //
 // Rows kernel: with a workspace, the two
 // workgroups a compute unit holds take even shares of all blocks, 4 at least (a
@@ -1066,6 +1073,7 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
 //
 // Tile kernel: keys are split only while that keeps the grid within the two
 // workgroups a compute unit holds, into no less than 8 tiles each.
+constexpr int64_t kShortKeys = 12288;
 constexpr int64_t kTileSplitMost = 64;  // the join's weights: splits * 128 floats of LDS, 32 KiB for D = 64
 
 AttnPlan attn_plan(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q, int64_t max_kv, int64_t window,
@@ -1082,7 +1090,7 @@ AttnPlan attn_plan(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int
     };
     size_t bytes = 0;
     if (large) {
-        p.rows_most = B > 1 && rows > 64 ? kRowsMost : 0;
+        p.rows_most = B > 1 && rows > 64 && reach(kTileRows) > kShortKeys ? kRowsMost : 0;
         p.tiles = T * G / kTileRows + B;
         const int64_t blocks = (reach(kTileRows) + kTileKeys - 1) / kTileKeys;
         int64_t n = 2 * compute_units / (p.tiles * Hkv);

@@ -38,3 +38,11 @@ def test_messages_name_the_argument():
         tq.tq_sample(torch.zeros((2, 9)), torch.zeros(3))
     with pytest.raises(ValueError, match="k and v must have the cache's 1 heads, got 2 and 1"):
         tq.tq_kv_append(None, H.expand(3, 2, 64).contiguous(), H, C, C, torch.zeros(3, dtype=torch.int64))
+
+
+def test_every_source_is_built():
+    """Each kernel and API file of csrc is one of the library's sources."""
+    import os
+    from bit_weight_only_tq_amd import build
+    names = {f for f in os.listdir(build.CSRC) if f.endswith(".hip") or f.startswith("api")}
+    assert names == set(build.SOURCES)
