@@ -668,7 +668,7 @@ __device__ __forceinline__ void dma_runs(const void* base, const uint32_t (&off)
     if constexpr (N == 4)
         asm volatile("s_mov_b32 m0, %5\n\ts_nop 0\n\t"
                      "global_load_lds_dwordx4 %0, %4\n\tglobal_load_lds_dwordx4 %1, %4 offset:1024\n\t"
-                     "global_load_lds_dwordx4 %2, %4 offset:2048\n\tglobal_load_lds_dwordx4 %3, %4 offset:3072"
+                     "global_load_lds_dwordx4 %2, %4 offset:2048\n\tglobal_load_lds_dwordx4 %3, %4 offset:0xC00"
                      :: "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]), "s"(base), "s"(lds_addr) : "memory", "m0");
     else
         asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\t"

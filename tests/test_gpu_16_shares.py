@@ -45,3 +45,36 @@ def test_small_workspace_means_none():
     from gpu_common import require_gpu
     c = Case([1, 1], [3000, 100], 8, 2, 128, 16, "bf16")
     c.check(c.run(workspace=torch.zeros(20000, dtype=torch.uint8, device=require_gpu())))
+
+
+@pytest.mark.parametrize("dt,D", [("f16", 64), ("bf16", 128)])
+def test_both_kernels_in_one_call(dt, D):
+    """A chunk beside decoding requests over more than 12288 keys: two launches, one workspace, captured as well."""
+    import torch
+    import bit_weight_only_tq_amd as tq
+    from gpu_common import require_gpu
+    dev = require_gpu()
+    qn, kv = [1, 90, 0, 16, 1], [13000, 300, 5, 2000, 50]
+    c, got = _go(qn, kv, 2, 2, D, 16, dt)
+    ws = tq.new_workspace(tq.tq_paged_attention_workspace_bytes(sum(qn), 2, 2, D, 5, 90, 13000), dev)
+    d = [t.to(dev) for t in (c.q, c.k, c.v, c.table, c.cu, c.kv)]
+    out = torch.empty_like(got[0])
+    call = lambda: tq.tq_paged_attention(*d, 90, 13000, out=out, return_lse=True, workspace=ws)  # noqa: E731
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call()
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        _, lse = call()
+    for i in range(4):
+        out.fill_(0), lse.fill_(0)
+        torch.randn(1000, device=dev).sum()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, got[0]) and torch.equal(lse, got[1]), f"replay {i}"
+    assert int(ws[:tq.TQ_WORKSPACE_FLAG_BYTES].count_nonzero()) == 0
+    if D == 64:  # with a window that leaves little to read, one kernel does it all
+        c.check(c.run(1000, 4), 1000, 4)
+        c.check(c.run(12500, 4), 12500, 4)
