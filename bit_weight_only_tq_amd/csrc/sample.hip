@@ -14,7 +14,7 @@
 // weights, no sort.  A kept set hangs on comparisons of weight sums, so
 // weights are computed in fp64 and summed as 64-bit fixed point: such sums do
 // not depend on their order, so atomics and any split of the row give the same
-// bits, and their error (2^-44 of the largest weight each) is far below any
+// bits, and their error (2^-43 of the largest weight each, at most) is far below any
 // token's share.
 //
 // One workgroup a row.  What it costs is the passes over the row and the

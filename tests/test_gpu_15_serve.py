@@ -112,3 +112,29 @@ def test_example_runs(capsys):
     require_gpu()
     _example().main()
     assert "pages in use" in capsys.readouterr().out
+
+
+@pytest.mark.parametrize("mode", ["inference_mode", "no_grad", "enable_grad"])
+def test_outputs_are_ordinary_tensors(mode):
+    """A plan's outputs share one allocation: each can be changed in place, viewed, copied and outlive the others."""
+    import torch
+    import bit_weight_only_tq_amd as tq
+    dev = require_gpu()
+    log(f"outputs {mode}")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
+    with getattr(torch, mode)():
+        plan = tq.tq_paged_plan(i32([3, 0, 16]), i32([2, 1, 4]), torch.full((3, 4), -1, dtype=torch.int32, device=dev),
+                                i32([9, 8, 7, 6]), i32([0]), 8)
+        assert plan.cu_q.tolist() == [0, 2, 3, 7] and plan.kv_lens.tolist() == [5, 1, 20]
+        assert all(t.is_contiguous() and not t.requires_grad and t.device == dev for t in plan)
+        slots, state = plan.slots, plan.state
+        plan.positions.add_(100)
+        plan.cu_q.mul_(0)
+        plan.kv_lens.view(3, 1).fill_(7)
+        assert plan.positions.tolist() == [103, 104, 100, 116, 117, 118, 119, 100] and plan.kv_lens.tolist() == [7] * 3
+        assert slots.dtype == torch.int64 and slots[2].item() == 9 * 16 and slots[7].item() == -1
+        del plan
+        torch.empty(1 << 20, device=dev).fill_(1.0)
+        assert state.clone().tolist() == [2, 2] and slots[3:7].cpu().tolist() == [128, 129, 130, 131]
+        tokens, logprobs = tq.tq_sample(torch.zeros((2, 8), device=dev), torch.tensor([0.0, 0.99], device=dev))
+        assert tokens.add_(0).tolist() == [0, 7] and torch.allclose(logprobs.exp(), torch.full((2,), 0.125, device=dev))
