@@ -794,10 +794,16 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
         const int pg = trow[j >> a.shift];
         return (uint32_t)pg < (uint32_t)a.pages ? pg : -1;
     };
-    // Set for good by the first one of its kind that the workgroup meets: a
-    // value that is not finite in a tile that not every row sees whole, and a
-    // page that is not there.
-    uint32_t *poison = &ctrl[0], *absent = &ctrl[1];
+    // Set for good by the first value that is not finite in a tile that not every
+    // row sees whole.
+    uint32_t* poison = &ctrl[0];
+    // The first tile of which a page is not there.  Waves look their pages up at
+    // different times, up to two tiles ahead, and the waves must agree on which
+    // tiles have gaps (a barrier hangs on it): so a wave posts the tile's number
+    // and a tile i asks for one of at most i.  What was posted for the tiles up
+    // to i lies a barrier or more back when i is asked for, and what is posted
+    // meanwhile, for later tiles, does not change the answer.
+    uint32_t* absent = &ctrl[1];
     // A tile: its first key, and where this wave's run lies in the caches.
     // The page id is read one tile before it is used (id_of, then tile_at).
     struct Tile {
@@ -813,7 +819,7 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
         const int j = t.key0 + 16 * wave;
         if ((uint32_t)id >= (uint32_t)a.pages) {
             id = 0;
-            *absent = 1u;
+            atomicMin(absent, (uint32_t)i);
         }
         t.at = (int64_t)id * a.page_stride + head_at + (uint32_t)((j & page_mask) * D);
         return t;
@@ -836,7 +842,10 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
             vaddr[d] = (uint32_t)(key * TG::kRowBytes + (((4 * d + x) ^ TG::vswz(key)) << 4) + 8 * (lane & 1));
     }
     char* smem = reinterpret_cast<char*>(smem_tile);
-    if (tid == 0) *poison = *absent = 0u;
+    if (tid == 0) {
+        *poison = 0u;
+        *absent = 0xFFFFFFFFu;
+    }
     __syncthreads();
     const int wg_whole = min(wg_p0, last_key) - (kTileKeys - 1);  // tiles up to here are seen whole but for a window
 
@@ -871,7 +880,7 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
         scores(i0);
         for (int i = i0; i < i1; ++i) {
             const int key0 = cur.key0;
-            const bool gaps = *absent != 0u;  // of the tiles up to i + 1 at least
+            const bool gaps = *absent <= (uint32_t)i;
             cur = next;
             next = tile_at(i + 2, id);
             id = id_of(i + 3);
