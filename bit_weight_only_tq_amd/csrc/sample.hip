@@ -675,7 +675,8 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
         Row first;
         first.kmax = workgroup_best();
         first.max = (double)logit_of(first.kmax);
-        const float x0 = first.kmax > 0x007FFFFFu ? logit_of(floor_of(first, (double)T, min_w)) : -3.0e38f;
+        // without a logit above -inf in that round: every finite one
+        const float x0 = logit_of(first.kmax > 0x007FFFFFu ? floor_of(first, (double)T, min_w) : 0x00800000u);
         each_logit<L, L::FLIGHT>(row, V, [&](float x, int e) {
             largest(x, e);
             return x >= x0;
