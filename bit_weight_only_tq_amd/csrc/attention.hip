@@ -5,9 +5,13 @@
 // w: p - j < w or j < sinks),
 //   out_i = sum_j 2^(t_ij - m_i) v_j / l_i,   l_i = sum_j 2^(t_ij - m_i),
 //   lse_i = ln 2 (m_i + log2 l_i),
-// in one pass over the keys with a running maximum m_i.  Maxima, sums and
-// outputs are held in fp32; the weights 2^(t - m) are rounded to the cache's
-// type (the matrix cores' operand), as the output is.
+// in one pass over the keys with a running m_i near the maximum (any m_i gives
+// the same result).  Maxima, sums and outputs are held in fp32; the weights
+// 2^(t - m) are rounded to the cache's type, as the output is.  The matrix
+// cores take both operands of a product in one type, and a second product with
+// what a rounding leaves would double the work on V.  The rounding is what
+// the result loses against one in fp32: its error against fp64 is 1.04 to 1.4
+// times as large.
 //
 // The query heads that share a KV head are rows of one matrix: row r of a
 // request and KV head is token r / G, head r % G of the group of G.
@@ -26,8 +30,12 @@ namespace {
 constexpr float kLn2 = 0.69314718055994531f;
 
 // Element types: the matrix products, the rounding of two weights to a
-// dword, and the exponent step that carries a non-finite value's magnitude
-// into bit 15.
+// dword, the exponent step that carries a non-finite value's magnitude into
+// bit 15, and kLift: m_i is held that far below the running maximum.  fp16 has
+// its full step down to 2^-14 and nothing below 2^-25, so with m_i the maximum
+// itself many small weights behind a large one lost their bits, or vanished,
+// while l_i summed them whole.  2^7 is the room it has: weights reach 2^8 times
+// what they are at the maximum before m_i is raised, and 2^15 fits.
 struct AttnF16 {
     static __device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
@@ -41,6 +49,7 @@ struct AttnF16 {
     static __device__ __forceinline__ float lo(uint32_t w) { return (float)__builtin_bit_cast(f16x2, w).x; }
     static __device__ __forceinline__ float hi(uint32_t w) { return (float)__builtin_bit_cast(f16x2, w).y; }
     static constexpr uint32_t kExpStep = 0x04000400u;
+    static constexpr float kLift = 7.f;
 };
 struct AttnBF16 {
     static __device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
@@ -55,6 +64,7 @@ struct AttnBF16 {
     static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
     static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
     static constexpr uint32_t kExpStep = 0x00800080u;
+    static constexpr float kLift = 0.f;
 };
 
 template <class E>
@@ -488,16 +498,16 @@ __global__ __launch_bounds__(kRowsThreads, D == 64 ? 3 : 2) void rows_kernel(Att
                     }
                     poisoned = __any(bad != 0);
                 }
-                // running maximum, shared by the four lanes of a row; raised only
-                // when a score passes it by more than 2^8, so that most blocks
-                // rescale nothing (weights up to 256 fit both 16-bit types)
+                // running maximum less kLift, shared by the four lanes of a row;
+                // raised only when a score passes the maximum by more than 2^8,
+                // so that most blocks rescale nothing
                 float mx = t8[0];
 #pragma unroll
                 for (int e = 1; e < 8; ++e) mx = fmaxf(mx, t8[e]);
-                if (__any(mx > m + 8.f)) {
+                if (__any(mx > m + (E::kLift + 8.f))) {
                     mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
                     mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-                    const float mn = fmaxf(m, mx);
+                    const float mn = fmaxf(m, mx - E::kLift);
                     const float f = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
                     m = mn;
                     l *= f;
@@ -945,16 +955,16 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
                 }
                 if (there != 15u) each([&](int x) { return !((there >> (x >> 4)) & 1u); });
             }
-            // running maximum of the scaled scores, raised as in the rows kernel
+            // running maximum of the scaled scores, held and raised as in the rows kernel
             float mx = s[0][0];
 #pragma unroll
             for (int r = 1; r < 16; ++r) mx = fmaxf(mx, s[0][r]);
 #pragma unroll
             for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[1][r]);
             mx *= a.scale_log2;
-            if (__any(mx > m + 8.f)) {
+            if (__any(mx > m + (E::kLift + 8.f))) {
                 mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-                const float mn = fmaxf(m, mx);
+                const float mn = fmaxf(m, mx - E::kLift);
                 const float f = mn == -INFINITY ? 1.f : exp2_fast(m - mn);
                 m = mn;
                 l *= f;
