@@ -137,7 +137,8 @@ Heads heads_of(const char* name, const Tensor& t, at::ScalarType type, int64_t T
     if (t.size(0) != T || t.size(2) != D)
         value_error(std::string(name) + " must be [" + std::to_string(T) + ", heads, " + std::to_string(D) + "], got " + shape_of(t));
     if (D > 1 && t.stride(2) != 1) value_error("the heads of " + std::string(name) + " must be contiguous");
-    return Heads{t.data_ptr(), t.size(1), t.stride(0), t.stride(1)};
+    // a stride over one token or one head leads nowhere and may be any number
+    return Heads{t.data_ptr(), t.size(1), T > 1 ? t.stride(0) : 0, t.size(1) > 1 ? t.stride(1) : 0};
 }
 
 Tensor fresh(at::IntArrayRef sizes, const Tensor& like, at::ScalarType type) {
@@ -333,7 +334,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (want_lse) lse = fresh({T, hq.n}, q, at::kFloat);
     const hipStream_t s = dev.stream();
     const tq_status st = call([&] {
-        return tq_paged_attention(hq.p, hq.token, hq.n > 1 ? hq.head : 0, c.dt, T, hq.n, c.heads, c.D, kc.data_ptr(),
+        return tq_paged_attention(hq.p, hq.token, hq.head, c.dt, T, hq.n, c.heads, c.D, kc.data_ptr(),
                                   vc.data_ptr(), c.pages, c.page, c.stride, static_cast<const int32_t*>(table.data_ptr()), tab,
                                   width, pc, pk, B, max_q, max_kv, (float)scale, window, sinks, out.data_ptr(),
                                   want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr, ws ? ws->data_ptr() : nullptr,
