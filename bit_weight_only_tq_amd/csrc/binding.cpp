@@ -306,7 +306,8 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                   sinks = whole("sinks", a[10]);
     const int want_lse = PyObject_IsTrue(a[11]);
     if (want_lse < 0) throw python_error();
-    const Tensor *given = optional("out", a[12]), *ws = optional("workspace", a[13]);
+    const bool own_ws = PyUnicode_Check(a[13]);  // "auto"
+    const Tensor *given = optional("out", a[12]), *ws = own_ws ? nullptr : optional("workspace", a[13]);
     const Cache c = cache_of(kc, vc);
     double scale = std::pow((double)c.D, -0.5);
     if (a[8] != Py_None) {
@@ -332,6 +333,15 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Tensor out = given ? *given : fresh({T, hq.n, c.D}, q, q.scalar_type());
     Tensor lse;
     if (want_lse) lse = fresh({T, hq.n}, q, at::kFloat);
+    Tensor work;
+    if (own_ws) {
+        const size_t bytes = tq_paged_attention_workspace_bytes(T, hq.n, c.heads, c.D, B, max_q, max_kv, window, sinks);
+        if (bytes) {
+            work = fresh({(int64_t)bytes}, q, at::kByte);
+            work.narrow(0, 0, TQ_WORKSPACE_FLAG_BYTES).zero_();
+            ws = &work;
+        }
+    }
     const hipStream_t s = dev.stream();
     const tq_status st = call([&] {
         return tq_paged_attention(hq.p, hq.token, hq.head, c.dt, T, hq.n, c.heads, c.D, kc.data_ptr(),

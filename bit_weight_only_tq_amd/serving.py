@@ -92,16 +92,11 @@ def tq_paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q: in
     max_q, max_kv: the largest numbers of new tokens and of keys of a request;
     scale: 1 / sqrt(D) by default; window, sinks: a token sees its last
     `window` keys (0: all) and the first `sinks`.  Causal in each request.
-    workspace: as for tq_gemm ("auto", None or a contiguous device tensor)."""
-    entry = _entry()
-    if type(workspace) is str:
-        workspace = None
-        if q.dim() == 3 and k_cache.dim() == 4 and q.is_cuda:  # anything else is refused below
-            T, Hq, D = q.shape
-            workspace = _lib.new_workspace(_lib.load().tq_paged_attention_workspace_bytes(
-                T, Hq, k_cache.shape[1], D, page_table.shape[0], max_q, max_kv, window, sinks), q.device)
-    return _result("tq_paged_attention", entry.paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q, max_kv,
-                                                               scale, window, sinks, return_lse, out, workspace))
+    workspace: as for tq_gemm ("auto", None or a contiguous device tensor);
+    "auto" allocates and clears one in every call, so a program that makes many
+    keeps one (new_workspace of tq_paged_attention_workspace_bytes)."""
+    return _result("tq_paged_attention", _entry().paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_lens, max_q, max_kv,
+                                                                  scale, window, sinks, return_lse, out, workspace))
 
 
 # ----------------------------------------------------------------- sampling
