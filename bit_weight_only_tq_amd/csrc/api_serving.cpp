@@ -25,6 +25,16 @@ int page_shift(int64_t page_size) {
     return -1;
 }
 
+// `bytes` bytes of a caller's buffer; empty ones overlap nothing.
+struct Span {
+    const void* p;
+    int64_t bytes;
+    bool overlaps(const Span& o) const {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
+        return bytes > 0 && o.bytes > 0 && a < b + (uintptr_t)o.bytes && b < a + (uintptr_t)bytes;
+    }
+};
+
 }  // namespace
 
 extern "C" {
@@ -45,6 +55,13 @@ tq_status tq_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, int32_
         !aligned(free_head, 4) || !aligned(cu_q, 4) || !aligned(kv_lens, 4) || !aligned(positions, 4) ||
         !aligned(slots, 8) || !aligned(state, 4))
         return TQ_ERR_ALIGN;
+    // every workgroup reads the lengths and the free list while others write
+    const Span span[] = {{page_table, ((B - 1) * table_stride + width) * 4}, {cu_q, (B + 1) * 4}, {kv_lens, B * 4},
+                         {positions, T * 4}, {slots, T * 8}, {state, 8},  // written
+                         {ctx_lens, B * 4}, {new_lens, B * 4}, {free_pages, n_free * 4}, {free_head, 4}};
+    for (int w = 0; w < 6; ++w)
+        for (int o = w + 1; o < 10; ++o)
+            if (span[w].overlaps(span[o])) return TQ_ERR_VALUE;
     const tq::PlanArgs a{ctx_lens, new_lens, page_table, table_stride, free_pages, free_head, (int)B,     (int)width,
                          (int)n_free, (int)T, shift,     cu_q,         kv_lens,    positions, slots, state};
     return from_hip(tq::launch_paged_plan(a, stream));

@@ -55,7 +55,8 @@ def tq_paged_plan(ctx_lens, new_lens, page_table, free_pages, free_head, tokens:
     place (rows may be strided); free_pages: int32 [n]; free_head: int32 [1],
     read only: the head after the step is state[0]; tokens: entries of
     positions and slots, at least new_lens' sum (a larger number pads with
-    slot -1).  out: a plan to write into, for steps replayed from a graph."""
+    slot -1).  out: a plan to write into, for steps replayed from a graph; none
+    of it may lie over the inputs (kv_lens is not ctx_lens, state not free_head)."""
     r = _result("tq_paged_plan", _entry().paged_plan(ctx_lens, new_lens, page_table, free_pages, free_head, tokens, page_size,
                                                      out))
     return r if out is not None else PagedPlan(*r)

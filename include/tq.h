@@ -82,7 +82,7 @@ typedef enum tq_status {
     TQ_ERR_HIP = 9,        /* a HIP runtime call or kernel launch failed */
     TQ_ERR_PATH = 10,      /* a forced kernel path cannot run this shape */
     TQ_ERR_SCRATCH = 11,   /* tq_gemm_noalloc: the schedule needs more than its scratch */
-    TQ_ERR_VALUE = 12      /* serving calls: an argument's value is not allowed (page size, strides, scale, window) */
+    TQ_ERR_VALUE = 12      /* serving calls: a value is not allowed (page size, stride, scale, window, overlap) */
 } tq_status;
 
 typedef enum tq_dtype {
@@ -418,6 +418,8 @@ size_t w4a16_gemm_asym_workspace_bytes(int64_t M, int64_t N, int64_t K, tq_dtype
  * Tokens of `positions` and `slots` past the sum of new_lens are padding:
  * position 0, slot -1, not counted; tokens past T are not written and are
  * counted.  Negative lengths count as 0, sums are held at 2^31 - 1.
+ * What is written must not overlap what is read or is written elsewhere, so
+ * kv_lens is not ctx_lens and state is not free_head (TQ_ERR_VALUE).
  * 1 <= B <= 16384 (TQ_ERR_SHAPE).
  */
 tq_status tq_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, int32_t* page_table, int64_t table_stride,
