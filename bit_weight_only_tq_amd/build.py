@@ -46,25 +46,49 @@ def _hipcc():
     raise RuntimeError("hipcc not found (set HIPCC or install ROCm)")
 
 
-def _build_binding():
-    """Compile and link _serving.so beside libtq.so, which it needs."""
+def _binding_command():
+    """The compile and link of _serving.so, or what it lacks here (a RuntimeError's text)."""
     import sysconfig
-
-    import torch
-    from torch.utils import cpp_extension
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("no C++ compiler (g++ or c++)")
+    try:
+        import torch
+        from torch.utils import cpp_extension
+    except ImportError as e:
+        raise RuntimeError(f"torch cannot be imported ({e})")
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+    python = sysconfig.get_paths()["include"]
+    system = cpp_extension.include_paths() + [os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include")]
+    for header in ("Python.h", "ATen/ATen.h", "c10/hip/HIPStream.h", "torch/csrc/autograd/python_variable.h"):
+        if not any(os.path.exists(os.path.join(path, header)) for path in [python] + system):
+            raise RuntimeError(f"no header {header}")
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
            "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"]]
-    for path in cpp_extension.include_paths() + [os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include")]:
+           "-I", INCLUDE, "-I", python]
+    for path in system:
         cmd += ["-isystem", path]
-    tmp = BINDING + ".tmp"
-    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", HERE, "-l:libtq.so", "-L", lib, "-ltorch_python",
-            "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
+    return cmd + [os.path.join(CSRC, "binding.cpp"), "-o", BINDING + ".tmp", "-L", HERE, "-l:libtq.so", "-L", lib,
+                  "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
+
+
+def _build_binding():
+    """Compile and link _serving.so beside libtq.so, which it needs.
+
+    The library and its other calls do without it, so where its compiler or
+    headers are missing the build goes on: the serving calls then raise, and
+    one of an earlier build, for another library, is removed."""
+    try:
+        cmd = _binding_command()
+    except RuntimeError as e:
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        print(f"_serving.so not built: {e}; the serving calls will not run, libtq.so is complete", file=sys.stderr)
+        return
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     if r.returncode != 0:
         raise RuntimeError(f"_serving build failed: {' '.join(cmd)}\n" + r.stdout.decode(errors="replace"))
-    os.replace(tmp, BINDING)
+    os.replace(BINDING + ".tmp", BINDING)
 
 
 def build(verbose: bool = False, jobs: int = 4) -> str:
