@@ -120,7 +120,7 @@ tq_status tq_kv_append(const void* q, int64_t q_stride, int64_t q_head, const vo
 static bool attention_sizes_ok(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q, int64_t max_kv) {
     return T >= 0 && T <= kInt32Max && Hkv > 0 && Hkv <= 4096 && Hq > 0 && Hq <= 65536 && Hq % Hkv == 0 &&
            (D == 64 || D == 128) && B > 0 && B <= kInt32Max && max_q >= (T > 0 ? 1 : 0) && max_q <= kInt32Max &&
-           max_kv >= 0 && max_kv <= kInt32Max;
+           max_kv >= 0 && max_kv <= kInt32Max && T * Hq / 128 + B * Hkv < ((int64_t)1 << 24);  // workgroups, of 256 threads
 }
 
 size_t tq_paged_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q,

@@ -368,9 +368,9 @@ hipError_t launch_paged_plan(const PlanArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_kv_append(const AppendArgs& args, hipStream_t s) {
-    AppendArgs a = args;
-    if (!vectors_fit(a)) {
+// The tokens of one launch.
+static hipError_t launch_append_part(AppendArgs a, bool vectors, hipStream_t s) {
+    if (!vectors) {
         const int items = (a.Hq + a.Hkv) * (a.D - a.rot / 2) + a.Hkv * a.D;
         const int gy = items > 8 * 256 ? 8 : (items + 255) / 256;
         if (a.bf16) append_element_kernel<BF16><<<dim3((unsigned)a.T, gy), dim3(256), 0, s>>>(a);
@@ -397,6 +397,25 @@ hipError_t launch_kv_append(const AppendArgs& args, hipStream_t s) {
         else append_kernel<F16, false><<<grid, dim3(256), 0, s>>>(a);
     }
     return hipGetLastError();
+}
+
+hipError_t launch_kv_append(const AppendArgs& args, hipStream_t s) {
+    const bool vectors = vectors_fit(args);
+    for (int64_t t = 0; t < args.T; t += kMaxGroups) {
+        AppendArgs a = args;
+        a.T = args.T - t < kMaxGroups ? args.T - t : kMaxGroups;
+        if (a.Hq) {
+            a.q += t * a.q_stride;
+            a.q_out += t * a.Hq * a.D;
+        }
+        a.k += t * a.k_stride;
+        a.v += t * a.v_stride;
+        a.slots += t;
+        if (a.rot) a.positions += t;
+        const hipError_t e = launch_append_part(a, vectors, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace tq

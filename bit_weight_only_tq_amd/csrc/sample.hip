@@ -998,8 +998,8 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
 
 }  // namespace
 
-hipError_t launch_sample(const SampleArgs& args, hipStream_t s) {
-    SampleArgs a = args;
+// The rows of one launch.
+static hipError_t launch_sample_part(SampleArgs a, hipStream_t s) {
     int bits = 0;
     while (((int64_t)1 << bits) < a.V) ++bits;
     a.fix = bits < 10 ? 52 : 62 - bits;  // V weights of 2^fix at most: sums stay below 2^63
@@ -1022,6 +1022,26 @@ hipError_t launch_sample(const SampleArgs& args, hipStream_t s) {
         if (e == hipSuccess) sample_kernel<Logit16<F16>><<<grid, block, lds, s>>>(a);
     }
     return e != hipSuccess ? e : hipGetLastError();
+}
+
+hipError_t launch_sample(const SampleArgs& args, hipStream_t s) {
+    const int64_t size = args.dtype == 2 ? 4 : 2;
+    const auto from = [](auto* p, int64_t b) { return p ? p + b : p; };
+    for (int64_t b = 0; b < args.B; b += kMaxGroups) {
+        SampleArgs a = args;
+        a.B = args.B - b < kMaxGroups ? args.B - b : kMaxGroups;
+        a.logits = static_cast<const char*>(a.logits) + b * a.row_stride * size;
+        a.u += b;
+        a.temperature = from(a.temperature, b);
+        a.top_k = from(a.top_k, b);
+        a.top_p = from(a.top_p, b);
+        a.min_p = from(a.min_p, b);
+        a.tokens += b;
+        a.logprobs = from(a.logprobs, b);
+        const hipError_t e = launch_sample_part(a, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace tq

@@ -149,6 +149,10 @@ hipError_t launch_w4_prefill(const GemmArgs& a, void* workspace, size_t workspac
 
 // ---- serving operators (paged.hip, attention.hip, sample.hip)
 
+// A launch takes fewer than 2^32 threads a dimension: so many workgroups of 1024,
+// beyond which appends and samplings are cut into several launches.
+constexpr int64_t kMaxGroups = ((int64_t)1 << 22) - 1;
+
 // paged.hip: the plan of a step; arguments as tq_paged_plan.
 constexpr int kPlanMaxRequests = 16384;  // prefix sums of the requests stay in LDS
 struct PlanArgs {

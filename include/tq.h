@@ -487,7 +487,8 @@ tq_status tq_kv_append(const void* q, int64_t q_stride, int64_t q_head, const vo
  *              bytes the keys of few rows are split over workgroups and the
  *              partial results joined in the kernel in split order; with less
  *              (or NULL) each row's keys are one workgroup's work.
- * All pointers of values 16-byte aligned.  T = 0 does nothing.
+ * All pointers of values 16-byte aligned.  T = 0 does nothing.  T Hq / 128 +
+ * B Hkv is below 2^24 (TQ_ERR_SHAPE).
  */
 tq_status tq_paged_attention(const void* q, int64_t q_stride, int64_t q_head, tq_dtype dt, int64_t T, int64_t Hq,
                              int64_t Hkv, int64_t D, const void* k_cache, const void* v_cache, int64_t pages,

@@ -46,3 +46,11 @@ def test_plan_outputs_side_by_side(lib):
     import torch
     if not torch.cuda.is_available():
         assert call(lib, "tq_paged_plan", PLAN, **where) == "TQ_ERR_HIP"
+
+
+@pytest.mark.parametrize("change", [
+    dict(B=1 << 24, T=1), dict(B=1 << 30, T=3), dict(T=1 << 30, B=1), dict(T=(1 << 31) - 1, Hq=64, Hkv=1),
+])
+def test_attention_of_more_workgroups_than_a_launch_takes(lib, change):
+    """Refused on the host, where a launch of 2^32 threads would be the runtime's to judge."""
+    assert call(lib, "tq_paged_attention", ATTN, **change) == "TQ_ERR_SHAPE"
