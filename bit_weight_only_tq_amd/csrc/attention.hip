@@ -654,7 +654,12 @@ __global__ __launch_bounds__(kRowsThreads, D == 64 ? 3 : 2) void rows_kernel(Att
 // 8192 tokens over 12288 keys, 32 + 8 heads of 128, bf16: 1030 to 1090 us, 1010
 // to 1070 TFLOP/s; without the overlap of scores and weights 1220 us.  The
 // matrix cores are busy 56 % of the cycles, at a clock that the card's power
-// holds at 1.7 GHz under this load.
+// holds at 1.7 GHz under this load.  Heads of 64, three waves a SIMD: 168
+// registers, of which 2 spill (12 bytes of scratch a lane, stored before the key
+// loop and read back after it); 24 decoding requests beside 9 chunks, a window of 2047: 131 to 146 us.
+// There the vector unit counts as much as the matrix cores: 3.5e8 exponentials
+// at a quarter of its rate take 36 us of it, four or five more operations a
+// score 45 us, where the products alone take 72 us of the matrix cores.
 constexpr int kTileKeys = 64;
 constexpr int kTileRows = 128;
 constexpr int kTileThreads = 256;
@@ -1080,10 +1085,25 @@ __global__ __launch_bounds__(kTileThreads, D == 64 ? 3 : 2) void tile_kernel(Att
 // launch and its tail (24 decoding requests beside 9 chunks, a window of 2047:
 // 143 us against 165; 44 requests of up to 401 keys, 13 of them chunks of 23
 // tokens at most: 14 against 31; 60 decoding requests of up to 8191 keys beside
-// 4 chunks: 697 against 728).  With one request of 30000 keys among eight, whose
-// tiles have no even shares, it is 335 against 247.  The same holds, at any
-// length, where the largest request has 64 rows at most (64 requests of up to
-// 8191 keys and 3 tokens: 233 against 310).
+// 4 chunks: 697 against 728).  The same holds, at any length, where the largest
+// request has 64 rows at most (64 requests of up to 8191 keys and 3 tokens: 233
+// against 310).
+//
+// Which side is faster hangs on how even the lengths are, which the host does
+// not see, more than on the longest of them: the tile kernel has no even shares,
+// so a decoding request much longer than the others is one long run of tiles.
+// Us in one launch and in two, by the longest request's keys:
+//                                      4096      8192     12000     16000     32000
+//   32 requests, 2 chunks of 512,
+//     lengths spread evenly           92/105   174/206   249/288   327/372   645/711
+//     one long, the others 1/16       81/42    155/51    227/64    297/75    592/141
+//   8 requests, 1 chunk of 512, even  62/67    110/106   157/152   202/189   390/370
+//   33 requests, 9 of 300, 24 + 8
+//     heads of 64, even               73/85    135/145   186/210   248/269   483/506
+//     one long                        59/29    110/42    159/52    208/57    408/91
+//   4 requests, 1 chunk of 1000, even 85/55    161/86    233/114   306/145   608/260
+// (32 + 8 heads of 128 but where given.)  kShortKeys is no crossing, then: it
+// keeps the gain of even batches up to there, and bounds what an uneven one loses.
 //
 // Rows kernel: with a workspace, the two
 // workgroups a compute unit holds take even shares of all blocks, 4 at least (a

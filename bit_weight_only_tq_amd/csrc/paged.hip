@@ -38,11 +38,11 @@ __device__ __forceinline__ int last_at_most(const int* a, int n, int x) {
 // cu[b] <= t, the i-th fresh page of b is entry head + take[b] + i of the
 // free list, and the token that begins a fresh page writes its table entry.
 //
-// One launch: 2.7 us at 8 requests, 7.3 us at 2048 requests with 65 thousand new
-// tokens, where a launch that does nothing takes about 2.  Every workgroup scans
-// all B requests by itself (2048 requests
-// are 16 KiB out of L2) rather than waiting for a scan kernel: a step this
-// small is bound by launches, not by bytes.  Workgroup 0 writes the
+// One launch: 2.7 us in the kernel at 8 requests, 7.3 us at 2048 requests with
+// 67 thousand new tokens, where empty kernels follow each other every 2.5.  Every
+// workgroup scans all B requests by itself (2048 requests are 16 KiB out of L2)
+// rather than waiting for a scan kernel: a step this small is bound by launches,
+// not by bytes.  Workgroup 0 writes the
 // per-request outputs and counts the tokens left without a slot, by ranges of
 // tokens instead of token by token; the others take the tokens.
 __global__ __launch_bounds__(1024) void plan_kernel(PlanArgs a) {
@@ -300,7 +300,11 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 }
 
 // Element form for heads, strides or pointers that 16-byte vectors do not fit:
-// one item is a pair of a rotated head or one copied value.
+// one item is a pair of a rotated head or one copied value.  Bound by the number
+// of its 2-byte accesses: 16383 tokens of 64 + 8 heads of 128 in rows of 131 take
+// 270 us (336 without rotation, whose items are single values), heads of 80 with
+// 20 rotated 302 us; a copy of as many bytes takes 142 and 88.  A single token
+// takes as long as in vectors (4.8 us a call).
 template <class E>
 __global__ __launch_bounds__(256) void append_element_kernel(AppendArgs a) {
     const int half = a.rot >> 1;
