@@ -483,6 +483,8 @@ tq_status tq_kv_append(const void* q, int64_t q_stride, int64_t q_head, const vo
  * (fp16: held 2^7 times larger, so a weight of 2^-21 of the largest or more
  * keeps all its bits.)  The weighted sum is divided by the weights' at the
  * end, so bf16 values of 2^100 and more can overflow on the way.
+ * An infinite value gives NaN to a row that sees it with a weight of zero
+ * after rounding.
  *   workspace  as for tq_gemm_ws: with tq_paged_attention_workspace_bytes()
  *              bytes the keys of few rows are split over workgroups and the
  *              partial results joined in the kernel in split order; with less
