@@ -34,8 +34,12 @@ SOURCES = {
     "paged.hip": [],
     "attention.hip": [],
     "sample.hip": [],
+    "moe.hip": [],
+    "experts.hip": [],
+    "lora.hip": [],
     "api.cpp": ["-x", "hip"],
     "api_serving.cpp": ["-x", "hip"],
+    "api_experts.cpp": ["-x", "hip"],
 }
 
 

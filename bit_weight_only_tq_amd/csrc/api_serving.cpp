@@ -8,15 +8,10 @@
 #include <hip/hip_runtime.h>
 #include <math.h>
 
+#include "tq_checks.h"
 #include "tq_internal.h"
 
 namespace {
-
-constexpr int64_t kInt32Max = 0x7FFFFFFF;
-
-bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
-
-tq_status from_hip(hipError_t e) { return e == hipSuccess ? TQ_OK : TQ_ERR_HIP; }
 
 // log2 of a page size (a power of two from 16 to 1024), or -1.
 int page_shift(int64_t page_size) {
@@ -24,16 +19,6 @@ int page_shift(int64_t page_size) {
         if (page_size == (int64_t)1 << s) return s;
     return -1;
 }
-
-// `bytes` bytes of a caller's buffer; empty ones overlap nothing.
-struct Span {
-    const void* p;
-    int64_t bytes;
-    bool overlaps(const Span& o) const {
-        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
-        return bytes > 0 && o.bytes > 0 && a < b + (uintptr_t)o.bytes && b < a + (uintptr_t)bytes;
-    }
-};
 
 }  // namespace
 

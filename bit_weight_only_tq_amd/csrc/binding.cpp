@@ -1,4 +1,4 @@
-// Python entry of the serving operators (the module _serving): tensors are
+// Python entry of the serving, expert and adapter operators (the module _serving): tensors are
 // checked, outputs allocated and the C ABI (tq.h) called on torch's current
 // stream, without Python in between.  A serving step makes these calls once a
 // layer, often on a few rows, where the host's time is the call's: an append of
@@ -7,11 +7,12 @@
 //
 // The C ABI takes bare pointers, so everything it cannot see (types, shapes,
 // strides, devices) is checked here before any call.  bit_weight_only_tq_amd/
-// serving.py has the signatures and what the arguments mean.
+// serving.py and experts.py have the signatures and what the arguments mean.
 
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -417,8 +418,242 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// ---- experts and adapters
+
+tq_dtype half_type(const char* name, const Tensor& t) {
+    if (t.scalar_type() == at::kHalf) return TQ_F16;
+    if (t.scalar_type() == at::kBFloat16) return TQ_BF16;
+    type_error(std::string(name) + " must be float16 or bfloat16, got " + c10::toString(t.scalar_type()));
+}
+// [T, n] with contiguous rows of the type; -> elements between rows.
+int64_t rows_of(const char* name, const Tensor& t, at::ScalarType type, int64_t T, int64_t n) {
+    is(name, t, type, 2);
+    if ((T >= 0 && t.size(0) != T) || (n >= 0 && t.size(1) != n))
+        value_error(std::string(name) + " must be [" + (T >= 0 ? std::to_string(T) : "rows") + ", " +
+                    (n >= 0 ? std::to_string(n) : "columns") + "], got " + shape_of(t));
+    const int64_t width = t.size(1);
+    if (width > 1 && t.stride(1) != 1) value_error("the rows of " + std::string(name) + " must be contiguous");
+    const int64_t stride = t.size(0) > 1 ? t.stride(0) : width;
+    if (stride < width) value_error("the rows of " + std::string(name) + " must not overlap");
+    return stride;
+}
+void whole_of(const char* name, const Tensor& t, at::ScalarType type, at::IntArrayRef sizes) {
+    is(name, t, type, (int64_t)sizes.size());
+    if (t.sizes() != sizes) {
+        std::string want;
+        for (int64_t s : sizes) want += (want.empty() ? "" : ", ") + std::to_string(s);
+        value_error(std::string(name) + " must be (" + want + "), got " + shape_of(t));
+    }
+    contiguous(name, t);
+}
+
+// (logits, top_k, renormalize, out, workspace)
+PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    count(n, 5);
+    const Tensor& x = tensor("logits", a[0]);
+    const int64_t k = whole("top_k", a[1]);
+    const int renorm = PyObject_IsTrue(a[2]);
+    if (renorm < 0) throw python_error();
+    if (x.dim() != 2) type_error("logits must be 2-D [T, E], got " + std::to_string(x.dim()) + "-D");
+    tq_dtype dt;
+    switch (x.scalar_type()) {
+        case at::kHalf: dt = TQ_F16; break;
+        case at::kBFloat16: dt = TQ_BF16; break;
+        case at::kFloat: dt = TQ_F32; break;
+        default: type_error("logits must be float16, bfloat16 or float32, got " + std::string(c10::toString(x.scalar_type())));
+    }
+    const int64_t T = x.size(0), E = x.size(1), stride = rows_of("logits", x, x.scalar_type(), -1, -1);
+    // the library's own limits, before anything is allocated by them
+    if (T < 1 || E < 1 || E > 1024 || k < 1 || k > E || k > 64 || T > 0x7FFFFFFF / k) return PyLong_FromLong(TQ_ERR_SHAPE);
+    const size_t need = tq_moe_route_workspace_bytes(T, E, k);
+    static const char* const names[5] = {"out.experts", "out.weights", "out.offsets", "out.rows", "out.places"};
+    static const at::ScalarType types[5] = {at::kInt, at::kFloat, at::kInt, at::kInt, at::kInt};
+    const bool own_ws = PyUnicode_Check(a[4]);  // "auto"
+    const Tensor* ws = own_ws ? nullptr : optional("workspace", a[4]);
+    OneDevice dev;
+    dev.take(x);
+    Tensor out[5];
+    const bool given = a[3] != Py_None;
+    if (given) {
+        if (!PyTuple_Check(a[3]) || PyTuple_GET_SIZE(a[3]) != 5) type_error("out must be a MoeRoute");
+        for (int i = 0; i < 5; ++i) {
+            out[i] = tensor(names[i], PyTuple_GET_ITEM(a[3], i));
+            if (i == 2) vector(names[i], out[i], types[i], E + 1);
+            else if (i == 3) vector(names[i], out[i], types[i], T * k);
+            else whole_of(names[i], out[i], types[i], {T, k});
+            dev.take(out[i]);
+        }
+    }
+    if (ws) {
+        contiguous("workspace", *ws);
+        dev.take(*ws);
+    }
+    const c10::DeviceGuard guard(x.device());
+    Tensor buffer;
+    void* pw = ws ? ws->data_ptr() : nullptr;
+    size_t ws_bytes = ws ? ws->nbytes() : 0;
+    const int64_t extra = own_ws ? (int64_t)need / 4 : 0;
+    if (!given || extra) buffer = fresh({(given ? 0 : 4 * T * k + E + 1) + extra}, x, at::kInt);
+    if (!given) {
+        int64_t at = 0;
+        for (int i = 0; i < 5; ++i) {
+            const int64_t len = i == 2 ? E + 1 : T * k;
+            out[i] = part_of(buffer, 4 * at, types[i], len);
+            if (i != 2 && i != 3) {
+                const int64_t sizes[2] = {T, k}, steps[2] = {k, 1};
+                out[i].unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef(sizes, 2), at::IntArrayRef(steps, 2), at);
+            }
+            at += len;
+        }
+    }
+    if (own_ws && need) {
+        pw = static_cast<int32_t*>(buffer.data_ptr()) + (buffer.numel() - extra);
+        ws_bytes = need;
+    }
+    const hipStream_t s = dev.stream();
+    const tq_status st = call([&] {
+        return tq_moe_route(x.data_ptr(), dt, T, E, stride, k, renorm, static_cast<int32_t*>(out[0].data_ptr()),
+                            static_cast<float*>(out[1].data_ptr()), static_cast<int32_t*>(out[2].data_ptr()),
+                            static_cast<int32_t*>(out[3].data_ptr()), static_cast<int32_t*>(out[4].data_ptr()), pw, ws_bytes, s);
+    });
+    PyObject* r;
+    if (given) {
+        Py_INCREF(a[3]);
+        r = a[3];
+    } else {
+        r = PyTuple_New(5);
+        if (!r) throw python_error();
+        for (int i = 0; i < 5; ++i) PyTuple_SET_ITEM(r, i, THPVariable_Wrap(std::move(out[i])));
+    }
+    return with_status(st, r);
+    END_HANDLE_TH_ERRORS
+}
+
+// (A, codes or qweight, scale, zeros, offsets, rows, bias, gated, out)
+PyObject* moe_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    count(n, 9);
+    const Tensor &A = tensor("A", a[0]), &w = tensor("weights", a[1]), &scale = tensor("scale", a[2]),
+                 &offsets = tensor("offsets", a[4]);
+    const Tensor *zeros = optional("zeros", a[3]), *rows = optional("rows", a[5]), *bias = optional("bias", a[6]),
+                 *given = optional("out", a[8]);
+    const int gated = PyObject_IsTrue(a[7]);
+    if (gated < 0) throw python_error();
+    if (A.dim() != 2) type_error("A must be 2-D [T, K], got " + std::to_string(A.dim()) + "-D");
+    const tq_dtype dt = half_type("A", A);
+    contiguous("A", A);
+    const int64_t T = A.size(0), K = A.size(1);
+    if (w.dim() != 3 || (w.scalar_type() != at::kByte && w.scalar_type() != at::kInt))
+        type_error("the experts' weights must be 3-D uint8 codes [E, N, K / 4] or int32 words [E, N, K / 8], got " + kind_of(w));
+    const bool w4 = w.scalar_type() == at::kInt;
+    const int64_t E = w.size(0), N = w.size(1), G = K / 128;
+    if (K % (w4 ? 128 : 64) != 0) value_error("K must be a multiple of " + std::to_string(w4 ? 128 : 64) + ", got " + std::to_string(K));
+    whole_of(w4 ? "qweight" : "codes", w, w.scalar_type(), {E, N, w4 ? K / 8 : K / 4});
+    if (w4) whole_of("scales", scale, at::kHalf, {E, N, G});
+    else whole_of("scale", scale, at::kHalf, {E, N});
+    if (zeros) {
+        if (!w4) value_error("ternary weights have no zeros");
+        whole_of("zeros", *zeros, at::kByte, {E, N, G});
+    }
+    vector("offsets", offsets, at::kInt, E + 1);
+    int64_t P = T;
+    if (rows) {
+        vector("rows", *rows, at::kInt);
+        P = rows->size(0);
+        if (T == 0 ? P != 0 : P % T != 0)
+            value_error("rows must have a multiple of A's " + std::to_string(T) + " rows, got " + std::to_string(P));
+    }
+    if (bias) whole_of("bias", *bias, A.scalar_type(), {E, N});
+    if (gated && N % 2) value_error("a gated product needs an even number of weight rows, got " + std::to_string(N));
+    const int64_t width = gated ? N / 2 : N;
+    if (given) whole_of("out", *given, A.scalar_type(), {P, width});
+    OneDevice dev;
+    for (const Tensor* t : {&A, &w, &scale, &offsets, zeros, rows, bias, given}) dev.take(t);
+    const c10::DeviceGuard guard(A.device());
+    Tensor out = given ? *given : fresh({P, width}, A, A.scalar_type());
+    const hipStream_t s = dev.stream();
+    const int32_t *po = static_cast<const int32_t*>(offsets.data_ptr()),
+                  *pr = rows ? static_cast<const int32_t*>(rows->data_ptr()) : nullptr;
+    const uint16_t* ps = static_cast<const uint16_t*>(scale.data_ptr());
+    const void* pb = bias ? bias->data_ptr() : nullptr;
+    const tq_status st = call([&] {
+        if (w4)
+            return w4a16_moe_gemm(A.data_ptr(), dt, T, P, E, N, K, static_cast<const int32_t*>(w.data_ptr()), ps,
+                                  zeros ? static_cast<const uint8_t*>(zeros->data_ptr()) : nullptr, 128, po, pr, pb, gated,
+                                  out.data_ptr(), s);
+        return tq_moe_gemm(A.data_ptr(), dt, T, P, E, N, K, static_cast<const uint8_t*>(w.data_ptr()), ps, po, pr, pb, gated,
+                           out.data_ptr(), s);
+    });
+    return with_status(st, THPVariable_Wrap(std::move(out)));
+    END_HANDLE_TH_ERRORS
+}
+
+// (y, places, weights, add, out)
+PyObject* moe_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    count(n, 5);
+    const Tensor &y = tensor("y", a[0]), &places = tensor("places", a[1]), &weights = tensor("weights", a[2]);
+    const Tensor *add = optional("add", a[3]), *given = optional("out", a[4]);
+    if (y.dim() != 2) type_error("y must be 2-D [P, N], got " + std::to_string(y.dim()) + "-D");
+    const tq_dtype dt = half_type("y", y);
+    contiguous("y", y);
+    is("places", places, at::kInt, 2);
+    contiguous("places", places);
+    const int64_t P = y.size(0), N = y.size(1), T = places.size(0), k = places.size(1);
+    whole_of("weights", weights, at::kFloat, {T, k});
+    const int64_t stride = add ? rows_of("add", *add, y.scalar_type(), T, N) : 0;
+    if (given) whole_of("out", *given, y.scalar_type(), {T, N});
+    OneDevice dev;
+    for (const Tensor* t : {&y, &places, &weights, add, given}) dev.take(t);
+    const c10::DeviceGuard guard(y.device());
+    Tensor out = given ? *given : fresh({T, N}, y, y.scalar_type());
+    const hipStream_t s = dev.stream();
+    const tq_status st = call([&] {
+        return tq_moe_combine(y.data_ptr(), dt, T, P, N, k, static_cast<const int32_t*>(places.data_ptr()),
+                              static_cast<const float*>(weights.data_ptr()), add ? add->data_ptr() : nullptr, stride,
+                              out.data_ptr(), s);
+    });
+    return with_status(st, THPVariable_Wrap(std::move(out)));
+    END_HANDLE_TH_ERRORS
+}
+
+// (x, base, A, B, ids, scale, out)
+PyObject* lora(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    count(n, 7);
+    const Tensor &x = tensor("x", a[0]), &base = tensor("base", a[1]), &A = tensor("A", a[2]), &B = tensor("B", a[3]),
+                 &ids = tensor("ids", a[4]);
+    const Tensor *scale = optional("scale", a[5]), *given = optional("out", a[6]);
+    if (x.dim() != 2) type_error("x must be 2-D [T, K], got " + std::to_string(x.dim()) + "-D");
+    const tq_dtype dt = half_type("x", x);
+    const at::ScalarType type = x.scalar_type();
+    const int64_t T = x.size(0), K = x.size(1), xs = rows_of("x", x, type, T, K);
+    const int64_t bs = rows_of("base", base, type, T, -1), N = base.size(1);
+    if (A.dim() != 3) type_error("A must be 3-D [L, rank, K], got " + std::to_string(A.dim()) + "-D");
+    const int64_t L = A.size(0), r = A.size(1);
+    whole_of("A", A, type, {L, r, K});
+    whole_of("B", B, type, {L, N, r});
+    vector("ids", ids, at::kInt, T);
+    if (scale) vector("scale", *scale, at::kFloat, L);
+    const int64_t os = given ? rows_of("out", *given, type, T, N) : N;
+    OneDevice dev;
+    for (const Tensor* t : {&x, &base, &A, &B, &ids, scale, given}) dev.take(t);
+    const c10::DeviceGuard guard(x.device());
+    Tensor out = given ? *given : fresh({T, N}, x, type);
+    const hipStream_t s = dev.stream();
+    const tq_status st = call([&] {
+        return tq_lora(x.data_ptr(), xs, base.data_ptr(), bs, dt, T, K, N, L, r, A.data_ptr(), B.data_ptr(),
+                       static_cast<const int32_t*>(ids.data_ptr()), scale ? static_cast<const float*>(scale->data_ptr()) : nullptr,
+                       out.data_ptr(), os, s);
+    });
+    return with_status(st, THPVariable_Wrap(std::move(out)));
+    END_HANDLE_TH_ERRORS
+}
+
 #define ENTRY(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {ENTRY(paged_plan), ENTRY(kv_append), ENTRY(paged_attention), ENTRY(sample), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {ENTRY(paged_plan), ENTRY(kv_append), ENTRY(paged_attention), ENTRY(sample),
+                         ENTRY(moe_route), ENTRY(moe_gemm), ENTRY(moe_combine), ENTRY(lora), {nullptr, nullptr, 0, nullptr}};
 #undef ENTRY
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -250,4 +250,78 @@ struct SampleArgs {
 };
 hipError_t launch_sample(const SampleArgs& a, hipStream_t s);
 
+// ---- experts and adapters (moe.hip, experts.hip, lora.hip)
+
+// moe.hip: the router; arguments as tq_moe_route.
+constexpr int kRouteMaxExperts = 1024;   // counts of every expert stay in LDS, one a wave
+constexpr int kRouteMaxChosen = 64;      // a lane holds one
+constexpr int64_t kRouteOneTokens = 64;  // routed and sorted by one workgroup
+constexpr int64_t kRouteMaxChunks = 256;
+constexpr int kRouteMaxLds = (16 * 1025 + 1025 + 16) * 4 + 2 * 1024 * 4 + 64 * 64 * 2;
+struct RouteArgs {
+    const void* logits;
+    int dtype;  // tq_dtype
+    int64_t T;
+    int E, k;
+    int64_t row_stride;
+    int renormalize;
+    int32_t* experts;
+    float* weights;
+    int32_t *offsets, *rows, *places;
+    uint32_t* counts;   // [chunks][E], more than kRouteOneTokens tokens
+    int64_t chunk = 0;  // tokens of a workgroup, set by the launcher (0: one workgroup)
+};
+int64_t route_chunk(int64_t T);  // tokens of a chunk, 0 where one workgroup takes all
+hipError_t launch_moe_route(const RouteArgs& a, hipStream_t s);
+
+// moe.hip: arguments as tq_moe_combine.
+struct CombineArgs {
+    const uint16_t* y;
+    int bf16;
+    int64_t T, P, N;
+    int k;
+    const int32_t* places;
+    const float* weights;
+    const uint16_t* add;  // or nullptr
+    int64_t add_stride;
+    uint16_t* out;
+};
+hipError_t launch_moe_combine(const CombineArgs& a, hipStream_t s);
+
+// experts.hip: arguments as tq_moe_gemm and w4a16_moe_gemm.
+struct ExpertArgs {
+    const uint16_t* A;      // [T, K]
+    int bf16;
+    int64_t T, P, E, N, K;
+    int fmt;                // 0: ternary, 1: W4A16
+    const uint8_t* w;       // packed weights [E, N, K / 4 or K / 2 bytes]
+    const uint16_t* scale;  // [E, N] or [E, N, K / 128]
+    const uint8_t* zeros;   // W4A16: [E, N, K / 128] or nullptr
+    const int32_t* offsets; // [E + 1]
+    const int32_t* rows;    // [P] or nullptr: row p of A is row p of C
+    int fan;                // P / T with rows
+    const uint16_t* bias;   // [E, N] or nullptr
+    uint16_t* C;            // [P, N], [P, N / 2] gated
+    int gated;
+    int64_t first = 0;      // workgroup that this launch begins with (set by the launcher)
+};
+hipError_t launch_experts(const ExpertArgs& a, hipStream_t s);
+
+// lora.hip: arguments as tq_lora.
+struct LoraArgs {
+    const uint16_t* x;
+    int64_t x_stride;
+    const uint16_t* base;
+    int64_t base_stride;
+    int bf16;
+    int64_t T, K, N, L;
+    int r;
+    const uint16_t *A, *B;  // [L, r, K], [L, N, r]
+    const int32_t* ids;     // [T]
+    const float* scale;     // [L] or nullptr
+    uint16_t* out;
+    int64_t out_stride;
+};
+hipError_t launch_lora(const LoraArgs& a, hipStream_t s);
+
 }  // namespace tq

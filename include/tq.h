@@ -530,6 +530,119 @@ tq_status tq_sample(const void* logits, tq_dtype dt, int64_t B, int64_t V, int64
                     const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
                     int32_t* tokens, float* logprobs, hipStream_t stream);
 
+/* ------------------------------------------------------ experts and adapters
+ *
+ * A model may have E experts in place of one MLP, each with packed weights of
+ * its own, stacked: codes [E][N][K / 4] with scales [E][N], or qweight
+ * [E][N][K / 8] with scales and zero points [E][N][K / 128].  That is what
+ * tq_pack and the w4a16 packs write for E * N rows.  And it may be served with
+ * low-rank adapters beside its packed projections.
+ *
+ * A token t takes top_k experts: its pairs t * top_k + j.  A step routes
+ * (tq_moe_route), multiplies each expert's rows (tq_moe_gemm, w4a16_moe_gemm) and
+ * sums each token's rows (tq_moe_combine).
+ *
+ * All calls are asynchronous on `stream`, allocate nothing, never synchronize
+ * and can be captured in a graph.  Offsets, rows, places and ids are device data
+ * that the host does not see: no value in them makes a call read or write
+ * outside the buffers it was given.
+ */
+
+/*
+ * tq_moe_route - the experts of each token, and the pairs sorted by expert.
+ *   logits     [T][E] in `dt` (TQ_F16, TQ_BF16 or TQ_F32), row_stride elements
+ *              between rows, any alignment.  NaN counts as -inf, and an expert
+ *              at -inf is never chosen.
+ *   experts    [T][top_k] the experts of the largest logits, largest first,
+ *              equal ones by index; -1 where there is none left (written).
+ *   weights    [T][top_k] fp32 (written): exp(x - max x) of each over the sum
+ *              of the chosen ones (renormalize) or of all; 0 where none is left.
+ *              Infinite logits share the weight.
+ *   offsets    [E + 1]: expert e has the places offsets[e] .. offsets[e + 1] - 1
+ *              (written).
+ *   rows       [T * top_k]: the pair at each place, in ascending order within an
+ *              expert; pairs without an expert follow behind offsets[E] (written).
+ *   places     [T][top_k] the place of each pair, -1 without an expert (written).
+ *   workspace  tq_moe_route_workspace_bytes() bytes, 4-byte aligned, of any
+ *              contents; TQ_ERR_SHAPE if it is smaller.
+ * 1 <= T, 1 <= E <= 1024, top_k at most E and 64, T * top_k below 2^31.  Outputs
+ * and workspace must not overlap each other or the logits (TQ_ERR_VALUE).
+ */
+tq_status tq_moe_route(const void* logits, tq_dtype dt, int64_t T, int64_t E, int64_t row_stride, int64_t top_k,
+                       int renormalize, int32_t* experts, float* weights, int32_t* offsets, int32_t* rows,
+                       int32_t* places, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace tq_moe_route needs (0: none, up to 64 tokens; or invalid arguments). */
+size_t tq_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t top_k);
+
+/*
+ * tq_moe_gemm - rows grouped by expert times their experts' ternary weights.
+ *   A        [T][K] in `dt`.
+ *   codes, scale_f16  [E][N][K / 4] and [E][N].
+ *   offsets  [E + 1], as of tq_moe_route.
+ *   rows     [P] or NULL.  Row p of C, offsets[e] <= p < offsets[e + 1], is made
+ *            from row rows[p] / (P / T) of A (P a multiple of T), or from row p
+ *            (P = T) without rows.
+ *   bias     [E][N] in `dt` or NULL.
+ *   gated    0: C[p] = A_row W[e]^T + bias[e], C is [P][N].  1: the first N / 2
+ *            weight rows are a gate, the others an up projection, and
+ *            C[p] = gate / (1 + exp(-gate)) * up, C is [P][N / 2]; gate and up
+ *            stay in fp32.
+ *   C        (written) rounded once from fp32; rows behind offsets[E] are left
+ *            as they were.
+ * Offsets are held to [0, P] and rows to [0, P); where they are not what
+ * tq_moe_route writes, which rows of C are written is unspecified.
+ * K % 64 == 0, K and N at most 2^22, E <= 65536, N even if gated.  A and codes are
+ * 16-byte aligned.  The sums' order depends on P, E and N alone.
+ */
+tq_status tq_moe_gemm(const void* A, tq_dtype dt, int64_t T, int64_t P, int64_t E, int64_t N, int64_t K,
+                      const uint8_t* codes, const uint16_t* scale_f16, const int32_t* offsets, const int32_t* rows,
+                      const void* bias, int gated, void* C, hipStream_t stream);
+
+/*
+ * w4a16_moe_gemm - the same with W4A16 experts: qweight [E][N][K / 8], scales_f16
+ * and zeros [E][N][K / 128] (zeros may be NULL: 8).  K % 128 == 0.
+ */
+tq_status w4a16_moe_gemm(const void* A, tq_dtype dt, int64_t T, int64_t P, int64_t E, int64_t N, int64_t K,
+                         const int32_t* qweight, const uint16_t* scales_f16, const uint8_t* zeros, int64_t group_size,
+                         const int32_t* offsets, const int32_t* rows, const void* bias, int gated, void* C,
+                         hipStream_t stream);
+
+/*
+ * tq_moe_combine - the weighted sum of each token's rows.
+ *   y        [P][N] in `dt`, the rows by place.
+ *   places, weights  [T][top_k]; a place outside [0, P) adds nothing.
+ *   add      [T][N] in `dt`, add_stride elements between rows, or NULL.
+ *   out      [T][N] (written): add[t] + sum over j of weights[t][j] y[places[t][j]],
+ *            in fp32 in the order of j, rounded once.  It may be `add` itself
+ *            and must not overlap anything else (TQ_ERR_VALUE).
+ */
+tq_status tq_moe_combine(const void* y, tq_dtype dt, int64_t T, int64_t P, int64_t N, int64_t top_k,
+                         const int32_t* places, const float* weights, const void* add, int64_t add_stride, void* out,
+                         hipStream_t stream);
+
+/*
+ * tq_lora - the low-rank updates of many requests' adapters, added to what the
+ * shared projection gave.
+ *   x        [T][K] in `dt`, x_stride elements between rows.
+ *   base     [T][N], base_stride between rows.
+ *   A, B     [L][rank][K] and [L][N][rank] in `dt`: L adapters.  One of a smaller
+ *            rank is filled up with zeros.
+ *   ids      [T] each row's adapter; outside [0, L): none.
+ *   scale    [L] fp32, or NULL for 1.
+ *   out      [T][N], out_stride between rows (written):
+ *            base[t] + scale[l] (x[t] A[l]^T) B[l]^T, or base[t] without an
+ *            adapter.  It may be `base` itself (rows without an adapter are then
+ *            left alone) and must not overlap anything else (TQ_ERR_VALUE).
+ * Sums are fp32, and the result is rounded once: x A^T enters the second product
+ * with at least 16 bits of the row's largest value.
+ * rank % 8 == 0, rank <= 256; K % 8 == 0; K, N <= 2^22; T <= 2^27.  x, A and B are
+ * 16-byte aligned and x_stride is a multiple of 8.
+ */
+tq_status tq_lora(const void* x, int64_t x_stride, const void* base, int64_t base_stride, tq_dtype dt, int64_t T,
+                  int64_t K, int64_t N, int64_t L, int64_t rank, const void* A, const void* B, const int32_t* ids,
+                  const float* scale, void* out, int64_t out_stride, hipStream_t stream);
+
 /* ----------------------------------------------------------- measurement
  *
  * Instruments for the benchmark, not part of the layer: they measure the
