@@ -21,7 +21,7 @@ tq_status moe_gemm(const void* A, tq_dtype dt, int64_t T, int64_t P, int64_t E, 
                    const int32_t* rows, const void* bias, int gated, void* C, hipStream_t stream) {
     if (dt != TQ_F16 && dt != TQ_BF16) return TQ_ERR_DTYPE;
     if (T < 0 || T > kInt32Max || P < 0 || P > kInt32Max || E <= 0 || E > 65536 || N <= 0 || N > tq::kMaxK || K <= 0 ||
-        K > tq::kMaxK || K % (fmt == 0 ? 64 : 128) != 0 || (gated && N % 2 != 0))
+        K > tq::kMaxK || K % (fmt == 0 ? 64 : 128) != 0 || (gated && N % 2 != 0) || N * K > (int64_t)1 << 32)
         return TQ_ERR_SHAPE;
     if (rows ? (T == 0 ? P != 0 : P % T != 0) : P != T) return TQ_ERR_SHAPE;
     if (P == 0) return TQ_OK;

@@ -592,7 +592,8 @@ size_t tq_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t top_k);
  *            as they were.
  * Offsets are held to [0, P] and rows to [0, P); where they are not what
  * tq_moe_route writes, which rows of C are written is unspecified.
- * K % 64 == 0, K and N at most 2^22, E <= 65536, N even if gated.  A and codes are
+ * K % 64 == 0, K and N at most 2^22, N * K at most 2^32, E <= 65536, N even if
+ * gated.  A and codes are
  * 16-byte aligned.  The sums' order depends on P, E and N alone.
  */
 tq_status tq_moe_gemm(const void* A, tq_dtype dt, int64_t T, int64_t P, int64_t E, int64_t N, int64_t K,
@@ -601,7 +602,9 @@ tq_status tq_moe_gemm(const void* A, tq_dtype dt, int64_t T, int64_t P, int64_t 
 
 /*
  * w4a16_moe_gemm - the same with W4A16 experts: qweight [E][N][K / 8], scales_f16
- * and zeros [E][N][K / 128] (zeros may be NULL: 8).  K % 128 == 0.
+ * and zeros [E][N][K / 128] (zeros may be NULL: 8).  K % 128 == 0.  Sums may be
+ * held in units of a group's scale on the way, so bf16 activations of 2^60 and
+ * more can overflow between groups whose scales differ by 2^40.
  */
 tq_status w4a16_moe_gemm(const void* A, tq_dtype dt, int64_t T, int64_t P, int64_t E, int64_t N, int64_t K,
                          const int32_t* qweight, const uint16_t* scales_f16, const uint8_t* zeros, int64_t group_size,

@@ -176,3 +176,36 @@ def test_same_bits_again_and_in_a_graph(fmt, counts):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("counts", [[3, 2], [50, 20], [200, 3]])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_scales_of_zero_and_of_every_size(fmt, counts, dt):
+    """Groups whose scale is 0 (whole rows of them, the first and the last group), and scales from 2^-24 to 2^9 beside each other."""
+    import torch
+    log(f"experts {fmt} {dt} scales counts={counts}")
+    d, h = make(fmt, 2, 96, 1024, counts, dt, 13)
+    rng = np.random.default_rng(14)
+    old = values(d["packed"]["scale"])
+    scale = 2.0 ** rng.integers(-24, 10, old.shape) * (1 + rng.integers(0, 4, old.shape) / 4)
+    scale = scale.astype(np.float16).astype(np.float64)
+    scale[:, 5:20:3] = 0.0
+    if fmt != "ternary":
+        scale[:, 30:60][rng.random(scale[:, 30:60].shape) < 0.5] = 0.0
+        scale[:, 60, 0] = scale[:, 61, -1] = 0.0
+        W = h["W"].reshape(2, 96, 8, 128) / old[..., None] * scale[..., None]
+    else:
+        W = h["W"] / old[..., None] * scale[..., None]
+    h["W"] = W.reshape(2, 96, 1024)
+    d["packed"]["scale"].copy_(torch.from_numpy(scale).half())
+    for gated in (False, True):
+        out = torch.full((h["P"], 48 if gated else 96), 123.0, dtype=d["A"].dtype, device=d["A"].device)
+        got = values(call(d["A"], d["packed"], d["off"], gated=gated, out=out))
+        C, mag = OE.product(h["A"], h["W"], h["off"])
+        want, bound = (OE.gated(C), gated_bound(1024, C, mag)) if gated else (C, sum_bound(1024, mag))
+        over = {"f16": 65520.0, "bf16": 3.3961775e38}[dt]
+        fine = np.abs(want) + bound < over
+        assert_within(got[fine], want[fine], rounded(dt, bound, want)[fine], "scales")
+        past = np.abs(want) - bound >= over  # a value within the bound of want is then past the type's range
+        assert np.array_equal(got[past], np.sign(want[past]) * np.inf)
