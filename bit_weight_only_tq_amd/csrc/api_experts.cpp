@@ -147,12 +147,15 @@ tq_status tq_lora(const void* x, int64_t x_stride, const void* base, int64_t bas
                   const float* scale, void* out, int64_t out_stride, hipStream_t stream) {
     if (dt != TQ_F16 && dt != TQ_BF16) return TQ_ERR_DTYPE;
     if (T < 0 || T > ((int64_t)1 << 27) || K <= 0 || K > tq::kMaxK || K % 8 != 0 || N <= 0 || N > tq::kMaxK || L <= 0 ||
-        L > kInt32Max || rank <= 0 || rank > 256 || rank % 8 != 0)
+        L > kInt32Max || rank <= 0 || rank > 256 || rank % 8 != 0 || rank * K > tq::kLoraMaxAdapter ||
+        rank * N > tq::kLoraMaxAdapter)
         return TQ_ERR_SHAPE;
-    if (T > 1 && (x_stride < K || base_stride < N || out_stride < N)) return TQ_ERR_VALUE;
+    if (T == 1) x_stride = K, base_stride = out_stride = N;  // not looked at
+    for (const int64_t* s : {&x_stride, &base_stride, &out_stride})
+        if (*s < (s == &x_stride ? K : N) || *s > tq::kLoraMaxStride) return TQ_ERR_VALUE;
     if (T == 0) return TQ_OK;
     if (!x || !base || !A || !B || !ids || !out) return TQ_ERR_NULL;
-    if (!aligned(x, 16) || (T > 1 && x_stride % 8) || !aligned(A, 16) || !aligned(B, 16) || !aligned(base, 2) ||
+    if (!aligned(x, 16) || x_stride % 8 || !aligned(A, 16) || !aligned(B, 16) || !aligned(base, 2) ||
         !aligned(out, 2) || !aligned(ids, 4) || !aligned(scale, 4))
         return TQ_ERR_ALIGN;
     // the update may be made in place; nothing else that is read may be written
@@ -161,7 +164,7 @@ tq_status tq_lora(const void* x, int64_t x_stride, const void* base, int64_t bas
                          {scale, scale ? L * 4 : 0}};
     for (const Span& s : from)
         if (to.overlaps(s)) return TQ_ERR_VALUE;
-    if (!(base == out && (T == 1 || base_stride == out_stride)) && to.overlaps(Span{base, ((T - 1) * base_stride + N) * 2}))
+    if (!(base == out && base_stride == out_stride) && to.overlaps(Span{base, ((T - 1) * base_stride + N) * 2}))
         return TQ_ERR_VALUE;
     tq::LoraArgs a{};
     a.x = static_cast<const uint16_t*>(x);

@@ -307,7 +307,10 @@ struct ExpertArgs {
 };
 hipError_t launch_experts(const ExpertArgs& a, hipStream_t s);
 
-// lora.hip: arguments as tq_lora.
+// lora.hip: arguments as tq_lora.  A block's rows and an adapter's matrices are
+// addressed with 31 bits.
+constexpr int64_t kLoraMaxAdapter = (int64_t)1 << 29;  // values of one matrix
+constexpr int64_t kLoraMaxStride = (int64_t)1 << 25;
 struct LoraArgs {
     const uint16_t* x;
     int64_t x_stride;
@@ -321,6 +324,8 @@ struct LoraArgs {
     const float* scale;     // [L] or nullptr
     uint16_t* out;
     int64_t out_stride;
+    // set by the launcher: blocks of rows, adapters of a block at most, columns of a workgroup
+    int64_t blocks = 0, slots = 0, chunks = 0, cols = 0;
 };
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s);
 

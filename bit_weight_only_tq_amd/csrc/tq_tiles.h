@@ -25,6 +25,19 @@ template <> struct Mfma<BF16> {
     }
 };
 
+// Two values rounded to the activation type by the hardware's conversion (to
+// nearest even, infinities and NaN kept), in one word.
+template <class T>
+__device__ __forceinline__ uint32_t round_pair(float lo, float hi) {
+    if constexpr (std::is_same<T, F16>::value) return __builtin_bit_cast(uint32_t, f16x2{(_Float16)lo, (_Float16)hi});
+    else return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});
+}
+template <class T>
+__device__ __forceinline__ uint16_t round_one(float v) {
+    if constexpr (std::is_same<T, F16>::value) return __builtin_bit_cast(uint16_t, (_Float16)v);
+    else return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
 // Natural-order operand pairs of byte b of a code dword x (fields f_4b ..
 // f_4b+3 at bits 0, 2, 4, 6 of the byte): one byte permute puts the byte in
 // the low byte of both halves, a mask into 1024.0 keeps field 4b (low half)

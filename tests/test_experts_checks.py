@@ -108,7 +108,9 @@ def _lora(**c):
     (dict(bs=31), "TQ_ERR_VALUE"), (dict(os=31), "TQ_ERR_VALUE"), (dict(xs=68), "TQ_ERR_ALIGN"), (dict(x=V(0x10008)), "TQ_ERR_ALIGN"),
     (dict(A=V(0x10008)), "TQ_ERR_ALIGN"), (dict(B=V(0x10008)), "TQ_ERR_ALIGN"), (dict(out=V(0x10001)), "TQ_ERR_ALIGN"),
     (dict(out=P(0)), "TQ_ERR_VALUE"), (dict(out=P(2)), "TQ_ERR_VALUE"), (dict(out=V((2 << 36) + 64)), "TQ_ERR_VALUE"),
-    (dict(out=P(1), os=40), "TQ_ERR_VALUE"), (dict(T=0), "TQ_OK"),
+    (dict(out=P(1), os=40), "TQ_ERR_VALUE"), (dict(T=0), "TQ_OK"), (dict(xs=(1 << 25) + 8), "TQ_ERR_VALUE"),
+    (dict(os=(1 << 25) + 1), "TQ_ERR_VALUE"), (dict(K=1 << 22, xs=1 << 22, r=136), "TQ_ERR_SHAPE"),
+    (dict(N=1 << 22, bs=1 << 22, os=1 << 22, r=256), "TQ_ERR_SHAPE"),
 ])
 def test_lora(change, want):
     assert _lora(**change) == want
