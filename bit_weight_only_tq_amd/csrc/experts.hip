@@ -13,59 +13,78 @@ namespace tq {
 
 namespace {
 
-// Block `y` of BM rows among all experts' blocks (an expert's last one may have
-// fewer rows): its expert, first row and number of rows; rows 0: no such block.
-// Offsets are held to [0, P], so nothing outside A and C is named by any values.
+// A block of BM rows (an expert's last one may have fewer): its expert, first row
+// and number of rows; rows 0: no such block.
 struct Block {
     int expert;
     int64_t row;
     int rows;
 };
-__device__ __forceinline__ Block find_block(const int32_t* offsets, int E, int64_t P, int BM, int64_t y) {
-    const int lane = threadIdx.x & 63;
-    int64_t before = 0;  // blocks of the experts before this 64
-    for (int e0 = 0; e0 < E; e0 += 64) {
-        const int e = e0 + lane;
-        int64_t lo = 0, hi = 0;
-        if (e < E) {
-            lo = offsets[e];
-            hi = offsets[e + 1];
-            lo = lo < 0 ? 0 : lo > P ? P : lo;
-            hi = hi < lo ? lo : hi > P ? P : hi;
-        }
-        const int n = (int)((hi - lo + BM - 1) / BM);
-        int sum = n;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int o = __shfl_up(sum, d, kWave);
-            if (lane >= d) sum += o;
-        }
-        const uint64_t past = __ballot(before + sum > y);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            const int64_t first = before + __builtin_amdgcn_readlane(sum - n, l);
-            const int64_t row = __builtin_amdgcn_readlane((int)lo, l) + (y - first) * BM;
-            const int64_t end = __builtin_amdgcn_readlane((int)hi, l);
-            return Block{e0 + l, row, (int)(end - row < BM ? end - row : BM)};
-        }
-        before += __builtin_amdgcn_readlane(sum, 63);
-    }
-    return Block{0, 0, 0};
+
+// Inclusive sum over the wave: shifts within the rows of 16 lanes, then the rows'
+// last lanes to the rows behind them.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15 to rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31 to rows 2 and 3
+    return v;
 }
 
-// All experts' blocks.
-__device__ __forceinline__ int64_t count_blocks(const int32_t* offsets, int E, int64_t P, int BM) {
+// All experts' blocks: a lane has the blocks of V experts in a row.  Offsets are
+// held to [0, P], so nothing outside A and C is named by any values.
+struct Blocks {
+    int V, sum;  // blocks up to and with this lane's experts
+    int own;     // of its own
+    int total;
+};
+struct Rows {
+    int lo, hi;
+};
+__device__ __forceinline__ Rows rows_of(const ExpertArgs& a, int e) {
+    const int P = (int)a.P;
+    const bool in = (uint32_t)e < (uint32_t)a.E;
+    int lo = in ? a.offsets[e] : 0, hi = in ? a.offsets[e + 1] : 0;
+    lo = lo < 0 ? 0 : lo > P ? P : lo;
+    hi = hi < lo ? lo : hi > P ? P : hi;
+    return Rows{lo, hi};
+}
+__device__ __forceinline__ Blocks count_blocks(const ExpertArgs& a, int BM) {
     const int lane = threadIdx.x & 63;
-    int sum = 0;  // a lane's experts: their rows are at most P together where offsets ascend
-    for (int e = lane; e < E; e += 64) {
-        int64_t lo = offsets[e], hi = offsets[e + 1];
-        lo = lo < 0 ? 0 : lo > P ? P : lo;
-        hi = hi < lo ? lo : hi > P ? P : hi;
-        sum += (int)((hi - lo + BM - 1) / BM);
+    Blocks b;
+    b.V = ((int)a.E + 63) / 64;
+    b.own = 0;
+    for (int v = 0; v < b.V; ++v) {
+        const Rows r = rows_of(a, lane * b.V + v);
+        b.own += (int)(((uint32_t)(r.hi - r.lo) + BM - 1) / (uint32_t)BM);
     }
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d, kWave);
-    return __builtin_amdgcn_readfirstlane(sum);
+    b.sum = wave_scan(b.own);
+    b.total = __builtin_amdgcn_readlane(b.sum, 63);
+    return b;
+}
+// Block y < total.
+__device__ __forceinline__ Block find_block(const ExpertArgs& a, const Blocks& b, int BM, int y) {
+    const int lane = threadIdx.x & 63;
+    const int l = __builtin_ctzll(__ballot(b.sum > y));
+    int left = y - __builtin_amdgcn_readlane(b.sum - b.own, l);
+    // the experts of lane l, 64 at a time (one where V is 1)
+    for (int v0 = 0;; v0 += 64) {
+        const int v = v0 + lane;
+        Rows r = rows_of(a, v < b.V ? l * b.V + v : (int)a.E);
+        const int n = (int)(((uint32_t)(r.hi - r.lo) + BM - 1) / (uint32_t)BM);
+        const int sum = wave_scan(n);
+        const uint64_t past = __ballot(sum > left);
+        if (past) {
+            const int w = __builtin_ctzll(past);
+            const int row = __builtin_amdgcn_readlane(r.lo, w) + (left - __builtin_amdgcn_readlane(sum - n, w)) * BM;
+            const int end = __builtin_amdgcn_readlane(r.hi, w);
+            return Block{l * b.V + v0 + w, row, end - row < BM ? end - row : BM};
+        }
+        left -= __builtin_amdgcn_readlane(sum, 63);
+        if (v0 + 64 >= b.V) return Block{0, 0, 0};
+    }
 }
 
 // The row of A that row p of C is made from; entries of `rows` outside [0, P)
@@ -78,156 +97,6 @@ __device__ __forceinline__ int64_t source_row(const ExpertArgs& a, int64_t p) {
 }
 
 __device__ __forceinline__ float gate(float g, float u) { return g / (1.0f + expf(-g)) * u; }
-
-// ---------------------------------------------------------------- few rows
-//
-// 16 rows of one expert and R blocks of 16 weight rows a workgroup, its waves
-// dealing the columns.  A wave reads weights and activations straight into
-// matrix operands: lane 16 g + i has 16 bytes of codes of weight row i and the
-// activations of the same columns of row i (natural order, tq_tiles.h).
-// W4A16: a step is one scale group of 128 columns, its sum starts from zero and
-// is scaled into the result; ternary: 256 columns, scaled at the end.  The waves'
-// results meet in LDS and are summed in the waves' order.
-// Gated: the first half of the R blocks are rows of the gate, the second half the
-// same rows of the up projection.
-constexpr int kStreamWaves = 8;
-
-template <class T, int FMT, bool ASYM, bool GATED, int R>
-__global__ __launch_bounds__(kStreamWaves * kWave) void stream_kernel(ExpertArgs a) {
-    typedef typename Mfma<T>::vec vec;
-    constexpr int kCols = FMT == 0 ? 256 : 128;  // of a step
-    constexpr int kUnits = FMT == 0 ? 8 : 4;     // 8-column units a lane and step
-    constexpr int kOut = GATED ? R / 2 : R;      // blocks of 16 output columns
-    __shared__ f32x4 red[kStreamWaves][R][kWave];
-    const int64_t id = a.first + blockIdx.x;
-    const int64_t tiles = ((GATED ? a.N / 2 : a.N) + 16 * kOut - 1) / (16 * kOut);
-    const Block blk = find_block(a.offsets, (int)a.E, a.P, 16, id / tiles);
-    if (blk.rows == 0) return;
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int g = lane >> 4, i16 = lane & 15;
-    const int64_t N = a.N, K = a.K;
-    const int64_t width = GATED ? N / 2 : N;       // output columns
-    const int64_t n0 = id % tiles * (16 * kOut);
-    const int64_t rb = FMT == 0 ? K / 4 : K / 2;   // code bytes of a weight row
-    const int64_t G = K / 128;
-    const bool live = i16 < blk.rows;
-    const uint16_t* arow = a.A + (live ? source_row(a, blk.row + i16) : 0) * K;
-    int64_t wr[R];  // weight rows (past the end: the last)
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int64_t c = n0 + 16 * (r % kOut) + i16;
-        wr[r] = (int64_t)blk.expert * N + (c < width ? c : width - 1) + (r >= kOut ? width : 0);
-    }
-    const int steps = (int)((K + kCols - 1) / kCols);
-    const int from = (int)((int64_t)steps * wave / kStreamWaves), to = (int)((int64_t)steps * (wave + 1) / kStreamWaves);
-    const uint32_t magic_v = vgpr_const<kMagic2>();
-    const uint32_t mask_v = sgpr_const<0x00F0000Fu>();
-    const f16x2 mul = __builtin_bit_cast(f16x2, 0x2C003C00u);  // (1, 1/16)
-    const NatConsts nat = nat_consts();
-    f32x4 acc[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int step = from; step < to; ++step) {
-        const int64_t c0 = (int64_t)step * kCols + g * (kCols / 4);  // this lane's columns
-        const bool in = FMT == 1 || c0 < K;                          // ternary: K is a multiple of 64 alone
-        uint4 q[R], av[kUnits];
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            q[r] = in ? *reinterpret_cast<const uint4*>(a.w + wr[r] * rb + (FMT == 0 ? c0 / 4 : c0 / 2)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u)
-            av[u] = in && live ? *reinterpret_cast<const uint4*>(arow + c0 + 8 * u) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            if constexpr (FMT == 0) {
-#pragma unroll
-                for (int u = 0; u < kUnits; ++u) {
-                    const uint32_t x = dword_of(q[r], u / 2);
-                    const uint4 b = u % 2 ? nat_quad<1>(x, magic_v, nat) : nat_quad<0>(x, magic_v, nat);
-                    acc[r] = Mfma<T>::mma(__builtin_bit_cast(vec, av[u]), __builtin_bit_cast(vec, b), acc[r]);
-                }
-            } else {
-                f16x2 sub = w4_nat_sub(8u);
-                if constexpr (ASYM) sub = w4_nat_sub(a.zeros[wr[r] * G + step]);
-                f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int u = 0; u < kUnits; ++u) {
-                    const uint4 b = nat_w4_quad<T>(dword_of(q[r], u), mask_v, magic_v, mul, sub);
-                    sum = Mfma<T>::mma(__builtin_bit_cast(vec, av[u]), __builtin_bit_cast(vec, b), sum);
-                }
-                const float s = f16_bits_to_f32(a.scale[wr[r] * G + step]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[r][i] = fmaf(s, sum[i], acc[r][i]);
-            }
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) red[wave][r][lane] = acc[r];
-    __syncthreads();
-    for (int t = threadIdx.x; t < kOut * kWave; t += kStreamWaves * kWave) {
-        const int r = t / kWave, l = t % kWave;
-        const int64_t c = n0 + 16 * r + (l & 15);
-        if (c >= width) continue;
-        f32x4 v = red[0][r][l];
-        for (int w = 1; w < kStreamWaves; ++w) v += red[w][r][l];
-        f32x4 u = v;
-        if constexpr (GATED) {
-            u = red[0][r + kOut][l];
-            for (int w = 1; w < kStreamWaves; ++w) u += red[w][r + kOut][l];
-        }
-        const int64_t n = (int64_t)blk.expert * N + c;
-        float sv = 1.0f, su = 1.0f;
-        if constexpr (FMT == 0) {
-            sv = f16_bits_to_f32(a.scale[n]) * Mfma<T>::kUnit;
-            if constexpr (GATED) su = f16_bits_to_f32(a.scale[n + width]) * Mfma<T>::kUnit;
-        }
-        const float bv = a.bias ? T::to_f32(a.bias[n]) : 0.0f;
-        const float bu = GATED && a.bias ? T::to_f32(a.bias[n + width]) : 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = 4 * (l >> 4) + i;
-            if (row >= blk.rows) continue;
-            float y = fmaf(v[i], sv, bv);
-            if constexpr (GATED) y = gate(y, fmaf(u[i], su, bu));
-            a.C[(blk.row + row) * width + c] = T::from_f32_fast(y);
-        }
-    }
-}
-
-// ---------------------------------------------------------------- many rows
-//
-// BM rows of one expert and 256 weight rows a workgroup, four waves of BM x 64.
-// Activations and codes come by DMA (no registers) into a ring of three stages of
-// 64 columns, two ahead of the matrix cores: BM rows x 128 bytes, 16-byte chunks
-// XOR-swizzled (chunk c of row r at c ^ (r % 8)), and 256 weight rows x 16 or 32
-// bytes.  Codes are unpacked in registers in the natural order of their columns.
-// Two workgroups share a compute unit, so one's barriers lie under the other's
-// products.
-//
-// W4A16: the accumulators hold the sum in units of the current group's scale, so
-// entering a group multiplies them by the ratio of the last scale to its own, and
-// the operands stay the exact q - z.  (Scaling every group's sum into a second set
-// of accumulators costs as many instructions and twice the registers, which
-// halves the tile.)  A group whose scale is 0 keeps the last unit, and its code
-// words are replaced by those of zero weights.
-namespace tile {
-
-constexpr int BN = 256, BK = 64, WN = 64, TN = 4;
-constexpr int kWaves = 4, kThreads = kWaves * kWave;
-constexpr int kStages = 3;
-constexpr int kEpiLd = WN + 8;  // halves of a row staged for its store
-constexpr int kGroupRows = 8;   // blocks of rows that pass over all columns together
-
-template <int FMT, int BM>
-struct Ring {
-    static constexpr int kABytes = BM * BK * 2;
-    static constexpr int kBBytes = BN * BK / (FMT == 0 ? 4 : 2);
-    static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kBytes = kStages * kStageBytes;
-    static constexpr int AU = BM / 32, BU = kBBytes / 4096;  // 1-KB transfers a wave and stage
-    static_assert(kWaves * 32 * kEpiLd * 2 <= kBytes, "epilogue staging must fit in the ring");
-};
 
 // Eight columns of a code word as exact operands.  fp16: q - z (add: the packed
 // constants of z).  bf16: (q - z) / 16, two nibbles' signed values by the
@@ -277,6 +146,8 @@ struct W4Unpack<BF16, ASYM> {
     }
 };
 
+constexpr int kGroupRows = 8;  // blocks of rows that pass over all columns together
+
 // The tile of workgroup `id`: workgroups go to the XCDs (each with an L2 of its
 // own) in turn, so each XCD takes a contiguous share of the tiles, in the order
 // of kGroupRows blocks of rows over all columns.
@@ -285,18 +156,315 @@ struct Place {
     int n_tile;
 };
 __device__ __forceinline__ Place find_tile(const ExpertArgs& a, int BM, uint32_t tiles_n, uint32_t id) {
-    const uint32_t blocks = (uint32_t)count_blocks(a.offsets, (int)a.E, a.P, BM);
-    const uint32_t total = blocks * tiles_n;  // below 2^31: the launcher's check
+    const Blocks b = count_blocks(a, BM);
+    const uint32_t total = (uint32_t)b.total * tiles_n;  // below 2^31: the launcher's check
     const uint32_t xcd = id & 7, s = id >> 3, per = total / 8, more = total % 8;
     if (s >= per + (xcd < more ? 1 : 0)) return Place{Block{0, 0, 0}, 0};
     const uint32_t tile = xcd * per + (xcd < more ? xcd : more) + s;
     const uint32_t band = tile / (kGroupRows * tiles_n), in = tile - band * kGroupRows * tiles_n;
-    const uint32_t left = blocks - band * kGroupRows;
+    const uint32_t left = (uint32_t)b.total - band * kGroupRows;
     const uint32_t rows = left < kGroupRows ? left : kGroupRows;
     const int n_tile = __builtin_amdgcn_readfirstlane((int)(in / rows));
     const int y = __builtin_amdgcn_readfirstlane((int)(band * kGroupRows + in % rows));
-    return Place{find_block(a.offsets, (int)a.E, a.P, BM, y), n_tile};
+    return Place{find_block(a, b, BM, y), n_tile};
 }
+
+// ---------------------------------------------------------------- few rows
+//
+// BM rows of one expert (16, or 4 where experts have one or two: a matrix tile
+// has 16 either way) and 32 weight rows a wave.  The call is bound by the read of
+// the weights, so what counts is bytes in flight and whole cache lines: read
+// straight into matrix operands, 16 rows x 64 bytes an instruction, a compute
+// unit gets 37 GB/s from its L2, in lines of 128 bytes 119 GB/s.  So codes and
+// activations go to LDS by DMA, a step of 128 code bytes a row (256 columns of
+// W4A16, 512 ternary ones), into a ring of kStages steps:
+//  - codes: [32 rows a wave][8 chunks of 16 bytes], chunk c of row r at c ^ (r % 8);
+//  - activations: [BM rows][BK columns], chunk c of row r at c ^ (r % 16).
+// NW waves share a step's activations; KW groups of waves deal the steps where
+// there are too few weight rows to fill the compute units, and their sums meet in
+// LDS in the groups' order.
+// Lane 16 g + i of a wave takes chunk 4 h + g of weight row i (h = 0, 1) and the
+// activations of the same columns of row i.  W4A16: that is one scale group an h,
+// whose sum starts from zero and is scaled into the result.
+// Gated: a wave's first 16 weight rows are the gate's, the others the same rows of
+// the up projection.
+namespace narrow {
+
+template <int FMT, int BM, int KW, int NW>
+struct Ring {
+    // two steps in the ring where a step's activations are as many bytes as its codes
+    static constexpr int kStages = 2;
+    static constexpr int kWaves = KW * NW, kThreads = kWaves * kWave;
+    static constexpr int BK = FMT == 0 ? 512 : 256;
+    static constexpr int kABytes = BM * BK * 2;
+    static constexpr int kBBytes = NW * 32 * 128;
+    static constexpr int kStageBytes = kABytes + kBBytes;      // of a group of waves
+    static constexpr int kBytes = kStages * KW * kStageBytes;
+    static constexpr int AU = kABytes / 1024 >= NW ? kABytes / 1024 / NW : 1;  // 1-KB transfers a wave and step
+    static constexpr int BU = 4;
+    // scales and zero points held in LDS, at most
+    static constexpr int kScaleBytes = FMT == 0 ? 0 : kBytes + 49152 <= 163840 ? 49152 : 163840 - kBytes;
+    static_assert(kBytes <= 163840, "a compute unit has 160 KB");
+};
+
+template <class T, int FMT, bool ASYM, bool GATED, int BM, int KW, int NW>
+__global__ __launch_bounds__(KW * NW * kWave) void kernel(ExpertArgs a, int scale_bytes) {
+    typedef typename Mfma<T>::vec vec;
+    typedef Ring<FMT, BM, KW, NW> G;
+    constexpr int BK = G::BK, AU = G::AU, BU = G::BU, kStages = G::kStages;
+    constexpr int kCols = GATED ? 16 * NW : 32 * NW;  // output columns of the workgroup
+    constexpr int kUnits = FMT == 0 ? 8 : 4;          // 8-column units of a 16-byte chunk of codes
+    extern __shared__ uint4 smem_narrow[];
+    uint8_t* lds = reinterpret_cast<uint8_t*>(smem_narrow);
+    const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem_narrow;
+    const int64_t N = a.N, width = GATED ? N / 2 : N;
+    const int K = (int)a.K;
+    const Place place = find_tile(a, BM, (uint32_t)((width + kCols - 1) / kCols), (uint32_t)a.first + blockIdx.x);
+    const Block blk = place.blk;
+    if (blk.rows == 0) return;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int kw = wave / NW, nw = wave % NW;
+    const int g = lane >> 4, i16 = lane & 15;
+    const int64_t c0 = (int64_t)place.n_tile * kCols;
+    const uint32_t rb = FMT == 0 ? K / 4 : K / 2;
+    const int GK = K / 128;
+    // weight row of row lr of the workgroup's 32 NW; past the end: the last
+    auto weight_row = [&](int lr) {
+        int64_t c, half = 0;
+        if constexpr (GATED) {
+            c = c0 + (lr >> 5) * 16 + (lr & 15);
+            half = (lr & 16) ? width : 0;
+        } else {
+            c = c0 + lr;
+        }
+        return (uint32_t)(half + (c < width ? c : width - 1));
+    };
+    const uint8_t* w_exp = a.w + (int64_t)blk.expert * N * rb;
+    const uint16_t* s_exp = a.scale + (int64_t)blk.expert * N * (FMT == 0 ? 1 : GK);
+    const uint8_t* z_exp = ASYM ? a.zeros + (int64_t)blk.expert * N * GK : nullptr;
+
+    // steps of this group of waves; the others of the workgroup go along idle
+    const int steps = (K + BK - 1) / BK;
+    const int from = steps * kw / KW, mine = steps * (kw + 1) / KW - from;
+    const int most = (steps + KW - 1) / KW;
+    // DMA sources.  Codes: lane l has chunk (l % 8) ^ (row % 8) of row 8 u + l / 8 of
+    // the wave's 32.  Activations: 16-byte chunks of the group's rows in LDS order.
+    // In the last step what lies past the row is its last chunk again.
+    uint32_t b_row[BU];
+    const uint32_t b_chunk = 16u * ((lane & 7) ^ (lane >> 3));
+#pragma unroll
+    for (int u = 0; u < BU; ++u) b_row[u] = weight_row(32 * nw + 8 * u + (lane >> 3)) * rb;
+    auto issue_codes = [&](int step, uint32_t at) {
+        const uint32_t byte = 128u * (from + step) + b_chunk;
+        const uint32_t off = byte < rb ? byte : rb - 16;
+#pragma unroll
+        for (int u = 0; u < BU; ++u) dma16s(w_exp, b_row[u] + off, at + G::kABytes + 4096u * nw + 1024u * u);
+    };
+    constexpr int kRowChunks = BK / 8;
+    const uint8_t* a_row[AU];
+    uint32_t a_chunk[AU];
+    auto issue_rows = [&](int step, uint32_t at) {
+#pragma unroll
+        for (int u = 0; u < AU; ++u) {
+            const uint32_t byte = 2u * BK * (from + step) + a_chunk[u];
+            dma16(a_row[u] + (byte < 2u * K ? byte : 2u * K - 16), at + 1024u * ((AU * nw + u) % (G::kABytes / 1024)));
+        }
+    };
+    auto stage_at = [&](int stage) { return lds_base + (uint32_t)((stage * KW + kw) * G::kStageBytes); };
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k)
+        if (k < mine) issue_codes(k, stage_at(k));
+    // the scales of the workgroup's rows, [row][GK] as they lie in memory: 16 rows in
+    // a row there are 16 in a row here (rows past the end are not used)
+    uint8_t* sc_lds = lds + G::kBytes;
+    const bool in_lds = FMT == 1 && scale_bytes > 0;
+    if (in_lds) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {  // rows 32 nw + 16 p .. + 15, by the groups of waves in turn
+            const uint32_t first = weight_row(32 * nw + 16 * p) * (uint32_t)GK;
+            const uint32_t end = (uint32_t)N * GK - first;
+            const int to = (32 * nw + 16 * p) * GK;
+            for (int e = kw * kWave + lane; e < 16 * GK; e += KW * kWave) {
+                const uint32_t i = first + ((uint32_t)e < end ? e : 0);
+                reinterpret_cast<uint16_t*>(sc_lds)[to + e] = s_exp[i];
+                if constexpr (ASYM) sc_lds[64 * NW * GK + to + e] = z_exp[i];
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < AU; ++u) {
+        const int at = ((AU * nw + u) % (G::kABytes / 1024)) * 64 + lane;  // chunk's place
+        const int r = at / kRowChunks;
+        a_row[u] = reinterpret_cast<const uint8_t*>(a.A + source_row(a, blk.row + (r < blk.rows ? r : 0)) * K);
+        a_chunk[u] = 16u * ((at % kRowChunks) ^ (r & 15));
+    }
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k)
+        if (k < mine) issue_rows(k, stage_at(k));
+
+    f32x4 acc[2];
+    acc[0] = acc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int a_frag = (i16 % BM) * (BK * 2), a_swz = i16 % BM;
+    const int b_frag = G::kABytes + (32 * nw + i16) * 128, b_swz = i16 & 7;
+    const uint32_t magic_v = vgpr_const<kMagic2>();
+    const uint32_t mask_v = sgpr_const<0x00F0000Fu>();
+    const NatConsts nat = nat_consts();
+    uint32_t sr[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) sr[j] = weight_row(32 * nw + 16 * j + i16);
+    // Half h of step k.  PART: a ternary row ends in it; the lanes past its end take
+    // weights and activations of 0.
+    auto contract = [&](auto part, const uint8_t* sbase, int k, int h) {
+        constexpr bool PART = decltype(part)::value;
+        const bool past = PART && BK * (from + k) + (BK / 2) * h + 64 * g >= K;
+        uint4 q[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            q[j] = *reinterpret_cast<const uint4*>(sbase + b_frag + 2048 * j + 16 * ((4 * h + g) ^ b_swz));
+            if (past) q[j] = make_uint4(0x55555555u, 0x55555555u, 0x55555555u, 0x55555555u);
+        }
+        f32x4 sum[2];
+        if constexpr (FMT == 1) sum[0] = sum[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+        else sum[0] = acc[0], sum[1] = acc[1];
+        float s[2];
+        W4Unpack<T, ASYM> un[2];
+        if constexpr (FMT == 1) {
+            const int group = 2 * (from + k) + h;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int at = (32 * nw + 16 * j + i16) * GK + group;
+                s[j] = f16_bits_to_f32(in_lds ? reinterpret_cast<const uint16_t*>(sc_lds)[at] : s_exp[(int64_t)sr[j] * GK + group]) *
+                       W4Unpack<T, ASYM>::kUnit;
+                if constexpr (ASYM) un[j].set(in_lds ? sc_lds[64 * NW * GK + at] : z_exp[(int64_t)sr[j] * GK + group], false);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            const int chunk = 4 * kUnits * h + kUnits * g + u;
+            uint4 av = *reinterpret_cast<const uint4*>(sbase + a_frag + 16 * (chunk ^ a_swz));
+            if (past) av = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                uint4 b;
+                if constexpr (FMT == 0) {
+                    const uint32_t x = dword_of(q[j], u / 2);
+                    b = u % 2 ? nat_quad<1>(x, magic_v, nat) : nat_quad<0>(x, magic_v, nat);
+                } else {
+                    b = un[j].quad(dword_of(q[j], u), mask_v, magic_v);
+                }
+                sum[j] = Mfma<T>::mma(__builtin_bit_cast(vec, av), __builtin_bit_cast(vec, b), sum[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if constexpr (FMT == 1) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[j][i] = fmaf(s[j], sum[j][i], acc[j][i]);
+            } else {
+                acc[j] = sum[j];
+            }
+        }
+    };
+    auto half = [&](const uint8_t* sbase, int k, int h) {
+        if (FMT == 0 && BK * (from + k) + (BK / 2) * (h + 1) > K) contract(std::true_type{}, sbase, k, h);
+        else contract(std::false_type{}, sbase, k, h);
+    };
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    stage_barrier();
+    int stage = 0;
+    for (int k = 0; k < most; ++k) {
+        const bool more = k + kStages - 1 < mine;
+        if (more) {
+            const int next = stage == 0 ? kStages - 1 : stage - 1;
+            issue_codes(k + kStages - 1, stage_at(next));
+            issue_rows(k + kStages - 1, stage_at(next));
+        }
+        if (k < mine) {
+            const uint8_t* sbase = lds + (stage * KW + kw) * G::kStageBytes;
+            half(sbase, k, 0);
+            if (BK * (from + k) + BK / 2 < K) half(sbase, k, 1);
+        }
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+        // the next step has landed; of the later ones only the last may be on its way
+        if (more) asm volatile("s_waitcnt vmcnt(%0)" :: "n"((kStages - 2) * (AU + BU)) : "memory");
+        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        stage_barrier();
+    }
+
+    if constexpr (KW > 1) {  // the groups' sums, in their order
+        f32x4* red = reinterpret_cast<f32x4*>(lds);  // [KW - 1][NW][2][64]: the ring is idle
+        if (kw > 0) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) red[(((kw - 1) * NW + nw) * 2 + j) * kWave + lane] = acc[j];
+        }
+        __syncthreads();
+        if (kw > 0) return;
+#pragma unroll
+        for (int z = 0; z < KW - 1; ++z)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc[j] += red[((z * NW + nw) * 2 + j) * kWave + lane];
+    }
+    // lane 16 g + i: rows 4 g .. 4 g + 3, weight row i of each block
+    const int64_t bias_row = (int64_t)blk.expert * N;
+    float sc[2], bi[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        sc[j] = FMT == 0 ? f16_bits_to_f32(s_exp[sr[j]]) * Mfma<T>::kUnit : 1.0f;
+        bi[j] = a.bias ? T::to_f32(a.bias[bias_row + sr[j]]) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 4 * g + i;
+        if (row >= blk.rows || row >= BM) continue;
+        uint16_t* dst = a.C + (blk.row + row) * width;
+        if constexpr (GATED) {
+            const int64_t c = c0 + 16 * nw + i16;
+            if (c < width) dst[c] = T::from_f32_fast(gate(fmaf(acc[0][i], sc[0], bi[0]), fmaf(acc[1][i], sc[1], bi[1])));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int64_t c = c0 + 32 * nw + 16 * j + i16;
+                if (c < width) dst[c] = T::from_f32_fast(fmaf(acc[j][i], sc[j], bi[j]));
+            }
+        }
+    }
+}
+
+}  // namespace narrow
+
+// ---------------------------------------------------------------- many rows
+//
+// BM rows of one expert and 256 weight rows a workgroup, four waves of BM x 64.
+// Activations and codes come by DMA (no registers) into a ring of three stages of
+// 64 columns, two ahead of the matrix cores: BM rows x 128 bytes, 16-byte chunks
+// XOR-swizzled (chunk c of row r at c ^ (r % 8)), and 256 weight rows x 16 or 32
+// bytes.  Codes are unpacked in registers in the natural order of their columns.
+// Two workgroups share a compute unit, so one's barriers lie under the other's
+// products.
+//
+// W4A16: the accumulators hold the sum in units of the current group's scale, so
+// entering a group multiplies them by the ratio of the last scale to its own, and
+// the operands stay the exact q - z.  (Scaling every group's sum into a second set
+// of accumulators costs as many instructions and twice the registers, which
+// halves the tile.)  A group whose scale is 0 keeps the last unit, and its code
+// words are replaced by those of zero weights.
+namespace tile {
+
+constexpr int BN = 256, BK = 64, WN = 64, TN = 4;
+constexpr int kWaves = 4, kThreads = kWaves * kWave;
+constexpr int kStages = 3;
+constexpr int kEpiLd = WN + 8;  // halves of a row staged for its store
+
+template <int FMT, int BM>
+struct Ring {
+    static constexpr int kABytes = BM * BK * 2;
+    static constexpr int kBBytes = BN * BK / (FMT == 0 ? 4 : 2);
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kBytes = kStages * kStageBytes;
+    static constexpr int AU = BM / 32, BU = kBBytes / 4096;  // 1-KB transfers a wave and stage
+    static_assert(kWaves * 32 * kEpiLd * 2 <= kBytes, "epilogue staging must fit in the ring");
+};
 
 template <class T, int FMT, bool ASYM, bool GATED, int BM>
 __global__ __launch_bounds__(kThreads, 2) void kernel(ExpertArgs a) {
@@ -521,20 +689,37 @@ int64_t most_blocks(int64_t P, int64_t E, int64_t BM) {
     return (P + used * (BM - 1)) / BM;
 }
 
-template <class T, int FMT, bool ASYM, bool GATED>
-hipError_t launch_stream(const ExpertArgs& args, hipStream_t s) {
-    constexpr int R = 4;
-    constexpr int kOut = GATED ? R / 2 : R;
-    const int64_t width = GATED ? args.N / 2 : args.N;
-    const int64_t groups = (width + 16 * kOut - 1) / (16 * kOut) * most_blocks(args.P, args.E, 16);
+template <class T, int FMT, bool ASYM, bool GATED, int BM, int KW, int NW>
+hipError_t launch_narrow(const ExpertArgs& args, hipStream_t s) {
+    typedef narrow::Ring<FMT, BM, KW, NW> G;
+    static DeviceFlags lds_limit_set;
+    hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&narrow::kernel<T, FMT, ASYM, GATED, BM, KW, NW>),
+                                   G::kBytes + G::kScaleBytes, lds_limit_set);
+    if (e != hipSuccess) return e;
+    const int64_t width = GATED ? args.N / 2 : args.N, cols = (GATED ? 16 : 32) * NW;
+    const int64_t groups = ((width + cols - 1) / cols * most_blocks(args.P, args.E, BM) + 7) / 8 * 8;
+    if (groups >= (int64_t)1 << 31) return hipErrorInvalidValue;
+    const int64_t scales = FMT == 0 ? 0 : 32 * NW * (args.K / 128) * (ASYM ? 3 : 2);
+    const int scale_bytes = scales <= G::kScaleBytes ? (int)scales : 0;
     ExpertArgs a = args;
-    for (a.first = 0; a.first < groups; a.first += kMaxGroups) {
-        const int64_t n = groups - a.first < kMaxGroups ? groups - a.first : kMaxGroups;
-        stream_kernel<T, FMT, ASYM, GATED, R><<<(unsigned)n, kStreamWaves * kWave, 0, s>>>(a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
+    constexpr int64_t kMost = kMaxGroups / 8 * 8;
+    for (a.first = 0; a.first < groups; a.first += kMost) {
+        const int64_t n = groups - a.first < kMost ? groups - a.first : kMost;
+        narrow::kernel<T, FMT, ASYM, GATED, BM, KW, NW><<<(unsigned)n, G::kThreads, G::kBytes + scale_bytes, s>>>(a, scale_bytes);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     return hipSuccess;
+}
+
+// Four waves a workgroup: side by side over the weight rows where that makes two
+// workgroups a compute unit of the experts that have rows, else over the columns.
+template <class T, int FMT, bool ASYM, bool GATED, int BM>
+hipError_t launch_few(const ExpertArgs& a, hipStream_t s) {
+    const int64_t blocks = a.P < a.E ? a.P : a.E;
+    const int64_t rows = blocks * a.N;  // weight rows
+    if (rows >= 2 * 128 * compute_units()) return launch_narrow<T, FMT, ASYM, GATED, BM, 1, 4>(a, s);
+    if (rows >= 2 * 64 * compute_units()) return launch_narrow<T, FMT, ASYM, GATED, BM, 2, 2>(a, s);
+    return launch_narrow<T, FMT, ASYM, GATED, BM, 4, 1>(a, s);
 }
 
 template <class T, int FMT, bool ASYM, bool GATED, int BM>
@@ -561,7 +746,8 @@ hipError_t launch_rows(const ExpertArgs& a, hipStream_t s) {
     const int64_t rows = a.P / (a.P < a.E ? a.P : a.E);  // of an expert, on average
     if (rows >= 48) return launch_tile<T, FMT, ASYM, GATED, 128>(a, s);
     if (rows >= 16) return launch_tile<T, FMT, ASYM, GATED, 64>(a, s);
-    return launch_stream<T, FMT, ASYM, GATED>(a, s);
+    if (rows >= 3) return launch_few<T, FMT, ASYM, GATED, 16>(a, s);
+    return launch_few<T, FMT, ASYM, GATED, 4>(a, s);
 }
 
 template <class T>
