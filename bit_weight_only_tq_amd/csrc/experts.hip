@@ -178,7 +178,7 @@ __device__ __forceinline__ Place find_tile(const ExpertArgs& a, int BM, uint32_t
 // unit gets 37 GB/s from its L2, in lines of 128 bytes 119 GB/s.  So codes and
 // activations go to LDS by DMA, a step of 128 code bytes a row (256 columns of
 // W4A16, 512 ternary ones), into a ring of kStages steps:
-//  - codes: [32 rows a wave][8 chunks of 16 bytes], chunk c of row r at c ^ (r % 8);
+//  - codes: [32 rows a wave][8 chunks of 16 bytes], chunk c of row r at c ^ (r / 2 % 8);
 //  - activations: [BM rows][BK columns], chunk c of row r at c ^ (r % 16).
 // NW waves share a step's activations; KW groups of waves deal the steps where
 // there are too few weight rows to fill the compute units, and their sums meet in
@@ -248,18 +248,24 @@ __global__ __launch_bounds__(KW * NW * kWave) void kernel(ExpertArgs a, int scal
     const int steps = (K + BK - 1) / BK;
     const int from = steps * kw / KW, mine = steps * (kw + 1) / KW - from;
     const int most = (steps + KW - 1) / KW;
-    // DMA sources.  Codes: lane l has chunk (l % 8) ^ (row % 8) of row 8 u + l / 8 of
+    // DMA sources.  Codes: lane l has chunk (l % 8) ^ (row / 2 % 8) of row 8 u + l / 8 of
     // the wave's 32.  Activations: 16-byte chunks of the group's rows in LDS order.
     // In the last step what lies past the row is its last chunk again.
     uint32_t b_row[BU];
-    const uint32_t b_chunk = 16u * ((lane & 7) ^ (lane >> 3));
+    uint32_t b_chunk[2];  // of even and of odd u
+    b_chunk[0] = 16u * ((lane & 7) ^ (lane >> 4));
+    b_chunk[1] = b_chunk[0] ^ 64u;
 #pragma unroll
     for (int u = 0; u < BU; ++u) b_row[u] = weight_row(32 * nw + 8 * u + (lane >> 3)) * rb;
     auto issue_codes = [&](int step, uint32_t at) {
-        const uint32_t byte = 128u * (from + step) + b_chunk;
-        const uint32_t off = byte < rb ? byte : rb - 16;
+        uint32_t off[2];
 #pragma unroll
-        for (int u = 0; u < BU; ++u) dma16s(w_exp, b_row[u] + off, at + G::kABytes + 4096u * nw + 1024u * u);
+        for (int u = 0; u < 2; ++u) {
+            const uint32_t byte = 128u * (from + step) + b_chunk[u];
+            off[u] = byte < rb ? byte : rb - 16;
+        }
+#pragma unroll
+        for (int u = 0; u < BU; ++u) dma16s(w_exp, b_row[u] + off[u % 2], at + G::kABytes + 4096u * nw + 1024u * u);
     };
     constexpr int kRowChunks = BK / 8;
     const uint8_t* a_row[AU];
@@ -306,7 +312,7 @@ __global__ __launch_bounds__(KW * NW * kWave) void kernel(ExpertArgs a, int scal
     f32x4 acc[2];
     acc[0] = acc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int a_frag = (i16 % BM) * (BK * 2), a_swz = i16 % BM;
-    const int b_frag = G::kABytes + (32 * nw + i16) * 128, b_swz = i16 & 7;
+    const int b_frag = G::kABytes + (32 * nw + i16) * 128, b_swz = i16 >> 1;
     const uint32_t magic_v = vgpr_const<kMagic2>();
     const uint32_t mask_v = sgpr_const<0x00F0000Fu>();
     const NatConsts nat = nat_consts();
@@ -437,8 +443,9 @@ __global__ __launch_bounds__(KW * NW * kWave) void kernel(ExpertArgs a, int scal
 //
 // BM rows of one expert and 256 weight rows a workgroup, four waves of BM x 64.
 // Activations and codes come by DMA (no registers) into a ring of three stages of
-// 64 columns, two ahead of the matrix cores: BM rows x 128 bytes, 16-byte chunks
-// XOR-swizzled (chunk c of row r at c ^ (r % 8)), and 256 weight rows x 16 or 32
+// 64 columns, two or three ahead of the matrix cores: BM rows x 128 bytes, 16-byte chunks
+// XOR-swizzled (chunk c of row r at c ^ (r / 2 % 8): two rows span the banks, so 16
+// rows' reads of a chunk meet 16 different places), and 256 weight rows x 16 or 32
 // bytes.  Codes are unpacked in registers in the natural order of their columns.
 // Two workgroups share a compute unit, so one's barriers lie under the other's
 // products.
@@ -462,6 +469,7 @@ struct Ring {
     static constexpr int kBBytes = BN * BK / (FMT == 0 ? 4 : 2);
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kBytes = kStages * kStageBytes;
+    static constexpr int kScaleBytes = FMT == 0 ? 0 : 512 * kWaves * 3;  // eight groups of the tile's rows
     static constexpr int AU = BM / 32, BU = kBBytes / 4096;  // 1-KB transfers a wave and stage
     static_assert(kWaves * 32 * kEpiLd * 2 <= kBytes, "epilogue staging must fit in the ring");
 };
@@ -509,7 +517,7 @@ __global__ __launch_bounds__(kThreads, 2) void kernel(ExpertArgs a) {
     for (int u = 0; u < AU; ++u) {
         const int r = 8 * (AU * wave + u) + (lane >> 3);
         const int64_t row = source_row(a, blk.row + (r < blk.rows ? r : blk.rows - 1));
-        a_src[u] = reinterpret_cast<const uint8_t*>(a.A + row * K) + 16 * ((lane & 7) ^ (lane >> 3));
+        a_src[u] = reinterpret_cast<const uint8_t*>(a.A + row * K) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
     }
     uint32_t b_src[BU];  // from the expert's weights: below 2^31 bytes
 #pragma unroll
@@ -519,7 +527,7 @@ __global__ __launch_bounds__(kThreads, 2) void kernel(ExpertArgs a) {
     }
     // The sources run on from stage to stage and stay at the last K-step, so that the
     // counts of transfers in flight stay exact; what is issued past the end goes
-    // into a stage that nobody reads any more.
+    // where nobody reads any more.
     const uint8_t* b_at = w_exp;
     const int nk = (int)(K / BK);
     int issued = 0;
@@ -535,8 +543,6 @@ __global__ __launch_bounds__(kThreads, 2) void kernel(ExpertArgs a) {
 #pragma unroll
         for (int u = 0; u < AU; ++u) a_src[u] += on ? 2 * BK : 0;
     };
-    // all but the stage issued last have landed
-    auto wait_stage = [&]() { asm volatile("s_waitcnt vmcnt(%0)" :: "n"(AU + BU) : "memory"); };
 
     f32x4 acc[TM][TN];
 #pragma unroll
@@ -544,87 +550,144 @@ __global__ __launch_bounds__(kThreads, 2) void kernel(ExpertArgs a) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int a_frag = i16 * (BK * 2);
-    const int swz = i16 & 7;
+    const int swz = i16 >> 1;
     const int b_frag = G::kABytes + (wave * WN + i16) * (FMT == 0 ? 16 : 32) + (FMT == 0 ? 4 : 8) * g;
     const uint32_t magic_v = vgpr_const<kMagic2>();
     const uint32_t mask_v = sgpr_const<0x00F0000Fu>();
     const NatConsts nat = nat_consts();
-    uint32_t sr[TN];  // index of the scales of this lane's weight rows
-#pragma unroll
-    for (int j = 0; j < TN; ++j) sr[j] = weight_row(wave * WN + 16 * j + i16) * (uint32_t)(FMT == 0 ? 1 : GK);
     W4Unpack<T, ASYM> un[TN];
-    float unit[TN];              // scale that the accumulators are in units of
-    uint16_t next_s[TN];         // the next group's
-    uint8_t next_z[TN];
-    auto load_scales = [&](int64_t group) {
+    float unit[TN];  // scale that the accumulators are in units of
+    // The wave's 64 rows of scales (and zero points), eight groups at a time, in an
+    // LDS area of its own, [8][64]: a lane reads one row's eight at once, so that a
+    // line is touched once in sixteen K-steps, and only then waits for memory.
+    uint16_t* sc_lds = reinterpret_cast<uint16_t*>(lds + G::kBytes) + 512 * wave;
+    uint8_t* zp_lds = lds + G::kBytes + 1024 * kWaves + 512 * wave;
+    const uint32_t s_row = weight_row(wave * WN + lane) * (uint32_t)GK;
+    auto load_scales = [&](int first) {  // groups first .. first + 7, or the last eight
+        const int from = GK < 8 ? 0 : first < (int)GK - 8 ? first : (int)GK - 8;
+        uint16_t v[8];
+        uint8_t z[8];
+        if (GK >= 8) {
+            __builtin_memcpy(v, s_exp + from + s_row, 16);
+            if constexpr (ASYM) __builtin_memcpy(z, z_exp + from + s_row, 8);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int at = e < (int)GK ? e : 0;
+                v[e] = s_exp[s_row + at];
+                if constexpr (ASYM) z[e] = z_exp[s_row + at];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            sc_lds[64 * e + lane] = v[e];
+            if constexpr (ASYM) zp_lds[64 * e + lane] = z[e];
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the wave's own area: no barrier
+        return from;
+    };
+
+    // the unpacking constants of the next group, and what takes the sums to its unit
+    float ratio[TN];
+    int held = 0;  // first group in LDS
+    auto enter_group = [&](int group) {
+        if ((group & 7) == 0) held = load_scales(group);
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-            next_s[j] = (s_exp + group)[sr[j]];
-            if constexpr (ASYM) next_z[j] = (z_exp + group)[sr[j]];
+            const int at = 64 * (group - held) + 16 * j + i16;
+            const float s = f16_bits_to_f32(sc_lds[at]);
+            const bool zero = s == 0.0f;
+            un[j].set(ASYM ? zp_lds[at] : 8u, zero);
+            float r = __builtin_amdgcn_rcpf(s);
+            r = unit[j] * fmaf(fmaf(-s, r, 1.0f), r, r);  // a Newton step: within an ulp
+            ratio[j] = zero ? 1.0f : r;
+            if (!zero) unit[j] = s;
+        }
+    };
+    uint2 x[TN];      // code words of a K-step: .x its first half (ternary: both)
+    uint32_t y[TN];   // of the second half, while x takes the next K-step's
+    auto read_codes = [&](const uint8_t* stage) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            if constexpr (FMT == 0) x[j].x = *reinterpret_cast<const uint32_t*>(stage + b_frag + 16 * 16 * j);
+            else x[j] = *reinterpret_cast<const uint2*>(stage + b_frag + 16 * 32 * j);
+        }
+    };
+    auto unpack = [&](int half, int j) {
+        uint4 b;
+        if constexpr (FMT == 0) b = half ? nat_quad<1>(y[j], magic_v, nat) : nat_quad<0>(x[j].x, magic_v, nat);
+        else b = un[j].quad(half ? y[j] : x[j].x, mask_v, magic_v);
+        return __builtin_bit_cast(vec, b);
+    };
+    // Half a K-step: 16 weight rows at a time against all activation rows, while the
+    // next 16 are unpacked (a product leaves the vector unit three issue slots).  The
+    // activations' registers take the next half's as they become free.
+    vec af[TM], bf;
+    auto read_rows = [&](const uint8_t* stage, int half, int i) {
+        af[i] = __builtin_bit_cast(vec, *reinterpret_cast<const uint4*>(stage + a_frag + 16 * ((2 * g + half) ^ swz) + i * 16 * (BK * 2)));
+    };
+    auto products = [&](auto rescale, int half, const uint8_t* next) {
+        constexpr bool kRescale = decltype(rescale)::value;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                if constexpr (kRescale) acc[i][j] *= ratio[j];
+                acc[i][j] = Mfma<T>::mma(af[i], bf, acc[i][j]);
+                if (j == TN - 1) read_rows(next, half ^ 1, i);
+            }
+            if (j + 1 < TN) bf = unpack(half, j + 1);
+            else if (half == 0) bf = unpack(1, 0);
+            if constexpr (FMT == 0) {  // two vector instructions beside each product
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x002, 16 / TM, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    if (j == TN - 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
 
+    issue();
+    issue();
+    issue();
     if constexpr (FMT == 1) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) unit[j] = 1.0f;
-        load_scales(0);
+        enter_group(0);
     }
-    issue();
-    issue();
-    wait_stage();
+    asm volatile("s_waitcnt vmcnt(%0)" :: "n"(2 * (AU + BU)) : "memory");
     stage_barrier();
-    uint32_t read_at = 0;  // of the stage that is read
-    constexpr int kHalves = FMT == 1 ? 2 : 1;  // K-steps of a scale group
-    for (int kt = 0; kt < nk; kt += kHalves) {
-        if constexpr (FMT == 1) {  // enter group kt / 2
+    const uint8_t* at = lds;                       // this K-step's stage
+    const uint8_t* const last_stage = lds + (kStages - 1) * G::kStageBytes;
+    auto second_half = [&]() {
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                const float s = f16_bits_to_f32(next_s[j]);
-                const bool zero = s == 0.0f;
-                un[j].set(ASYM ? next_z[j] : 8u, zero);
-                float r = __builtin_amdgcn_rcpf(s);
-                r = unit[j] * fmaf(fmaf(-s, r, 1.0f), r, r);  // a Newton step: within an ulp
-                if (zero) r = 1.0f;
-                else unit[j] = s;
-                if (kt > 0) {
+        for (int j = 0; j < TN; ++j) y[j] = FMT == 0 ? x[j].x : x[j].y;
+    };
+    read_codes(at);
 #pragma unroll
-                    for (int i = 0; i < TM; ++i) acc[i][j] *= r;
-                }
-            }
-            load_scales(kt + 2 < nk ? kt / 2 + 1 : kt / 2);
-        }
+    for (int i = 0; i < TM; ++i) read_rows(at, 0, i);
+    second_half();
+    bf = unpack(0, 0);
+    constexpr int kSteps = FMT == 1 ? 2 : 1;  // of a scale group
+    for (int kt = 0; kt < nk; kt += kSteps) {
 #pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
-            issue();  // K-step kt + h + 2
-            const uint8_t* sbase = lds + read_at;
-            read_at = read_at == (kStages - 1) * G::kStageBytes ? 0 : read_at + G::kStageBytes;
-            uint2 x[TN];
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                if constexpr (FMT == 0) x[j].x = *reinterpret_cast<const uint32_t*>(sbase + b_frag + 16 * 16 * j);
-                else x[j] = *reinterpret_cast<const uint2*>(sbase + b_frag + 16 * 32 * j);
-            }
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if (s) asm volatile("" ::: "memory");  // the second half's loads stay behind the first: registers
-                const uint8_t* arow = sbase + a_frag + 16 * ((2 * g + s) ^ swz);
-                vec bf[TN];
-#pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    uint4 b;
-                    if constexpr (FMT == 0) b = s ? nat_quad<1>(x[j].x, magic_v, nat) : nat_quad<0>(x[j].x, magic_v, nat);
-                    else b = un[j].quad(s ? x[j].y : x[j].x, mask_v, magic_v);
-                    bf[j] = __builtin_bit_cast(vec, b);
-                }
-#pragma unroll
-                for (int i = 0; i < TM; ++i) {
-                    const vec af = __builtin_bit_cast(vec, *reinterpret_cast<const uint4*>(arow + i * 16 * (BK * 2)));
-#pragma unroll
-                    for (int j = 0; j < TN; ++j) acc[i][j] = Mfma<T>::mma(af, bf[j], acc[i][j]);
-                }
-            }
-            wait_stage();     // the next stage has landed
-            stage_barrier();  // ... for every wave, and nobody reads this one any more
+        for (int h = 0; h < kSteps; ++h) {
+            if (FMT == 1 && h == 0) products(std::true_type{}, 0, at);
+            else products(std::false_type{}, 0, at);
+            // The next stage has landed, for every wave, and everything of this one is
+            // in registers: its place takes the third stage from here.
+            asm volatile("s_waitcnt vmcnt(%0)" :: "n"(AU + BU) : "memory");
+            stage_barrier();
+            issue();
+            at = at == last_stage ? lds : at + G::kStageBytes;
+            read_codes(at);
+            products(std::false_type{}, 1, at);
+            if (FMT == 1 && h == 1 && kt / 2 + 1 < (int)GK) enter_group(kt / 2 + 1);
+            second_half();
+            bf = unpack(0, 0);
         }
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -636,7 +699,7 @@ __global__ __launch_bounds__(kThreads, 2) void kernel(ExpertArgs a) {
     float sc[TN], bi[TN];
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-        if constexpr (FMT == 0) sc[j] = f16_bits_to_f32(s_exp[sr[j]]) * Mfma<T>::kUnit;
+        if constexpr (FMT == 0) sc[j] = f16_bits_to_f32(s_exp[weight_row(wave * WN + 16 * j + i16)]) * Mfma<T>::kUnit;
         else sc[j] = unit[j] * W4Unpack<T, ASYM>::kUnit;
         bi[j] = a.bias ? T::to_f32(a.bias[(int64_t)blk.expert * N + weight_row(wave * WN + 16 * j + i16)]) : 0.0f;
     }
@@ -726,7 +789,7 @@ template <class T, int FMT, bool ASYM, bool GATED, int BM>
 hipError_t launch_tile(const ExpertArgs& args, hipStream_t s) {
     typedef tile::Ring<FMT, BM> G;
     static DeviceFlags lds_limit_set;
-    hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&tile::kernel<T, FMT, ASYM, GATED, BM>), G::kBytes, lds_limit_set);
+    hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&tile::kernel<T, FMT, ASYM, GATED, BM>), G::kBytes + G::kScaleBytes, lds_limit_set);
     if (e != hipSuccess) return e;
     const int64_t width = GATED ? args.N / 2 : args.N, cols = GATED ? tile::BN / 2 : tile::BN;
     const int64_t groups = ((width + cols - 1) / cols * most_blocks(args.P, args.E, BM) + 7) / 8 * 8;
@@ -735,7 +798,7 @@ hipError_t launch_tile(const ExpertArgs& args, hipStream_t s) {
     constexpr int64_t kMost = kMaxGroups / 8 * 8;
     for (a.first = 0; a.first < groups; a.first += kMost) {
         const int64_t n = groups - a.first < kMost ? groups - a.first : kMost;
-        tile::kernel<T, FMT, ASYM, GATED, BM><<<(unsigned)n, tile::kThreads, G::kBytes, s>>>(a);
+        tile::kernel<T, FMT, ASYM, GATED, BM><<<(unsigned)n, tile::kThreads, G::kBytes + G::kScaleBytes, s>>>(a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     return hipSuccess;
