@@ -17,6 +17,7 @@
 
 #include "tq_device.h"
 #include "tq_internal.h"
+#include "tq_tiles.h"
 
 namespace tq {
 
@@ -26,25 +27,34 @@ constexpr int kRouteThreads = 1024;
 constexpr int kRouteWaves = kRouteThreads / kWave;
 
 struct F32 {
+    static constexpr bool kShort = false;
     static __device__ __forceinline__ float load(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
 };
 struct H16 {
-    static __device__ __forceinline__ float load(const void* p, int64_t i) {
-        return f16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
-    }
+    static constexpr bool kShort = true;
+    static constexpr uint32_t kMinusInf = 0xFC00u;
+    static __device__ __forceinline__ float value(uint16_t h) { return f16_bits_to_f32(h); }
 };
 struct B16 {
-    static __device__ __forceinline__ float load(const void* p, int64_t i) {
-        return bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
-    }
+    static constexpr bool kShort = true;
+    static constexpr uint32_t kMinusInf = 0xFF80u;
+    static __device__ __forceinline__ float value(uint16_t h) { return bf16_bits_to_f32(h); }
 };
 
-// Integers ordered like the values; 0 for what is never chosen (NaN, -inf).
+// Integers ordered like the values; 0 for what is never chosen (NaN, -inf).  For a
+// 16-bit type the same with its own 16 bits.
 __device__ __forceinline__ uint32_t order_of(float x) {
     const uint32_t u = __float_as_uint(x + 0.0f);  // -0 is 0
     if (!(x > -__builtin_inff())) return 0u;
     return (u >> 31) ? ~u : (u | 0x80000000u);
 }
+__device__ __forceinline__ uint32_t order16_of(uint16_t h, uint32_t minus_inf) {
+    const uint32_t u = (h & 0x7FFFu) ? h : 0u;  // -0 is 0
+    const uint32_t inf = minus_inf & 0x7FFFu;
+    if ((u & 0x7FFFu) > inf || u == minus_inf) return 0u;
+    return (u >> 15) ? ~u & 0xFFFFu : (u | 0x8000u);
+}
+__device__ __forceinline__ uint16_t bits16_of(uint32_t o) { return (uint16_t)((o >> 15) ? (o & 0x7FFFu) : ~o); }
 __device__ __forceinline__ float value_of(uint32_t o) {
     return __uint_as_float((o >> 31) ? (o & 0x7FFFFFFFu) : ~o);
 }
@@ -88,47 +98,92 @@ __device__ __forceinline__ float group_sum(float v) {
     else return row16_sum(v);
 }
 
+// A lane's logits of token t, experts sub + LANES v, and the best of what is left.
+// 16-bit types: value and index (downwards) in one word, so a round is one maximum.
+// fp32: the largest value, then the lowest index of the lanes that hold it.
+struct Best {
+    uint32_t key;    // order of the value, 0: none
+    uint32_t index;
+};
+template <class L, int LANES, int V>
+struct Logits {
+    uint32_t key[V];
+    int sub;
+    __device__ __forceinline__ void load(const RouteArgs& a, int64_t row) {
+        sub = (int)threadIdx.x & (LANES - 1);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = sub + LANES * v;
+            const bool in = e < a.E;
+            if constexpr (L::kShort) {
+                const uint32_t o = in ? order16_of(static_cast<const uint16_t*>(a.logits)[row + e], L::kMinusInf) : 0u;
+                key[v] = o ? (o << 16) | (0xFFFFu - (uint32_t)e) : 0u;
+            } else {
+                key[v] = in ? order_of(L::load(a.logits, row + e)) : 0u;
+            }
+        }
+    }
+    static __device__ __forceinline__ float value(uint32_t k) {
+        if constexpr (L::kShort) return L::value(bits16_of(k));
+        else return value_of(k);
+    }
+    // order of a key that is not 0
+    __device__ __forceinline__ uint32_t order(int v) const { return L::kShort ? key[v] >> 16 : key[v]; }
+    __device__ __forceinline__ Best take() {
+        uint32_t best = 0u;
+        if constexpr (L::kShort) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) best = umax(best, key[v]);
+            best = group_max<LANES>(best);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (key[v] == best) key[v] = 0u;
+            return Best{best >> 16, 0xFFFFu - (best & 0xFFFFu)};
+        } else {
+            int at = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (key[v] > best) best = key[v], at = v;
+            const uint32_t m = group_max<LANES>(best);
+            const uint32_t i = group_min<LANES>(m && best == m ? (uint32_t)(sub + LANES * at) : 0xFFFFFFFFu);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if ((uint32_t)(sub + LANES * v) == i) key[v] = 0u;
+            return Best{m, i};
+        }
+    }
+};
+
 // Routes token t (the same for the LANES lanes of a group; t >= T does nothing
 // but goes along): writes its experts and weights; -> lane j < k has expert j,
 // E where there is none.
 template <class L, int LANES, int V>
 __device__ __forceinline__ int route_token(const RouteArgs& a, int64_t t) {
+    typedef Logits<L, LANES, V> Keys;
     const int sub = (int)threadIdx.x & (LANES - 1);
     const bool live = t < a.T;
-    const int64_t row = (live ? t : a.T - 1) * a.row_stride;
-    uint32_t key[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int e = sub + LANES * v;
-        key[v] = e < a.E ? order_of(L::load(a.logits, row + e)) : 0u;
-    }
+    Keys keys;
+    keys.load(a, (live ? t : a.T - 1) * a.row_stride);
     uint32_t top = 0u, mine = 0u;
     uint32_t expert = (uint32_t)a.E;
     float all = 0.0f;
+    if (!a.renormalize) {  // the sum over all, before any is taken
+        uint32_t m = 0u;
+#pragma unroll
+        for (int v = 0; v < V; ++v) m = umax(m, keys.key[v] ? keys.order(v) : 0u);
+        top = group_max<LANES>(m);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (keys.key[v]) all += keys.order(v) == top ? 1.0f : expf(Keys::value(keys.order(v)) - Keys::value(top));
+        all = group_sum<LANES>(all);
+    }
     for (int j = 0; j < a.k; ++j) {
-        uint32_t best = 0u;
-        int at = 0;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (key[v] > best) best = key[v], at = v;
-        const uint32_t m = group_max<LANES>(best);
-        const uint32_t i = group_min<LANES>(m && best == m ? (uint32_t)(sub + LANES * at) : 0xFFFFFFFFu);
-        if (j == 0) {
-            top = m;
-            if (!a.renormalize) {
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (key[v]) all += key[v] == top ? 1.0f : expf(value_of(key[v]) - value_of(top));
-                all = group_sum<LANES>(all);
-            }
-        }
-        if (sub == j && m) mine = m, expert = i;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if ((uint32_t)(sub + LANES * v) == i) key[v] = 0u;
+        const Best b = keys.take();
+        if (j == 0) top = b.key;
+        if (sub == j && b.key) mine = b.key, expert = b.index;
     }
     // equal largest logits, infinite ones among them, weigh the same
-    const float w = mine == 0u ? 0.0f : mine == top ? 1.0f : expf(value_of(mine) - value_of(top));
+    const float w = mine == 0u ? 0.0f : mine == top ? 1.0f : expf(Keys::value(mine) - Keys::value(top));
     const float total = a.renormalize ? group_sum<LANES>(w) : all;
     if (live && sub < a.k) {
         a.experts[t * a.k + sub] = mine ? (int32_t)expert : -1;
@@ -145,6 +200,12 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
         const uint32_t o = (uint32_t)__shfl_up((int)v, d, kWave);
         if (lane >= d) v += o;
     }
+    return v;
+}
+
+__device__ __forceinline__ uint32_t wave_sum_u32(uint32_t v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v += (uint32_t)__shfl_xor((int)v, d, kWave);
     return v;
 }
 
@@ -183,11 +244,13 @@ __device__ __forceinline__ void sort_pairs(const RouteArgs& a, int64_t p0, int64
     for (int64_t i = from + lane; i < to; i += 64) atomicAdd(&hist[wave * E1 + id_of(i)], 1u);
     __syncthreads();
     for (int e = threadIdx.x; e < E1; e += kRouteThreads) {
-        uint32_t at = base(e);
+        uint32_t at = base(e), c[kRouteWaves];
+#pragma unroll
+        for (int w = 0; w < kRouteWaves; ++w) c[w] = hist[w * E1 + e];
+#pragma unroll
         for (int w = 0; w < kRouteWaves; ++w) {
-            const uint32_t c = hist[w * E1 + e];
             hist[w * E1 + e] = at;
-            at += c;
+            at += c[w];
         }
     }
     __syncthreads();
@@ -276,6 +339,13 @@ __global__ __launch_bounds__(kRouteThreads) void sort_chunk_kernel(RouteArgs a) 
     uint32_t* first = hist + kRouteWaves * (a.E + 1);     // [E + 1]
     uint32_t* scratch = first + a.E + 1;                  // [waves]
     uint32_t* part = scratch + kRouteWaves;               // [2][1024]
+    int16_t* held = reinterpret_cast<int16_t*>(part + 2 * kRouteThreads);  // [1024] the chunk's experts, if they fit
+    const int64_t t0 = (int64_t)blockIdx.x * a.chunk;
+    const int64_t t1 = t0 + a.chunk < a.T ? t0 + a.chunk : a.T;
+    const int32_t* ids = a.experts + t0 * a.k;
+    const int64_t n = (t1 - t0) * a.k;
+    int id = 0;
+    if (n <= kRouteThreads && threadIdx.x < n) id = ids[threadIdx.x];  // beside the counts
     int width = 16;
     while (width < a.E) width *= 2;
     const int S = kRouteThreads / width, s = (int)threadIdx.x / width, e = (int)threadIdx.x & (width - 1);
@@ -283,7 +353,7 @@ __global__ __launch_bounds__(kRouteThreads) void sort_chunk_kernel(RouteArgs a) 
     uint32_t before = 0, all = 0;
     if (e < a.E) {
         const uint32_t* p = a.counts + e;
-#pragma unroll 8
+#pragma unroll 16
         for (int c = s; c < chunks; c += S) {
             const uint32_t v = p[(int64_t)c * a.E];
             all += v;
@@ -300,11 +370,14 @@ __global__ __launch_bounds__(kRouteThreads) void sort_chunk_kernel(RouteArgs a) 
             all += part[kRouteThreads + i * width + threadIdx.x];
         }
     }
-    uint32_t total, chosen_before;
+    // places of the experts' first pairs, and how many of the pairs before this chunk
+    // have an expert
+    uint32_t total, chosen_before = wave_sum_u32(before);
+    if ((threadIdx.x & 63) == 0) hist[threadIdx.x >> 6] = chosen_before;  // read behind block_scan's barriers
     const uint32_t start = block_scan(all, scratch, &total);
-    block_scan(before, scratch, &chosen_before);
-    const int64_t t0 = (int64_t)mine * a.chunk;
-    const int64_t t1 = t0 + a.chunk < a.T ? t0 + a.chunk : a.T;
+    chosen_before = 0;
+#pragma unroll
+    for (int w = 0; w < kRouteWaves; ++w) chosen_before += hist[w];
     if ((int)threadIdx.x < a.E) {
         first[threadIdx.x] = start + before;
         if (mine == 0) a.offsets[threadIdx.x] = (int32_t)start;
@@ -313,14 +386,19 @@ __global__ __launch_bounds__(kRouteThreads) void sort_chunk_kernel(RouteArgs a) 
         first[a.E] = total + (uint32_t)(t0 * a.k) - chosen_before;
         if (mine == 0) a.offsets[a.E] = (int32_t)total;
     }
-    __syncthreads();
-    const int32_t* ids = a.experts + t0 * a.k;
-    sort_pairs(a, t0 * a.k, (t1 - t0) * a.k, hist,
-               [&](int64_t i) {
-                   const int id = ids[i];
-                   return id < 0 ? a.E : id;
-               },
-               [&](int c) { return first[c]; });
+    if (n <= kRouteThreads) {
+        if (threadIdx.x < n) held[threadIdx.x] = (int16_t)(id < 0 ? a.E : id);
+        __syncthreads();
+        sort_pairs(a, t0 * a.k, n, hist, [&](int64_t i) { return (int)held[i]; }, [&](int c) { return first[c]; });
+    } else {
+        __syncthreads();
+        sort_pairs(a, t0 * a.k, n, hist,
+                   [&](int64_t i) {
+                       const int e1 = ids[i];
+                       return e1 < 0 ? a.E : e1;
+                   },
+                   [&](int c) { return first[c]; });
+    }
 }
 
 template <class L, int LANES, int V>
@@ -340,14 +418,15 @@ hipError_t route_variant(const RouteArgs& a, hipStream_t s) {
     if ((e = hipGetLastError()) != hipSuccess) return e;
     e = raise_lds_limit(reinterpret_cast<const void*>(&sort_chunk_kernel), kRouteMaxLds, sort_set);
     if (e != hipSuccess) return e;
-    sort_chunk_kernel<<<chunks, kRouteThreads, lds + 2 * kRouteThreads * 4, s>>>(a);
+    sort_chunk_kernel<<<chunks, kRouteThreads, lds + 2 * kRouteThreads * 4 + kRouteThreads * 2, s>>>(a);
     return hipGetLastError();
 }
 
 template <class L>
 hipError_t route_type(const RouteArgs& a, hipStream_t s) {
     if (a.E > 256 || a.k > 16) return route_variant<L, 64, 16>(a, s);
-    if (a.E > 64) return route_variant<L, 16, 16>(a, s);
+    if (a.E > 128) return route_variant<L, 16, 16>(a, s);
+    if (a.E > 64) return route_variant<L, 16, 8>(a, s);
     return route_variant<L, 16, 4>(a, s);
 }
 
@@ -384,23 +463,42 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
         if constexpr (VEC) add8<T>(acc, *reinterpret_cast<const uint4*>(src), 1.0f);
         else acc[0] = T::to_f32(*src);
     }
-#pragma unroll 4
-    for (int j = 0; j < a.k; ++j) {
-        const int32_t p = places[j];
-        if (p < 0 || p >= a.P) continue;
-        const uint16_t* src = a.y + (int64_t)p * a.N + c;
-        if constexpr (VEC) add8<T>(acc, *reinterpret_cast<const uint4*>(src), weights[j]);
-        else acc[0] = fmaf(weights[j], T::to_f32(*src), acc[0]);
+    constexpr int U = 8;  // rows in flight
+    for (int j0 = 0; j0 < a.k; j0 += U) {
+        int32_t p[U];
+        float w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u < a.k ? j0 + u : a.k - 1;
+            p[u] = places[j];
+            w[u] = weights[j];
+        }
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (j0 + u >= a.k) break;
+            const bool in = p[u] >= 0 && p[u] < a.P;
+            const uint16_t* src = a.y + (int64_t)(in ? p[u] : 0) * a.N + c;
+            if constexpr (VEC) v[u] = *reinterpret_cast<const uint4*>(src);
+            else v[u].x = *src;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (j0 + u >= a.k) break;
+            if (p[u] < 0 || p[u] >= a.P) continue;
+            if constexpr (VEC) add8<T>(acc, v[u], w[u]);
+            else acc[0] = fmaf(w[u], T::to_f32((uint16_t)v[u].x), acc[0]);
+        }
     }
     uint16_t* dst = a.out + t * a.N + c;
     if constexpr (VEC) {
         uint32_t d[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            d[i] = (uint32_t)T::from_f32_fast(acc[2 * i]) | ((uint32_t)T::from_f32_fast(acc[2 * i + 1]) << 16);
+            d[i] = round_pair<T>(acc[2 * i], acc[2 * i + 1]);
         *reinterpret_cast<uint4*>(dst) = make_uint4(d[0], d[1], d[2], d[3]);
     } else {
-        *dst = T::from_f32_fast(acc[0]);
+        *dst = round_one<T>(acc[0]);
     }
 }
 
@@ -443,7 +541,9 @@ hipError_t launch_moe_route(const RouteArgs& args, hipStream_t s) {
     }
 }
 
-hipError_t launch_moe_combine(const CombineArgs& a, hipStream_t s) {
+hipError_t launch_moe_combine(const CombineArgs& args, hipStream_t s) {
+    CombineArgs a = args;
+    if (a.P == 0) a.k = 0;  // no place has a row
     const uintptr_t bits = reinterpret_cast<uintptr_t>(a.y) | reinterpret_cast<uintptr_t>(a.out) |
                            reinterpret_cast<uintptr_t>(a.add) | (uintptr_t)(a.add ? a.add_stride * 2 : 0);
     const bool vec = a.N % 8 == 0 && (bits & 15u) == 0;
