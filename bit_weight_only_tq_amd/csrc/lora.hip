@@ -44,6 +44,51 @@ struct Depth {
     static constexpr int kLd = 16 * RT + 4;  // words of a row of sums in LDS
 };
 
+// Rows of sums [16 MB][kLd] in LDS as operands of the second product: lane
+// 16 g + i has row i, ranks 32 s + 8 g .. + 7, as the rounded value and the rounded
+// rest of the sum times 2^-e, and `scale` 2^e.
+template <class T, int MB, int RT>
+__device__ __forceinline__ void split_sums16(const float* lds, int ld, float scale, u32x4 (&hi)[MB][(RT + 1) / 2],
+                                             u32x4 (&lo)[MB][(RT + 1) / 2], float (&factor)[MB]) {
+    constexpr int kKs = (RT + 1) / 2;
+    const int g = (threadIdx.x & 63) >> 4, i16 = threadIdx.x & 15;
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+        const float* sums = lds + (16 * m + i16) * ld;
+        f32x4 h[kKs][2];
+        float most = 0.0f;
+#pragma unroll
+        for (int s = 0; s < kKs; ++s)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                // ranks past 16 RT (RT = 1 alone): zeros
+                const int j = 32 * s + 8 * g + 4 * q;
+                h[s][q] = *reinterpret_cast<const f32x4*>(sums + (RT > 1 || j < 16 ? j : 0));
+                if (RT == 1 && j >= 16) h[s][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v = fabsf(h[s][q][e]);
+                    most = fmaxf(most, v < __builtin_inff() ? v : 0.0f);
+                }
+            }
+        most = fmaxf(most, __shfl_xor(most, 16, kWave));
+        most = fmaxf(most, __shfl_xor(most, 32, kWave));
+        int ex = most > 0.0f ? __builtin_amdgcn_frexp_expf(most) : 0;  // most = f 2^ex, 1/2 <= f < 1
+        ex = ex < -100 ? -100 : ex > 120 ? 120 : ex;                   // 2^ex is a normal number
+        factor[m] = ldexpf(scale, ex);
+#pragma unroll
+        for (int s = 0; s < kKs; ++s)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float v0 = ldexpf(h[s][e / 2][2 * (e % 2)], -ex), v1 = ldexpf(h[s][e / 2][2 * (e % 2) + 1], -ex);
+                const uint32_t top = round_pair<T>(v0, v1);
+                const float r0 = v0 - T::to_f32((uint16_t)top), r1 = v1 - T::to_f32((uint16_t)(top >> 16));
+                hi[m][s][e] = top;
+                lo[m][s][e] = round_pair<T>(fabsf(v0) < __builtin_inff() ? r0 : 0.0f, fabsf(v1) < __builtin_inff() ? r1 : 0.0f);
+            }
+    }
+}
+
 // The rows `mine` of the block at t0, all of adapter l (-1: none), and the columns
 // of the chunk.  W waves deal the columns of x in steps of 32 S (whole cache lines
 // of a row), then those of the output in steps of 32.  Both loops have the next
@@ -58,7 +103,7 @@ __device__ __forceinline__ void update(const LoraArgs& a, int64_t t0, uint32_t c
     constexpr int kThreads = W * kWave, kRows = 16 * MB;
     constexpr int kKs = (RT + 1) / 2;  // 32-deep steps of the second product
     constexpr int S = Q::S, D = Q::D, kAhead = Q::kAhead, kLd = Q::kLd;
-    extern __shared__ float smem_lora[];
+    extern __shared__ __attribute__((aligned(16))) float smem_lora[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int g = lane >> 4, i16 = lane & 15;
@@ -185,42 +230,7 @@ __device__ __forceinline__ void update(const LoraArgs& a, int64_t t0, uint32_t c
             *p = v;
         }
         __syncthreads();
-#pragma unroll
-        for (int m = 0; m < MB; ++m) {
-            const float* sums = smem_lora + (16 * m + i16) * kLd;
-            f32x4 h[kKs][2];
-            float most = 0.0f;
-#pragma unroll
-            for (int s = 0; s < kKs; ++s)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    // ranks past 16 RT (RT = 1 alone): zeros
-                    const int j = 32 * s + 8 * g + 4 * q;
-                    h[s][q] = *reinterpret_cast<const f32x4*>(sums + (RT > 1 || j < 16 ? j : 0));
-                    if (RT == 1 && j >= 16) h[s][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float v = fabsf(h[s][q][e]);
-                        most = fmaxf(most, v < __builtin_inff() ? v : 0.0f);
-                    }
-                }
-            most = fmaxf(most, __shfl_xor(most, 16, kWave));
-            most = fmaxf(most, __shfl_xor(most, 32, kWave));
-            int ex = most > 0.0f ? __builtin_amdgcn_frexp_expf(most) : 0;  // most = f 2^ex, 1/2 <= f < 1
-            ex = ex < -100 ? -100 : ex > 120 ? 120 : ex;                   // 2^ex is a normal number
-            factor[m] = ldexpf(scale, ex);
-#pragma unroll
-            for (int s = 0; s < kKs; ++s) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float v0 = ldexpf(h[s][e / 2][2 * (e % 2)], -ex), v1 = ldexpf(h[s][e / 2][2 * (e % 2) + 1], -ex);
-                    const uint32_t top = round_pair<T>(v0, v1);
-                    const float r0 = v0 - T::to_f32((uint16_t)top), r1 = v1 - T::to_f32((uint16_t)(top >> 16));
-                    hi[m][s][e] = top;
-                    lo[m][s][e] = round_pair<T>(fabsf(v0) < __builtin_inff() ? r0 : 0.0f, fabsf(v1) < __builtin_inff() ? r1 : 0.0f);
-                }
-            }
-        }
+        split_sums16<T, MB, RT>(smem_lora, kLd, scale, hi, lo, factor);
     }
 
     auto finish = [&](int n, const Cols& c) {
@@ -309,6 +319,278 @@ __global__ __launch_bounds__(W * kWave) void lora_kernel(LoraArgs a) {
     } while (left);
 }
 
+// ---------------------------------------------------------------- long prompts
+//
+// The same for 32 rows a workgroup and rank up to 64, with every operand brought to
+// LDS by DMA in whole cache lines.  Read straight into matrix operands (16 rows x
+// 64 bytes, neighbouring lanes in different rows) a compute unit gets 37 GB/s from
+// its L2, in lines of 128 bytes 119; the adapter alone is read once per 32 rows.
+// Each wave has a ring of its own of S stages, so the loops have no barrier:
+//  - first product: 64 columns of 32 rows of x and of the 16 RT rows of A;
+//  - second: 64 rows of B, which lie in a row, and 64 columns of base.
+// Chunk c (16 bytes) of row r of a 128-byte row lies at c ^ (r / 2 % 8).  The sum
+// takes the place of base in LDS and leaves from there, in lines again.
+// Rows and ranks past the end are the last one again (ranks past it count as 0).
+// Needs N % 8 == 0 and 16-byte aligned rows.
+template <int RT>
+struct Stage {
+    static constexpr int W = RT <= 2 ? 8 : 4, S = RT == 2 ? 2 : 3;
+    static constexpr int kBytes = 4096 + 2048 * RT;  // x and A, or base and 64 rows of B
+    static constexpr int kRing = W * S * kBytes;
+    static constexpr int kLd = 16 * RT + 4;
+    static_assert(W * 32 * kLd * 4 <= kRing, "the sums take the ring's place");
+};
+
+__device__ __forceinline__ int line_swizzle(int r) { return (r >> 1) & 7; }
+
+template <class T, int RT>
+__device__ __forceinline__ void update_staged(const LoraArgs& a, int64_t t0, uint32_t chunk, int l, uint64_t mine) {
+    typedef typename Mfma<T>::vec vec;
+    typedef Stage<RT> Q;
+    constexpr int W = Q::W, S = Q::S, kKs = (RT + 1) / 2, kLd = Q::kLd;
+    extern __shared__ __attribute__((aligned(16))) float smem_lora[];
+    uint8_t* lds = reinterpret_cast<uint8_t*>(smem_lora);
+    const uint32_t lds_base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)smem_lora;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int g = lane >> 4, i16 = lane & 15;
+    const int N = (int)a.N, K = (int)a.K, r = a.r;
+    const int n_lo = (int)chunk * (int)a.cols;
+    const int n_hi = n_lo + (int)a.cols < N ? n_lo + (int)a.cols : N;
+    const int rows = a.T - t0 < 32 ? (int)(a.T - t0) : 32;
+    const bool some = l >= 0;
+    uint8_t* const ring = lds + wave * (S * Q::kBytes);
+    const uint32_t ring_at = lds_base + (uint32_t)(wave * (S * Q::kBytes));
+
+    u32x4 hi[2][kKs], lo[2][kKs];  // operands of the second product: lane 16 g + i, row i, ranks 32 s + 8 g ..
+    float factor[2];
+    if (some) {
+        f32x4 acc[2][RT];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int q = 0; q < RT; ++q) acc[m][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        const uint16_t* x = a.x + t0 * a.x_stride;
+        const uint16_t* A = a.A + (int64_t)l * r * a.K;
+        uint32_t x_off[4], a_off[2 * RT];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int row = 8 * u + (lane >> 3);
+            x_off[u] = (uint32_t)((row < rows ? row : rows - 1) * a.x_stride) * 2u + 16u * ((lane & 7) ^ line_swizzle(row));
+        }
+#pragma unroll
+        for (int u = 0; u < 2 * RT; ++u) {
+            const int row = 8 * u + (lane >> 3);
+            a_off[u] = (uint32_t)((row < r ? row : r - 1) * K) * 2u + 16u * ((lane & 7) ^ line_swizzle(row));
+        }
+        constexpr int kCount = 4 + 2 * RT;  // transfers of a stage
+        auto issue = [&](int k0, int stage) {
+            const uint32_t to = ring_at + (uint32_t)(stage * Q::kBytes);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) dma16s(x + k0, x_off[u], to + 1024u * u);
+#pragma unroll
+            for (int u = 0; u < 2 * RT; ++u) dma16s(A + k0, a_off[u], to + 4096u + 1024u * u);
+        };
+        const int steps = K / 64;
+        const int own = steps > wave ? (steps - wave + W - 1) / W : 0;  // steps wave, wave + W, ...
+#pragma unroll
+        for (int d = 0; d < S - 1; ++d)
+            if (d < own) issue(64 * (wave + W * d), d);
+        int stage = 0;
+        for (int k = 0; k < own; ++k) {
+            // the stage read last is free: its reads have been used
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            if (k + S - 1 < own) {
+                issue(64 * (wave + W * (k + S - 1)), stage == 0 ? S - 1 : stage - 1);
+                asm volatile("s_waitcnt vmcnt(%0)" :: "n"((S - 1) * kCount) : "memory");
+            } else {
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            }
+            const uint8_t* p = ring + stage * Q::kBytes;
+            stage = stage == S - 1 ? 0 : stage + 1;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                vec xv[2], av[RT];
+                const int at = i16 * 128 + 16 * ((4 * u + g) ^ line_swizzle(i16));
+#pragma unroll
+                for (int m = 0; m < 2; ++m) xv[m] = __builtin_bit_cast(vec, *reinterpret_cast<const u32x4*>(p + 2048 * m + at));
+#pragma unroll
+                for (int q = 0; q < RT; ++q) av[q] = __builtin_bit_cast(vec, *reinterpret_cast<const u32x4*>(p + 4096 + 2048 * q + at));
+#pragma unroll
+                for (int q = 0; q < RT; ++q)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) acc[m][q] = Mfma<T>::mma(xv[m], av[q], acc[m][q]);
+            }
+        }
+        const int whole = K & ~63;
+        if (whole < K && wave == W - 1) {  // the rest, a multiple of 8 columns, through buffer bounds
+            const auto xbuf = buffer(x, ((rows - 1) * a.x_stride + K) * 2);
+            const auto abuf = buffer(A, (int64_t)r * K * 2);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int k = whole + 32 * u + 8 * g;
+                vec xv[2];
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+                    xv[m] = __builtin_bit_cast(vec, __builtin_amdgcn_raw_buffer_load_b128(
+                        xbuf, k < K && 16 * m + i16 < rows ? (uint32_t)((16 * m + i16) * a.x_stride + k) * 2u : kNowhere, 0, 0));
+#pragma unroll
+                for (int q = 0; q < RT; ++q) {
+                    const vec av = __builtin_bit_cast(vec, __builtin_amdgcn_raw_buffer_load_b128(
+                        abuf, k < K && 16 * q + i16 < r ? (uint32_t)((16 * q + i16) * K + k) * 2u : kNowhere, 0, 0));
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) acc[m][q] = Mfma<T>::mma(xv[m], av, acc[m][q]);
+                }
+            }
+        }
+        __syncthreads();  // the rings are idle
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int q = 0; q < RT; ++q)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) smem_lora[(wave * 32 + 16 * m + 4 * g + e) * kLd + 16 * q + i16] = acc[m][q][e];
+        __syncthreads();
+        for (int i = threadIdx.x; i < 32 * 4 * RT; i += W * kWave) {
+            const int j = 4 * (i % (4 * RT));
+            f32x4* p = reinterpret_cast<f32x4*>(smem_lora + (i / (4 * RT)) * kLd + j);
+            f32x4 v = *p;
+#pragma unroll
+            for (int w = 1; w < W; ++w) v += p[w * 32 * kLd / 4];
+            *p = j < r ? v : f32x4{0.f, 0.f, 0.f, 0.f};  // r is a multiple of 8
+        }
+        __syncthreads();
+        const float scale = a.scale ? a.scale[l] : 1.0f;
+        split_sums16<T, 2, RT>(smem_lora, kLd, scale, hi, lo, factor);
+        __syncthreads();  // the sums have been read: the rings again
+    }
+
+    // 64 columns of the output from n on.  Rows of B as they lie in memory, r values
+    // each; for r = 64 chunk c of row n at c ^ (n / 2 % 2 + 2 (n / 8 % 4)), so that the
+    // 16 rows of a matrix operand meet 16 different places.
+    const uint16_t* base = a.base + t0 * a.base_stride;
+    uint16_t* out = a.out + t0 * a.out_stride;
+    const uint16_t* B = some ? a.B + (int64_t)l * a.N * r : a.base;
+    const int b_count = some ? r / 8 : 0;  // transfers: 64 rows of 2 r bytes
+    uint32_t base_off[4];
+    int base_col[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int row = 8 * u + (lane >> 3);
+        base_off[u] = (uint32_t)((row < rows ? row : rows - 1) * a.base_stride) * 2u;
+        base_col[u] = 8 * ((lane & 7) ^ line_swizzle(row));
+    }
+    auto row_swizzle = [&](int n) { return ((n >> 1) & 1) | (((n >> 3) & 3) << 1); };
+    const uint32_t b_end = (uint32_t)N * (uint32_t)r * 2u - 16u;
+    auto issue = [&](int n, int stage) {
+        const uint32_t to = ring_at + (uint32_t)(stage * Q::kBytes);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int col = n + base_col[u] < N ? n + base_col[u] : N - 8;
+            dma16s(base, base_off[u] + 2u * col, to + 1024u * u);
+        }
+#pragma unroll
+        for (int u = 0; u < 2 * RT; ++u)
+            if (u < b_count) {
+                uint32_t off = (uint32_t)n * r * 2u + 1024u * u + 16u * lane;
+                if (r == 64) off ^= 16u * row_swizzle(8 * u + (lane >> 3));
+                dma16s(B, off < b_end ? off : b_end, to + 4096u + 1024u * u);
+            }
+    };
+    auto at = [&](int i) { return n_lo + 64 * (wave + W * i); };
+    int own = 0;
+    while (at(own) < n_hi) ++own;
+#pragma unroll
+    for (int d = 0; d < S - 1; ++d)
+        if (d < own) issue(at(d), d);
+    int stage = 0;
+    for (int i = 0; i < own; ++i) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the stage read last is free
+        if (i + S - 1 < own) issue(at(i + S - 1), stage == 0 ? S - 1 : stage - 1);
+        // Stores are counted with the transfers: with the four of the last step behind
+        // this stage's, all that was issued before them has landed.
+        if (i + S - 1 < own) {
+            if (some) {
+                if (r == 16 * RT) asm volatile("s_waitcnt vmcnt(%0)" :: "n"((S - 1) * (4 + 2 * RT)) : "memory");
+                else asm volatile("s_waitcnt vmcnt(%0)" :: "n"((S - 1) * 5) : "memory");
+            } else {
+                asm volatile("s_waitcnt vmcnt(%0)" :: "n"((S - 1) * 4) : "memory");
+            }
+        } else {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+        uint8_t* p = ring + stage * Q::kBytes;
+        stage = stage == S - 1 ? 0 : stage + 1;
+        const int n = at(i);
+        if (some) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                f32x4 d[2][2];
+#pragma unroll
+                for (int m = 0; m < 2; ++m) d[m][0] = d[m][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int row = 32 * half + 8 * (i16 >> 2) + 4 * t + (i16 & 3);
+#pragma unroll
+                    for (int st = 0; st < kKs; ++st) {
+                        const int j = 32 * st + 8 * g;
+                        uint32_t off = (uint32_t)row * r * 2u + (j < r ? 2u * j : 0u);
+                        if (r == 64) off ^= 16u * row_swizzle(row);
+                        u32x4 b = *reinterpret_cast<const u32x4*>(p + 4096 + off);
+                        const uint32_t keep = j < r ? ~0u : 0u;
+                        b &= keep;
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            d[m][t] = Mfma<T>::mma(__builtin_bit_cast(vec, b), __builtin_bit_cast(vec, hi[m][st]), d[m][t]);
+                            d[m][t] = Mfma<T>::mma(__builtin_bit_cast(vec, b), __builtin_bit_cast(vec, lo[m][st]), d[m][t]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    u32x4* q = reinterpret_cast<u32x4*>(p + (16 * m + i16) * 128 + 16 * ((4 * half + g) ^ line_swizzle(i16)));
+                    u32x4 v = *q;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = round_pair<T>(fmaf(factor[m], d[m][e / 2][2 * (e % 2)], T::to_f32((uint16_t)v[e])),
+                                             fmaf(factor[m], d[m][e / 2][2 * (e % 2) + 1], T::to_f32((uint16_t)(v[e] >> 16))));
+                    *q = v;
+                }
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int row = 8 * u + (lane >> 3);
+            const u32x4 v = *reinterpret_cast<const u32x4*>(p + 1024 * u + 16 * lane);
+            if (((mine >> row) & 1) && n + base_col[u] < n_hi)
+                *reinterpret_cast<u32x4*>(out + (int64_t)row * a.out_stride + n + base_col[u]) = v;
+        }
+    }
+}
+
+template <class T, int RT>
+__global__ __launch_bounds__(Stage<RT>::W * kWave) void staged_kernel(LoraArgs a) {
+    const int lane = threadIdx.x & 63;
+    const int64_t t0 = (int64_t)(blockIdx.x / (uint32_t)a.chunks) * 32;
+    const uint32_t chunk = blockIdx.x % (uint32_t)a.chunks;
+    int id = -2;
+    if (lane < 32 && t0 + lane < a.T) {
+        id = a.ids[t0 + lane];
+        if (id < 0 || id >= a.L) id = -1;
+    }
+    uint64_t left = __ballot(id > -2);
+    do {
+        const int l = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        const uint64_t mine = __ballot(id == l);
+        left &= ~mine;
+        if (!(l < 0 && a.out == a.base)) {
+            update_staged<T, RT>(a, t0, chunk, l, mine);
+            if (left) __syncthreads();  // every wave's ring is idle
+        }
+    } while (left);
+}
+
 constexpr int64_t kLoraDecodeRows = 256;
 
 template <class T, int MB, int RT, int W>
@@ -348,11 +630,46 @@ hipError_t launch_variant(const LoraArgs& args, hipStream_t s) {
     return hipSuccess;
 }
 
+template <class T, int RT>
+hipError_t launch_staged(const LoraArgs& args, hipStream_t s) {
+    typedef Stage<RT> Q;
+    static DeviceFlags set;
+    hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&staged_kernel<T, RT>), Q::kRing, set);
+    if (e != hipSuccess) return e;
+    constexpr int64_t kMostRows = (int64_t)1 << 20;
+    for (int64_t t = 0; t < args.T; t += kMostRows) {
+        LoraArgs a = args;
+        a.T = args.T - t < kMostRows ? args.T - t : kMostRows;
+        a.x += t * a.x_stride;
+        a.base += t * a.base_stride;
+        a.out += t * a.out_stride;
+        a.ids += t;
+        a.blocks = (a.T + 31) / 32;
+        // one workgroup a compute unit (its rings take most of the LDS)
+        const int64_t pass = 64 * Q::W, passes = (a.N + pass - 1) / pass;
+        int64_t want = (compute_units() + a.blocks - 1) / a.blocks;
+        if (want > passes) want = passes;
+        a.cols = (passes + want - 1) / want * pass;
+        a.chunks = (a.N + a.cols - 1) / a.cols;
+        staged_kernel<T, RT><<<(unsigned)(a.blocks * a.chunks), Q::W * kWave, Q::kRing, s>>>(a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 // Few rows: 16 waves, so that one pass of loads covers 4096 columns.  Many: 32
-// rows, so that an adapter is read half as often.
+// rows, so that an adapter is read half as often, and through LDS where rows are
+// whole 16-byte vectors.
 template <class T>
 hipError_t launch_type(const LoraArgs& a, hipStream_t s) {
     if (a.T >= 2048) {
+        const bool vec = a.N % 8 == 0 && ((a.base_stride | a.out_stride) & 7) == 0 &&
+                         ((reinterpret_cast<uintptr_t>(a.base) | reinterpret_cast<uintptr_t>(a.out)) & 15u) == 0;
+        if (vec && a.r <= 64 && a.K >= 64) {
+            if (a.r <= 16) return launch_staged<T, 1>(a, s);
+            if (a.r <= 32) return launch_staged<T, 2>(a, s);
+            return launch_staged<T, 4>(a, s);
+        }
         if (a.r <= 16) return launch_variant<T, 2, 1, 8>(a, s);
         if (a.r <= 32) return launch_variant<T, 2, 2, 8>(a, s);
         if (a.r <= 64) return launch_variant<T, 2, 4, 8>(a, s);

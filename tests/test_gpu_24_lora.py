@@ -83,6 +83,17 @@ def test_mixtures(T, L):
     check(T, 320, 264, L, 64, "f16", seed=L, ids=np.searchsorted(cuts, np.arange(T), side="right") % L)
 
 
+@pytest.mark.parametrize("r", [8, 16, 24, 32, 40, 64, 72, 256])
+def test_long_prompts(r):
+    """From 2048 rows on: whole and ragged columns, K that ends inside a step, blocks of several adapters, rows without one."""
+    log(f"lora prompts r={r}")
+    ids = np.repeat([0, 2, -1, 1, 5, 0], [700, 13, 64, 1000, 200, 100])[:2055]
+    assert len(ids) == 2055
+    check(2055, 200, 520, 3, r, "bf16", seed=r, ids=ids)
+    check(2055, 64, 72, 3, r, "f16", seed=r, ids=ids)
+    check(2048, 1096, 1032, 2, r, "f16", seed=r + 1)
+
+
 def test_ids_of_any_values():
     log("lora ids")
     check(9, 64, 48, 2, 8, "f16", ids=[0, -1, 1, 2, -2 ** 31, 2 ** 31 - 1, 1, 0, -2])
