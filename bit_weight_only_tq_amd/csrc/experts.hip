@@ -171,47 +171,53 @@ __device__ __forceinline__ Place find_tile(const ExpertArgs& a, int BM, uint32_t
 
 // ---------------------------------------------------------------- few rows
 //
-// BM rows of one expert (16, or 4 where experts have one or two: a matrix tile
-// has 16 either way) and 32 weight rows a wave.  The call is bound by the read of
-// the weights, so what counts is bytes in flight and whole cache lines: read
-// straight into matrix operands, 16 rows x 64 bytes an instruction, a compute
-// unit gets 37 GB/s from its L2, in lines of 128 bytes 119 GB/s.  So codes and
-// activations go to LDS by DMA, a step of 128 code bytes a row (256 columns of
-// W4A16, 512 ternary ones), into a ring of kStages steps:
-//  - codes: [32 rows a wave][8 chunks of 16 bytes], chunk c of row r at c ^ (r / 2 % 8);
+// BM rows of one expert (4 to 64; a matrix tile has 16 in any case) and 32 weight
+// rows a wave.  Such calls are bound by the read of the weights, so what counts is
+// bytes in flight and whole cache lines: read straight into matrix operands, 16
+// rows x 64 bytes an instruction, a compute unit gets 37 GB/s from its L2, in lines
+// of 128 bytes 119 GB/s.  So codes and activations go to LDS by DMA, a step of RB
+// code bytes a row (128, or 64 where 16 rows of activations and more need the room:
+// two workgroups a compute unit instead of one hide more than half lines cost, 53
+// instead of 55 us for 48 tokens of 64 experts and 67 instead of 87 for 1010 of 87),
+// into a ring of two steps (three: 65 instead of 58 us, for half the workgroups):
+//  - codes: [32 rows a wave][RB / 16 chunks of 16 bytes], chunk c of row r at
+//    c ^ (r / 2 % 8), or c ^ (r / 4 % 4) of 64 bytes;
 //  - activations: [BM rows][BK columns], chunk c of row r at c ^ (r % 16).
 // NW waves share a step's activations; KW groups of waves deal the steps where
 // there are too few weight rows to fill the compute units, and their sums meet in
 // LDS in the groups' order.
-// Lane 16 g + i of a wave takes chunk 4 h + g of weight row i (h = 0, 1) and the
-// activations of the same columns of row i.  W4A16: that is one scale group an h,
+// Lane 16 g + i of a wave takes chunk 4 h + g of weight row i (h = 0, and 1 where
+// RB is 128) and the activations of the same columns of row i.  W4A16: that is one scale group an h,
 // whose sum starts from zero and is scaled into the result.
 // Gated: a wave's first 16 weight rows are the gate's, the others the same rows of
 // the up projection.
 namespace narrow {
 
-template <int FMT, int BM, int KW, int NW>
+template <int FMT, int BM, int KW, int NW, int RB>
 struct Ring {
-    // two steps in the ring where a step's activations are as many bytes as its codes
     static constexpr int kStages = 2;
     static constexpr int kWaves = KW * NW, kThreads = kWaves * kWave;
-    static constexpr int BK = FMT == 0 ? 512 : 256;
+    static constexpr int kRowBytes = RB;                       // of codes, a row and step
+    static constexpr int BK = FMT == 0 ? RB * 4 : RB * 2;      // columns of a step
+    static constexpr int kHalves = kRowBytes / 64;
+    static constexpr int MT = BM <= 16 ? 1 : BM / 16;             // matrix tiles of activation rows
     static constexpr int kABytes = BM * BK * 2;
-    static constexpr int kBBytes = NW * 32 * 128;
+    static constexpr int kBBytes = NW * 32 * kRowBytes;
     static constexpr int kStageBytes = kABytes + kBBytes;      // of a group of waves
     static constexpr int kBytes = kStages * KW * kStageBytes;
     static constexpr int AU = kABytes / 1024 >= NW ? kABytes / 1024 / NW : 1;  // 1-KB transfers a wave and step
-    static constexpr int BU = 4;
+    static constexpr int BU = kRowBytes / 32;
     // scales and zero points held in LDS, at most
     static constexpr int kScaleBytes = FMT == 0 ? 0 : kBytes + 49152 <= 163840 ? 49152 : 163840 - kBytes;
     static_assert(kBytes <= 163840, "a compute unit has 160 KB");
 };
 
-template <class T, int FMT, bool ASYM, bool GATED, int BM, int KW, int NW>
+template <class T, int FMT, bool ASYM, bool GATED, int BM, int KW, int NW, int RB>
 __global__ __launch_bounds__(KW * NW * kWave) void kernel(ExpertArgs a, int scale_bytes) {
     typedef typename Mfma<T>::vec vec;
-    typedef Ring<FMT, BM, KW, NW> G;
-    constexpr int BK = G::BK, AU = G::AU, BU = G::BU, kStages = G::kStages;
+    typedef Ring<FMT, BM, KW, NW, RB> G;
+    constexpr int BK = G::BK, AU = G::AU, BU = G::BU, kStages = G::kStages, MT = G::MT, kRowBytes = G::kRowBytes;
+    constexpr int kChunks = kRowBytes / 16;           // of a row's codes
     constexpr int kCols = GATED ? 16 * NW : 32 * NW;  // output columns of the workgroup
     constexpr int kUnits = FMT == 0 ? 8 : 4;          // 8-column units of a 16-byte chunk of codes
     extern __shared__ uint4 smem_narrow[];
@@ -251,21 +257,18 @@ __global__ __launch_bounds__(KW * NW * kWave) void kernel(ExpertArgs a, int scal
     // DMA sources.  Codes: lane l has chunk (l % 8) ^ (row / 2 % 8) of row 8 u + l / 8 of
     // the wave's 32.  Activations: 16-byte chunks of the group's rows in LDS order.
     // In the last step what lies past the row is its last chunk again.
+    // swizzle of a row of codes: as many rows span the banks as 256 bytes hold
+    auto code_swizzle = [](int r) { return kChunks == 8 ? (r >> 1) & 7 : (r >> 2) & 3; };
     uint32_t b_row[BU];
-    uint32_t b_chunk[2];  // of even and of odd u
-    b_chunk[0] = 16u * ((lane & 7) ^ (lane >> 4));
-    b_chunk[1] = b_chunk[0] ^ 64u;
+    const int b_lane = lane / kChunks;  // row of a transfer
 #pragma unroll
-    for (int u = 0; u < BU; ++u) b_row[u] = weight_row(32 * nw + 8 * u + (lane >> 3)) * rb;
+    for (int u = 0; u < BU; ++u) b_row[u] = weight_row(32 * nw + 64 / kChunks * u + b_lane) * rb;
     auto issue_codes = [&](int step, uint32_t at) {
-        uint32_t off[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const uint32_t byte = 128u * (from + step) + b_chunk[u];
-            off[u] = byte < rb ? byte : rb - 16;
+        for (int u = 0; u < BU; ++u) {
+            const uint32_t byte = (uint32_t)kRowBytes * (from + step) + 16u * ((lane % kChunks) ^ code_swizzle(64 / kChunks * u + b_lane));
+            dma16s(w_exp, b_row[u] + (byte < rb ? byte : rb - 16), at + G::kABytes + 32u * kRowBytes * nw + 1024u * u);
         }
-#pragma unroll
-        for (int u = 0; u < BU; ++u) dma16s(w_exp, b_row[u] + off[u % 2], at + G::kABytes + 4096u * nw + 1024u * u);
     };
     constexpr int kRowChunks = BK / 8;
     const uint8_t* a_row[AU];
@@ -309,10 +312,11 @@ __global__ __launch_bounds__(KW * NW * kWave) void kernel(ExpertArgs a, int scal
     for (int k = 0; k < kStages - 1; ++k)
         if (k < mine) issue_rows(k, stage_at(k));
 
-    f32x4 acc[2];
-    acc[0] = acc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 acc[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int a_frag = (i16 % BM) * (BK * 2), a_swz = i16 % BM;
-    const int b_frag = G::kABytes + (32 * nw + i16) * 128, b_swz = i16 >> 1;
+    const int b_frag = G::kABytes + (32 * nw + i16) * kRowBytes, b_swz = code_swizzle(i16);
     const uint32_t magic_v = vgpr_const<kMagic2>();
     const uint32_t mask_v = sgpr_const<0x00F0000Fu>();
     const NatConsts nat = nat_consts();
@@ -323,20 +327,22 @@ __global__ __launch_bounds__(KW * NW * kWave) void kernel(ExpertArgs a, int scal
     // weights and activations of 0.
     auto contract = [&](auto part, const uint8_t* sbase, int k, int h) {
         constexpr bool PART = decltype(part)::value;
-        const bool past = PART && BK * (from + k) + (BK / 2) * h + 64 * g >= K;
+        const bool past = PART && BK * (from + k) + 16 * kUnits * 2 * h + 64 * g >= K;
         uint4 q[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            q[j] = *reinterpret_cast<const uint4*>(sbase + b_frag + 2048 * j + 16 * ((4 * h + g) ^ b_swz));
+            q[j] = *reinterpret_cast<const uint4*>(sbase + b_frag + 16 * kRowBytes * j + 16 * ((4 * h + g) ^ b_swz));
             if (past) q[j] = make_uint4(0x55555555u, 0x55555555u, 0x55555555u, 0x55555555u);
         }
-        f32x4 sum[2];
-        if constexpr (FMT == 1) sum[0] = sum[1] = f32x4{0.f, 0.f, 0.f, 0.f};
-        else sum[0] = acc[0], sum[1] = acc[1];
+        f32x4 sum[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) sum[m][j] = FMT == 1 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[m][j];
         float s[2];
         W4Unpack<T, ASYM> un[2];
         if constexpr (FMT == 1) {
-            const int group = 2 * (from + k) + h;
+            const int group = G::kHalves * (from + k) + h;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int at = (32 * nw + 16 * j + i16) * GK + group;
@@ -348,8 +354,13 @@ __global__ __launch_bounds__(KW * NW * kWave) void kernel(ExpertArgs a, int scal
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const int chunk = 4 * kUnits * h + kUnits * g + u;
-            uint4 av = *reinterpret_cast<const uint4*>(sbase + a_frag + 16 * (chunk ^ a_swz));
-            if (past) av = make_uint4(0, 0, 0, 0);
+            vec av[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                uint4 v = *reinterpret_cast<const uint4*>(sbase + a_frag + 16 * m * (BK * 2) + 16 * (chunk ^ a_swz));
+                if (past) v = make_uint4(0, 0, 0, 0);
+                av[m] = __builtin_bit_cast(vec, v);
+            }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 uint4 b;
@@ -359,21 +370,24 @@ __global__ __launch_bounds__(KW * NW * kWave) void kernel(ExpertArgs a, int scal
                 } else {
                     b = un[j].quad(dword_of(q[j], u), mask_v, magic_v);
                 }
-                sum[j] = Mfma<T>::mma(__builtin_bit_cast(vec, av), __builtin_bit_cast(vec, b), sum[j]);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) sum[m][j] = Mfma<T>::mma(av[m], __builtin_bit_cast(vec, b), sum[m][j]);
             }
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if constexpr (FMT == 1) {
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[j][i] = fmaf(s[j], sum[j][i], acc[j][i]);
-            } else {
-                acc[j] = sum[j];
+            for (int j = 0; j < 2; ++j) {
+                if constexpr (FMT == 1) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[m][j][i] = fmaf(s[j], sum[m][j][i], acc[m][j][i]);
+                } else {
+                    acc[m][j] = sum[m][j];
+                }
             }
-        }
     };
     auto half = [&](const uint8_t* sbase, int k, int h) {
-        if (FMT == 0 && BK * (from + k) + (BK / 2) * (h + 1) > K) contract(std::true_type{}, sbase, k, h);
+        if (FMT == 0 && BK * (from + k) + 256 * (h + 1) > K) contract(std::true_type{}, sbase, k, h);
         else contract(std::false_type{}, sbase, k, h);
     };
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -389,7 +403,7 @@ __global__ __launch_bounds__(KW * NW * kWave) void kernel(ExpertArgs a, int scal
         if (k < mine) {
             const uint8_t* sbase = lds + (stage * KW + kw) * G::kStageBytes;
             half(sbase, k, 0);
-            if (BK * (from + k) + BK / 2 < K) half(sbase, k, 1);
+            if (G::kHalves == 2 && BK * (from + k) + BK / 2 < K) half(sbase, k, 1);
         }
         stage = stage == kStages - 1 ? 0 : stage + 1;
         // the next step has landed; of the later ones only the last may be on its way
@@ -399,17 +413,23 @@ __global__ __launch_bounds__(KW * NW * kWave) void kernel(ExpertArgs a, int scal
     }
 
     if constexpr (KW > 1) {  // the groups' sums, in their order
-        f32x4* red = reinterpret_cast<f32x4*>(lds);  // [KW - 1][NW][2][64]: the ring is idle
+        constexpr int kTiles = NW * MT * 2;
+        f32x4* red = reinterpret_cast<f32x4*>(lds) + nw * (MT * 2 * kWave) + lane;  // [KW - 1][NW][MT][2][64]: the ring is idle
+        static_assert((KW - 1) * kTiles * 1024 <= G::kBytes, "the sums take the ring's place");
         if (kw > 0) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) red[(((kw - 1) * NW + nw) * 2 + j) * kWave + lane] = acc[j];
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) red[((kw - 1) * kTiles + 2 * m + j) * kWave] = acc[m][j];
         }
         __syncthreads();
         if (kw > 0) return;
 #pragma unroll
         for (int z = 0; z < KW - 1; ++z)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) acc[j] += red[((z * NW + nw) * 2 + j) * kWave + lane];
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[m][j] += red[(z * kTiles + 2 * m + j) * kWave];
     }
     // lane 16 g + i: rows 4 g .. 4 g + 3, weight row i of each block
     const int64_t bias_row = (int64_t)blk.expert * N;
@@ -420,30 +440,33 @@ __global__ __launch_bounds__(KW * NW * kWave) void kernel(ExpertArgs a, int scal
         bi[j] = a.bias ? T::to_f32(a.bias[bias_row + sr[j]]) : 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = 4 * g + i;
-        if (row >= blk.rows || row >= BM) continue;
-        uint16_t* dst = a.C + (blk.row + row) * width;
-        if constexpr (GATED) {
-            const int64_t c = c0 + 16 * nw + i16;
-            if (c < width) dst[c] = T::from_f32_fast(gate(fmaf(acc[0][i], sc[0], bi[0]), fmaf(acc[1][i], sc[1], bi[1])));
-        } else {
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int64_t c = c0 + 32 * nw + 16 * j + i16;
-                if (c < width) dst[c] = T::from_f32_fast(fmaf(acc[j][i], sc[j], bi[j]));
+        for (int i = 0; i < 4; ++i) {
+            const int row = 16 * m + 4 * g + i;
+            if (row >= blk.rows || row >= BM) continue;
+            uint16_t* dst = a.C + (blk.row + row) * width;
+            if constexpr (GATED) {
+                const int64_t c = c0 + 16 * nw + i16;
+                if (c < width)
+                    dst[c] = round_one<T>(gate(fmaf(acc[m][0][i], sc[0], bi[0]), fmaf(acc[m][1][i], sc[1], bi[1])));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int64_t c = c0 + 32 * nw + 16 * j + i16;
+                    if (c < width) dst[c] = round_one<T>(fmaf(acc[m][j][i], sc[j], bi[j]));
+                }
             }
         }
-    }
 }
 
 }  // namespace narrow
 
 // ---------------------------------------------------------------- many rows
 //
-// BM rows of one expert and 256 weight rows a workgroup, four waves of BM x 64.
+// 128 rows of one expert and 256 weight rows a workgroup, four waves of 128 x 64.
 // Activations and codes come by DMA (no registers) into a ring of three stages of
-// 64 columns, two or three ahead of the matrix cores: BM rows x 128 bytes, 16-byte chunks
+// 64 columns, two or three ahead of the matrix cores: 128 rows x 128 bytes, 16-byte chunks
 // XOR-swizzled (chunk c of row r at c ^ (r / 2 % 8): two rows span the banks, so 16
 // rows' reads of a chunk meet 16 different places), and 256 weight rows x 16 or 32
 // bytes.  Codes are unpacked in registers in the natural order of their columns.
@@ -458,12 +481,12 @@ __global__ __launch_bounds__(KW * NW * kWave) void kernel(ExpertArgs a, int scal
 // words are replaced by those of zero weights.
 namespace tile {
 
-constexpr int BN = 256, BK = 64, WN = 64, TN = 4;
+constexpr int BM = 128, BN = 256, BK = 64, WN = 64, TN = 4;
 constexpr int kWaves = 4, kThreads = kWaves * kWave;
 constexpr int kStages = 3;
 constexpr int kEpiLd = WN + 8;  // halves of a row staged for its store
 
-template <int FMT, int BM>
+template <int FMT>
 struct Ring {
     static constexpr int kABytes = BM * BK * 2;
     static constexpr int kBBytes = BN * BK / (FMT == 0 ? 4 : 2);
@@ -474,10 +497,10 @@ struct Ring {
     static_assert(kWaves * 32 * kEpiLd * 2 <= kBytes, "epilogue staging must fit in the ring");
 };
 
-template <class T, int FMT, bool ASYM, bool GATED, int BM>
+template <class T, int FMT, bool ASYM, bool GATED>
 __global__ __launch_bounds__(kThreads, 2) void kernel(ExpertArgs a) {
     typedef typename Mfma<T>::vec vec;
-    typedef Ring<FMT, BM> G;
+    typedef Ring<FMT> G;
     constexpr int TM = BM / 16, AU = G::AU, BU = G::BU;
     constexpr int kCols = GATED ? BN / 2 : BN;  // output columns of the tile
     extern __shared__ uint4 smem_tile[];
@@ -752,11 +775,11 @@ int64_t most_blocks(int64_t P, int64_t E, int64_t BM) {
     return (P + used * (BM - 1)) / BM;
 }
 
-template <class T, int FMT, bool ASYM, bool GATED, int BM, int KW, int NW>
+template <class T, int FMT, bool ASYM, bool GATED, int BM, int KW, int NW, int RB>
 hipError_t launch_narrow(const ExpertArgs& args, hipStream_t s) {
-    typedef narrow::Ring<FMT, BM, KW, NW> G;
+    typedef narrow::Ring<FMT, BM, KW, NW, RB> G;
     static DeviceFlags lds_limit_set;
-    hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&narrow::kernel<T, FMT, ASYM, GATED, BM, KW, NW>),
+    hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&narrow::kernel<T, FMT, ASYM, GATED, BM, KW, NW, RB>),
                                    G::kBytes + G::kScaleBytes, lds_limit_set);
     if (e != hipSuccess) return e;
     const int64_t width = GATED ? args.N / 2 : args.N, cols = (GATED ? 16 : 32) * NW;
@@ -768,49 +791,102 @@ hipError_t launch_narrow(const ExpertArgs& args, hipStream_t s) {
     constexpr int64_t kMost = kMaxGroups / 8 * 8;
     for (a.first = 0; a.first < groups; a.first += kMost) {
         const int64_t n = groups - a.first < kMost ? groups - a.first : kMost;
-        narrow::kernel<T, FMT, ASYM, GATED, BM, KW, NW><<<(unsigned)n, G::kThreads, G::kBytes + scale_bytes, s>>>(a, scale_bytes);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    return hipSuccess;
-}
-
-// Four waves a workgroup: side by side over the weight rows where that makes two
-// workgroups a compute unit of the experts that have rows, else over the columns.
-template <class T, int FMT, bool ASYM, bool GATED, int BM>
-hipError_t launch_few(const ExpertArgs& a, hipStream_t s) {
-    const int64_t blocks = a.P < a.E ? a.P : a.E;
-    const int64_t rows = blocks * a.N;  // weight rows
-    if (rows >= 2 * 128 * compute_units()) return launch_narrow<T, FMT, ASYM, GATED, BM, 1, 4>(a, s);
-    if (rows >= 2 * 64 * compute_units()) return launch_narrow<T, FMT, ASYM, GATED, BM, 2, 2>(a, s);
-    return launch_narrow<T, FMT, ASYM, GATED, BM, 4, 1>(a, s);
-}
-
-template <class T, int FMT, bool ASYM, bool GATED, int BM>
-hipError_t launch_tile(const ExpertArgs& args, hipStream_t s) {
-    typedef tile::Ring<FMT, BM> G;
-    static DeviceFlags lds_limit_set;
-    hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&tile::kernel<T, FMT, ASYM, GATED, BM>), G::kBytes + G::kScaleBytes, lds_limit_set);
-    if (e != hipSuccess) return e;
-    const int64_t width = GATED ? args.N / 2 : args.N, cols = GATED ? tile::BN / 2 : tile::BN;
-    const int64_t groups = ((width + cols - 1) / cols * most_blocks(args.P, args.E, BM) + 7) / 8 * 8;
-    if (groups >= (int64_t)1 << 31) return hipErrorInvalidValue;  // an output of more than 2^44 values
-    ExpertArgs a = args;
-    constexpr int64_t kMost = kMaxGroups / 8 * 8;
-    for (a.first = 0; a.first < groups; a.first += kMost) {
-        const int64_t n = groups - a.first < kMost ? groups - a.first : kMost;
-        tile::kernel<T, FMT, ASYM, GATED, BM><<<(unsigned)n, tile::kThreads, G::kBytes + G::kScaleBytes, s>>>(a);
+        narrow::kernel<T, FMT, ASYM, GATED, BM, KW, NW, RB><<<(unsigned)n, G::kThreads, G::kBytes + scale_bytes, s>>>(a, scale_bytes);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     return hipSuccess;
 }
 
 template <class T, int FMT, bool ASYM, bool GATED>
+hipError_t launch_tile(const ExpertArgs& args, hipStream_t s) {
+    typedef tile::Ring<FMT> G;
+    static DeviceFlags lds_limit_set;
+    hipError_t e = raise_lds_limit(reinterpret_cast<const void*>(&tile::kernel<T, FMT, ASYM, GATED>), G::kBytes + G::kScaleBytes, lds_limit_set);
+    if (e != hipSuccess) return e;
+    const int64_t width = GATED ? args.N / 2 : args.N, cols = GATED ? tile::BN / 2 : tile::BN;
+    const int64_t groups = ((width + cols - 1) / cols * most_blocks(args.P, args.E, tile::BM) + 7) / 8 * 8;
+    if (groups >= (int64_t)1 << 31) return hipErrorInvalidValue;  // an output of more than 2^44 values
+    ExpertArgs a = args;
+    constexpr int64_t kMost = kMaxGroups / 8 * 8;
+    for (a.first = 0; a.first < groups; a.first += kMost) {
+        const int64_t n = groups - a.first < kMost ? groups - a.first : kMost;
+        tile::kernel<T, FMT, ASYM, GATED><<<(unsigned)n, tile::kThreads, G::kBytes + G::kScaleBytes, s>>>(a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+// The workgroups a call can be cut into: rows of activations, weight rows, parts
+// the columns are dealt to, bytes of a weight row's codes in a step; and the time
+// of a step in us, of a workgroup with a compute unit to itself and for each
+// workgroup where several share one (ternary, W4A16, W4A16 with zero points).
+struct Cut {
+    int rows, weights, parts, bytes;
+    float alone[3], shared[3];
+};
+
+constexpr Cut kCuts[] = {
+    {4, 128, 1, 128, {1.20f, 1.10f, 1.72f}, {0.93f, 0.86f, 1.02f}},
+    {4, 64, 2, 128, {1.25f, 1.13f, 1.52f}, {0.87f, 0.77f, 0.89f}},
+    {4, 32, 4, 128, {1.25f, 1.27f, 1.59f}, {1.03f, 0.79f, 0.85f}},
+    {16, 128, 1, 64, {0.77f, 0.68f, 1.01f}, {0.53f, 0.44f, 0.52f}},
+    {16, 64, 2, 64, {0.83f, 0.74f, 1.06f}, {0.61f, 0.47f, 0.50f}},
+    {16, 32, 4, 64, {1.00f, 0.83f, 1.20f}, {0.90f, 0.55f, 0.60f}},
+    {32, 128, 1, 64, {1.01f, 0.76f, 1.11f}, {0.74f, 0.56f, 0.66f}},
+    {64, 128, 1, 64, {1.48f, 1.00f, 1.37f}, {1.28f, 0.78f, 1.07f}},
+    {tile::BM, tile::BN, 1, 0, {0.70f, 0.98f, 1.10f}, {0.91f, 1.06f, 1.18f}},
+};
+
+// The cut of the shortest estimated time: few rows waste the rows of a large
+// block, few blocks leave compute units idle, and a long row takes one workgroup
+// many steps.  kCuts was fitted to every cut's time for 206 calls (1 to 4096
+// tokens, 1 to 96 experts, 512 to 14336 columns): the one taken here is 3 %
+// slower than the best of the nine in the mean and 26 % at worst; by rows an expert
+// alone it is 28 % and fivefold.  Without any one of them the best is 12 to 47 % slower
+// for some call.
+int choose_cut(const ExpertArgs& a) {
+    const int kind = a.fmt == 0 ? 0 : a.zeros ? 2 : 1;
+    const int64_t used = a.P < a.E ? a.P : a.E;
+    int best = 0;
+    double best_time = 0;
+    for (int i = 0; i < (int)(sizeof(kCuts) / sizeof(kCuts[0])); ++i) {
+        const Cut& c = kCuts[i];
+        const bool tiled = c.rows == tile::BM;
+        const int64_t bk = tiled ? tile::BK : c.bytes * (a.fmt == 0 ? 4 : 2);
+        const int64_t steps = ((a.K + bk - 1) / bk + c.parts - 1) / c.parts;
+        // an expert's last block is half full; experts of fewer rows than that have one
+        const double full = (double)a.P / (double)(used * c.rows) + 0.5;
+        const double share = (full > 1.0 ? full : 1.0) * (double)(used * ((a.N + c.weights - 1) / c.weights)) / compute_units();
+        const double step = share * c.shared[kind] > c.alone[kind] ? share * c.shared[kind] : c.alone[kind];
+        // steps' worth of filling the ring and of the results, and the start
+        const double time = (double)(steps + (tiled ? 6 : 1)) * step + (tiled ? 5.5 : 2.5);
+        if (i == 0 || time < best_time) {
+            best = i;
+            best_time = time;
+        }
+    }
+    return best;
+}
+
+template <class T, int FMT, bool ASYM, bool GATED, int CUT>
+hipError_t launch_cut(const ExpertArgs& a, hipStream_t s) {
+    constexpr Cut c = kCuts[CUT];
+    return launch_narrow<T, FMT, ASYM, GATED, c.rows, c.parts, c.weights / 32, c.bytes>(a, s);
+}
+
+template <class T, int FMT, bool ASYM, bool GATED>
 hipError_t launch_rows(const ExpertArgs& a, hipStream_t s) {
-    const int64_t rows = a.P / (a.P < a.E ? a.P : a.E);  // of an expert, on average
-    if (rows >= 48) return launch_tile<T, FMT, ASYM, GATED, 128>(a, s);
-    if (rows >= 16) return launch_tile<T, FMT, ASYM, GATED, 64>(a, s);
-    if (rows >= 3) return launch_few<T, FMT, ASYM, GATED, 16>(a, s);
-    return launch_few<T, FMT, ASYM, GATED, 4>(a, s);
+    switch (choose_cut(a)) {
+        case 0: return launch_cut<T, FMT, ASYM, GATED, 0>(a, s);
+        case 1: return launch_cut<T, FMT, ASYM, GATED, 1>(a, s);
+        case 2: return launch_cut<T, FMT, ASYM, GATED, 2>(a, s);
+        case 3: return launch_cut<T, FMT, ASYM, GATED, 3>(a, s);
+        case 4: return launch_cut<T, FMT, ASYM, GATED, 4>(a, s);
+        case 5: return launch_cut<T, FMT, ASYM, GATED, 5>(a, s);
+        case 6: return launch_cut<T, FMT, ASYM, GATED, 6>(a, s);
+        case 7: return launch_cut<T, FMT, ASYM, GATED, 7>(a, s);
+        default: return launch_tile<T, FMT, ASYM, GATED>(a, s);
+    }
 }
 
 template <class T>
