@@ -826,24 +826,24 @@ struct Cut {
 };
 
 constexpr Cut kCuts[] = {
-    {4, 128, 1, 128, {1.20f, 1.10f, 1.72f}, {0.93f, 0.86f, 1.02f}},
-    {4, 64, 2, 128, {1.25f, 1.13f, 1.52f}, {0.87f, 0.77f, 0.89f}},
-    {4, 32, 4, 128, {1.25f, 1.27f, 1.59f}, {1.03f, 0.79f, 0.85f}},
-    {16, 128, 1, 64, {0.77f, 0.68f, 1.01f}, {0.53f, 0.44f, 0.52f}},
-    {16, 64, 2, 64, {0.83f, 0.74f, 1.06f}, {0.61f, 0.47f, 0.50f}},
-    {16, 32, 4, 64, {1.00f, 0.83f, 1.20f}, {0.90f, 0.55f, 0.60f}},
-    {32, 128, 1, 64, {1.01f, 0.76f, 1.11f}, {0.74f, 0.56f, 0.66f}},
-    {64, 128, 1, 64, {1.48f, 1.00f, 1.37f}, {1.28f, 0.78f, 1.07f}},
-    {tile::BM, tile::BN, 1, 0, {0.70f, 0.98f, 1.10f}, {0.91f, 1.06f, 1.18f}},
+    {4, 128, 1, 128, {1.08f, 1.03f, 1.44f}, {0.79f, 0.78f, 0.87f}},
+    {4, 64, 2, 128, {1.18f, 1.06f, 1.35f}, {0.69f, 0.68f, 0.68f}},
+    {4, 32, 8, 64, {1.10f, 1.03f, 1.23f}, {0.76f, 0.61f, 0.67f}},
+    {16, 128, 1, 64, {0.74f, 0.64f, 1.00f}, {0.48f, 0.39f, 0.41f}},
+    {16, 64, 2, 64, {0.81f, 0.67f, 1.02f}, {0.51f, 0.38f, 0.42f}},
+    {16, 32, 4, 64, {0.94f, 0.81f, 0.90f}, {0.69f, 0.46f, 0.50f}},
+    {32, 128, 1, 64, {0.96f, 0.70f, 1.05f}, {0.66f, 0.48f, 0.59f}},
+    {64, 128, 1, 64, {1.35f, 0.93f, 1.28f}, {1.10f, 0.76f, 0.96f}},
+    {tile::BM, tile::BN, 1, 0, {0.71f, 1.02f, 1.11f}, {0.85f, 1.13f, 1.09f}},
 };
 
 // The cut of the shortest estimated time: few rows waste the rows of a large
 // block, few blocks leave compute units idle, and a long row takes one workgroup
-// many steps.  kCuts was fitted to every cut's time for 206 calls (1 to 4096
-// tokens, 1 to 96 experts, 512 to 14336 columns): the one taken here is 3 %
-// slower than the best of the nine in the mean and 26 % at worst; by rows an expert
-// alone it is 28 % and fivefold.  Without any one of them the best is 12 to 47 % slower
-// for some call.
+// many steps.  kCuts was fitted to every cut's time for 253 calls (1 to 4096
+// tokens, 1 to 120 experts, 512 to 14336 columns): the one taken here is 3 %
+// slower than the best of the nine in the mean and 38 % at worst; by rows an expert
+// alone it is 28 % and fivefold.  Without any one of them some call is 11 to 85 %
+// slower at best.
 int choose_cut(const ExpertArgs& a) {
     const int kind = a.fmt == 0 ? 0 : a.zeros ? 2 : 1;
     const int64_t used = a.P < a.E ? a.P : a.E;
@@ -859,7 +859,7 @@ int choose_cut(const ExpertArgs& a) {
         const double share = (full > 1.0 ? full : 1.0) * (double)(used * ((a.N + c.weights - 1) / c.weights)) / compute_units();
         const double step = share * c.shared[kind] > c.alone[kind] ? share * c.shared[kind] : c.alone[kind];
         // steps' worth of filling the ring and of the results, and the start
-        const double time = (double)(steps + (tiled ? 6 : 1)) * step + (tiled ? 5.5 : 2.5);
+        const double time = (double)(steps + (tiled ? 6 : 2)) * step + (tiled ? 5.5 : 2.5);
         if (i == 0 || time < best_time) {
             best = i;
             best_time = time;
