@@ -13,9 +13,14 @@
 // row by a power of two to at most 1: together they keep at least 16 bits of the
 // row's largest value, so that the adapter's update is rounded once, with the sum.
 //
+// Rows of any alignment are read and written in 16-byte vectors (the memory mode of
+// this platform allows any address), but for the last columns of a row.
+//
 // Rows, ranks and columns that are not there are read through buffer descriptors
 // at an offset past their end, which gives zeros and drops stores: no load waits
 // for a mask, and nothing branches.
+
+#include <initializer_list>
 
 #include "tq_device.h"
 #include "tq_internal.h"
@@ -112,9 +117,6 @@ __device__ __forceinline__ void update(const LoraArgs& a, int64_t t0, uint32_t c
     const int n_hi = n_lo + (int)a.cols < N ? n_lo + (int)a.cols : N;
     const int rows = a.T - t0 < kRows ? (int)(a.T - t0) : kRows;
     const bool some = l >= 0;
-    const bool vec_ok = N % 8 == 0 && ((a.base_stride | a.out_stride) & 7) == 0 &&
-                        ((reinterpret_cast<uintptr_t>(a.base) | reinterpret_cast<uintptr_t>(a.out)) & 15u) == 0;
-
     const auto from = buffer(a.base + t0 * a.base_stride, ((rows - 1) * a.base_stride + N) * 2);
     const auto to = buffer(a.out + t0 * a.out_stride, ((rows - 1) * a.out_stride + N) * 2);
     const auto bbuf = buffer(a.B + (int64_t)(some ? l : 0) * a.N * a.r, (int64_t)N * a.r * 2);
@@ -140,11 +142,9 @@ __device__ __forceinline__ void update(const LoraArgs& a, int64_t t0, uint32_t c
                     c.b[t][st] = __builtin_amdgcn_raw_buffer_load_b128(
                         bbuf, 32 * st + 8 * g < a.r ? b_row + 8u * t * a.r + 64u * st : kNowhere, n * a.r * 2, 0);
         }
-        if (vec_ok) {
 #pragma unroll
-            for (int m = 0; m < MB; ++m)
-                c.base[m] = __builtin_amdgcn_raw_buffer_load_b128(from, n + 8 * g < n_hi ? from_row[m] : kNowhere, n * 2, 0);
-        }
+        for (int m = 0; m < MB; ++m)
+            c.base[m] = __builtin_amdgcn_raw_buffer_load_b128(from, n + 8 * g + 8 <= n_hi ? from_row[m] : kNowhere, n * 2, 0);
     };
     // Step i of a wave: two in a row where there are enough columns for every wave,
     // so that a wave's stores fill the cache lines that they begin.
@@ -252,25 +252,29 @@ __device__ __forceinline__ void update(const LoraArgs& a, int64_t t0, uint32_t c
         }
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
-            if (vec_ok) {
-                u32x4 v = c.base[m];
-                if (some) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[e] = round_pair<T>(fmaf(factor[m], d[m][e / 2][2 * (e % 2)], T::to_f32((uint16_t)v[e])),
-                                             fmaf(factor[m], d[m][e / 2][2 * (e % 2) + 1], T::to_f32((uint16_t)(v[e] >> 16))));
-                }
-                __builtin_amdgcn_raw_buffer_store_b128(v, to, n + 8 * g < n_hi ? to_row[m] : kNowhere, n * 2, 0);
-            } else {
-                uint16_t v[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] = __builtin_amdgcn_raw_buffer_load_b16(from, n + 8 * g + e < n_hi ? from_row[m] + 2u * e : kNowhere, n * 2, 0);
+            u32x4 v = c.base[m];
+            // the columns of a row's end that are no whole vector, one by one
+            const bool end = n + 32 > n_hi, part = n + 8 * g + 8 > n_hi;
+            if (end) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    if (some) v[e] = round_one<T>(fmaf(factor[m], d[m][e / 4][e % 4], T::to_f32(v[e])));
-                    __builtin_amdgcn_raw_buffer_store_b16(v[e], to, n + 8 * g + e < n_hi ? to_row[m] + 2u * e : kNowhere, n * 2, 0);
+                    const uint32_t one = __builtin_amdgcn_raw_buffer_load_b16(
+                        from, part && n + 8 * g + e < n_hi ? from_row[m] + 2u * e : kNowhere, n * 2, 0);
+                    v[e / 2] |= one << (16 * (e % 2));
                 }
+            }
+            if (some) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = round_pair<T>(fmaf(factor[m], d[m][e / 2][2 * (e % 2)], T::to_f32((uint16_t)v[e])),
+                                         fmaf(factor[m], d[m][e / 2][2 * (e % 2) + 1], T::to_f32((uint16_t)(v[e] >> 16))));
+            }
+            __builtin_amdgcn_raw_buffer_store_b128(v, to, part ? kNowhere : to_row[m], n * 2, 0);
+            if (end) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v[e / 2] >> (16 * (e % 2))), to,
+                                                          part && n + 8 * g + e < n_hi ? to_row[m] + 2u * e : kNowhere, n * 2, 0);
             }
         }
     };
@@ -593,6 +597,36 @@ __global__ __launch_bounds__(Stage<RT>::W * kWave) void staged_kernel(LoraArgs a
 
 constexpr int64_t kLoraDecodeRows = 256;
 
+// Columns of a workgroup, in whole passes of its waves.  Each workgroup makes the
+// first product again and reads its columns of the second, so its time goes with
+// K + cols, and with the workgroups of a compute unit where there are more than
+// one.  How many of a block's slots have an adapter is known on the device alone:
+// the sum of the times for one and for all of them is what is made small.  (Two
+// workgroups a compute unit in any case: 64 rows of 32 adapters, 6144 x 4096, rank
+// 16, 18.7 us instead of 11.5; one in any case: 229 rows of 10 prompts, 8840 x 704,
+// 22 instead of 14.)
+int64_t chunk_columns(const LoraArgs& a, int64_t pass) {
+    const int64_t passes = (a.N + pass - 1) / pass, units = compute_units();
+    int64_t best = 0;
+    double best_time = 0;
+    for (const int64_t live : {a.blocks, a.blocks * a.slots})
+        for (int64_t fill = 1; fill <= 2; ++fill) {
+            int64_t c = fill * units / ((live + 7) / 8 * 8);
+            c = c < 1 ? 1 : c > passes ? passes : c;
+            const int64_t cols = (passes + c - 1) / c * pass;
+            double time = 0;
+            for (const int64_t l : {a.blocks, a.blocks * a.slots}) {
+                const double share = (double)((l + 7) / 8 * 8 * c) / (double)units;
+                time += (share > 1.0 ? share : 1.0) * (double)(a.K + cols);
+            }
+            if (best == 0 || time < best_time) {
+                best = cols;
+                best_time = time;
+            }
+        }
+    return best;
+}
+
 template <class T, int MB, int RT, int W>
 hipError_t launch_variant(const LoraArgs& args, hipStream_t s) {
     constexpr int lds = W * 16 * MB * Depth<MB, RT, W>::kLd * 4;
@@ -616,12 +650,8 @@ hipError_t launch_variant(const LoraArgs& args, hipStream_t s) {
             if (a.slots > a.L + 1) a.slots = a.L + 1;
             if (a.slots > a.T) a.slots = a.T;
         }
-        // columns of a workgroup: all of them where the blocks alone fill the compute
-        // units, else chunks of whole passes of the waves
-        const int64_t pass = 32 * W, passes = (a.N + pass - 1) / pass;
-        int64_t want = (2 * compute_units() + a.blocks * a.slots - 1) / (a.blocks * a.slots);
-        if (want > passes) want = passes;
-        a.cols = (passes + want - 1) / want * pass;
+        const int64_t pass = 32 * W;
+        a.cols = chunk_columns(a, pass);
         a.chunks = (a.N + a.cols - 1) / a.cols;
         const int64_t groups = (a.blocks * a.slots + 7) / 8 * 8 * a.chunks;
         lora_kernel<T, MB, RT, W><<<(unsigned)groups, W * kWave, lds, s>>>(a);
@@ -657,29 +687,25 @@ hipError_t launch_staged(const LoraArgs& args, hipStream_t s) {
     return hipSuccess;
 }
 
-// Few rows: 16 waves, so that one pass of loads covers 4096 columns.  Many: 32
-// rows, so that an adapter is read half as often, and through LDS where rows are
-// whole 16-byte vectors.
+// Rows of whole 16-byte vectors go through LDS where a block of 32 has few
+// adapters (300 rows of 3 prompts, 4096 x 4096, rank 64: 24 us instead of 42; rank
+// 16 from 2048 rows on, 1200 rows 24 and 22).  Else, for many rows, blocks of 32
+// read an adapter half as often as those of 16.  Few rows of a small rank: 16 waves,
+// so that one pass of loads covers 4096 columns.
 template <class T>
 hipError_t launch_type(const LoraArgs& a, hipStream_t s) {
-    if (a.T >= 2048) {
-        const bool vec = a.N % 8 == 0 && ((a.base_stride | a.out_stride) & 7) == 0 &&
-                         ((reinterpret_cast<uintptr_t>(a.base) | reinterpret_cast<uintptr_t>(a.out)) & 15u) == 0;
-        if (vec && a.r <= 64 && a.K >= 64) {
-            if (a.r <= 16) return launch_staged<T, 1>(a, s);
-            if (a.r <= 32) return launch_staged<T, 2>(a, s);
-            return launch_staged<T, 4>(a, s);
-        }
-        if (a.r <= 16) return launch_variant<T, 2, 1, 8>(a, s);
-        if (a.r <= 32) return launch_variant<T, 2, 2, 8>(a, s);
-        if (a.r <= 64) return launch_variant<T, 2, 4, 8>(a, s);
-        if (a.r <= 128) return launch_variant<T, 2, 8, 8>(a, s);
-        return launch_variant<T, 1, 16, 8>(a, s);
+    const bool vec = a.N % 8 == 0 && ((a.base_stride | a.out_stride) & 7) == 0 &&
+                     ((reinterpret_cast<uintptr_t>(a.base) | reinterpret_cast<uintptr_t>(a.out)) & 15u) == 0;
+    const bool many = a.T >= 2048;
+    if (vec && a.r <= 64 && a.K >= 64 && (many || (a.r > 16 && a.T > kLoraDecodeRows))) {
+        if (a.r <= 16) return launch_staged<T, 1>(a, s);
+        if (a.r <= 32) return launch_staged<T, 2>(a, s);
+        return launch_staged<T, 4>(a, s);
     }
-    if (a.r <= 16) return launch_variant<T, 1, 1, 16>(a, s);
-    if (a.r <= 32) return launch_variant<T, 1, 2, 8>(a, s);
-    if (a.r <= 64) return launch_variant<T, 1, 4, 8>(a, s);
-    if (a.r <= 128) return launch_variant<T, 1, 8, 8>(a, s);
+    if (a.r <= 16) return many ? launch_variant<T, 2, 1, 8>(a, s) : launch_variant<T, 1, 1, 16>(a, s);
+    if (a.r <= 32) return many ? launch_variant<T, 2, 2, 8>(a, s) : launch_variant<T, 1, 2, 8>(a, s);
+    if (a.r <= 64) return many ? launch_variant<T, 2, 4, 8>(a, s) : launch_variant<T, 1, 4, 8>(a, s);
+    if (a.r <= 128) return many ? launch_variant<T, 2, 8, 8>(a, s) : launch_variant<T, 1, 8, 8>(a, s);
     return launch_variant<T, 1, 16, 8>(a, s);
 }
 
