@@ -826,7 +826,7 @@ struct Cut {
 };
 
 constexpr Cut kCuts[] = {
-    {4, 128, 1, 128, {1.08f, 1.03f, 1.44f}, {0.79f, 0.78f, 0.87f}},
+    {4, 128, 1, 128, {1.08f, 0.0f, 0.0f}, {0.79f, 0.0f, 0.0f}},  // ternary alone: W4A16 is faster by the next in any case
     {4, 64, 2, 128, {1.18f, 1.06f, 1.35f}, {0.69f, 0.68f, 0.68f}},
     {4, 32, 8, 64, {1.10f, 1.03f, 1.23f}, {0.76f, 0.61f, 0.67f}},
     {16, 128, 1, 64, {0.74f, 0.64f, 1.00f}, {0.48f, 0.39f, 0.41f}},
@@ -847,9 +847,10 @@ constexpr Cut kCuts[] = {
 int choose_cut(const ExpertArgs& a) {
     const int kind = a.fmt == 0 ? 0 : a.zeros ? 2 : 1;
     const int64_t used = a.P < a.E ? a.P : a.E;
-    int best = 0;
+    const int first = a.fmt == 0 ? 0 : 1;
+    int best = first;
     double best_time = 0;
-    for (int i = 0; i < (int)(sizeof(kCuts) / sizeof(kCuts[0])); ++i) {
+    for (int i = first; i < (int)(sizeof(kCuts) / sizeof(kCuts[0])); ++i) {
         const Cut& c = kCuts[i];
         const bool tiled = c.rows == tile::BM;
         const int64_t bk = tiled ? tile::BK : c.bytes * (a.fmt == 0 ? 4 : 2);
@@ -860,7 +861,7 @@ int choose_cut(const ExpertArgs& a) {
         const double step = share * c.shared[kind] > c.alone[kind] ? share * c.shared[kind] : c.alone[kind];
         // steps' worth of filling the ring and of the results, and the start
         const double time = (double)(steps + (tiled ? 6 : 2)) * step + (tiled ? 5.5 : 2.5);
-        if (i == 0 || time < best_time) {
+        if (i == first || time < best_time) {
             best = i;
             best_time = time;
         }
@@ -876,8 +877,11 @@ hipError_t launch_cut(const ExpertArgs& a, hipStream_t s) {
 
 template <class T, int FMT, bool ASYM, bool GATED>
 hipError_t launch_rows(const ExpertArgs& a, hipStream_t s) {
-    switch (choose_cut(a)) {
-        case 0: return launch_cut<T, FMT, ASYM, GATED, 0>(a, s);
+    const int cut = choose_cut(a);
+    if constexpr (FMT == 0) {
+        if (cut == 0) return launch_cut<T, FMT, ASYM, GATED, 0>(a, s);
+    }
+    switch (cut) {
         case 1: return launch_cut<T, FMT, ASYM, GATED, 1>(a, s);
         case 2: return launch_cut<T, FMT, ASYM, GATED, 2>(a, s);
         case 3: return launch_cut<T, FMT, ASYM, GATED, 3>(a, s);

@@ -1,0 +1,205 @@
+"""The experts' operators one after another as a layer uses them, in the sizes of every cut of a call, and calls at once.
+
+Each stage of the layer is held against the fp64 formula of the values that the stage before it wrote, within the bounds
+of moe_common.py; the whole layer replayed from a graph gives the eager layer's bits.
+"""
+import numpy as np
+import pytest
+
+import oracle.experts as OE
+from gpu_common import log, require_gpu
+from moe_common import assert_within, experts, gated_bound, rounded, sum_bound, to_dev, values
+from test_gpu_23_experts import call, check
+from test_gpu_24_lora import bound_of, make as make_lora
+
+pytestmark = pytest.mark.gpu
+
+
+def uneven(experts_, rows, seed):
+    """Counts of `experts_` experts around `rows` each, with their sum experts_ * rows."""
+    if rows == 1:
+        return [1] * experts_
+    return np.random.default_rng(seed).multinomial(experts_ * rows, np.full(experts_, 1.0 / experts_)).tolist()
+
+
+# (format, experts, rows of each, N, K): few and many rows, weight rows and columns, so that a call is cut into blocks of
+# 4, 16, 32, 64 and 128 rows and its columns go to one wave, two, four and eight.
+CUTS = [("ternary", 2, 1, 17772, 832), ("ternary", 35, 1, 519, 2048), ("ternary", 3, 1, 34, 4160), ("ternary", 1, 2, 34, 192),
+        ("ternary", 6, 9, 1032, 576), ("ternary", 2, 20, 33, 1088), ("ternary", 12, 700, 33, 128), ("ternary", 24, 700, 33, 128),
+        ("ternary", 12, 700, 528, 128), ("ternary", 40, 3, 2080, 320),
+        ("w4", 35, 1, 519, 1408), ("w4", 3, 1, 34, 4224), ("w4", 1, 2, 33, 128), ("w4", 6, 9, 1032, 640), ("w4", 2, 20, 33, 512),
+        ("w4", 12, 700, 33, 128), ("w4", 5, 3200, 16, 128), ("w4", 12, 2539, 142, 768), ("w4", 40, 3, 2080, 384),
+        ("w4z", 12, 1, 2080, 512), ("w4z", 3, 1, 34, 4224), ("w4z", 8, 1, 2080, 128), ("w4z", 12, 1, 2080, 256),
+        ("w4z", 2, 20, 33, 512), ("w4z", 24, 700, 33, 128), ("w4z", 48, 400, 33, 128), ("w4z", 7, 2773, 385, 128)]
+
+
+@pytest.mark.parametrize("fmt, E, rows, N, K", CUTS)
+def test_cuts(fmt, E, rows, N, K):
+    log(f"experts {fmt} E={E} rows={rows} N={N} K={K}")
+    counts = uneven(E, rows, N)
+    check(fmt, E, N, K, counts, "bf16" if N % 2 else "f16", seed=E, bias=True)
+    check(fmt, E, N + N % 2, K, counts, "f16" if N % 2 else "bf16", seed=E + 1, fan=1, gated=True)
+
+
+def layer(x, logits, residual, up, down, k):
+    import bit_weight_only_tq_amd as tq
+    r = tq.tq_moe_route(logits, k)
+    h = call(x, up, r.offsets, rows=r.rows, gated=True)
+    y = call(h, down, r.offsets)
+    return r, h, y, tq.tq_moe_combine(y, r.places, r.weights, add=residual)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt", ["ternary", "w4", "w4z"])
+@pytest.mark.parametrize("T", [1, 13, 300])
+def test_layer(T, fmt, dt):
+    """Routing, gated up and down products, the weighted sum; token 0 of several tokens has one expert alone."""
+    import torch
+    log(f"layer T={T} {fmt} {dt}")
+    dev = require_gpu()
+    E, k, H, F = 8, 2, 256, 384
+    rng = np.random.default_rng(T)
+    up, W13 = experts("ternary" if fmt == "ternary" else "w4", E, 2 * F, H, rng, zeros=fmt == "w4z")
+    down, W2 = experts("ternary" if fmt == "ternary" else "w4", E, H, F, rng, zeros=fmt == "w4z")
+    up, down = ({n: to_dev(v, dev) for n, v in p.items()} for p in (up, down))
+    x, residual = (to_dev(rng.standard_normal((T, H)).astype(np.float32), dev, dt) for _ in range(2))
+    logits = rng.standard_normal((T, E)).astype(np.float32)
+    if T > 1:
+        logits[0, 1:] = -np.inf
+    logits = to_dev(logits, dev, dt)
+
+    r, h, y, out = layer(x, logits, residual, up, down, k)
+    torch.cuda.synchronize()
+    off, rows, places = (t.cpu().numpy() for t in (r.offsets, r.rows, r.places))
+    n = off[-1]
+    want = OE.route(values(logits), k)
+    for got, right in zip((r.experts, r.offsets, r.places), (want[0], want[2], want[4])):
+        assert np.array_equal(got.cpu().numpy(), right)
+    assert n == (2 * T if T == 1 else 2 * T - 1)
+    C, mag = OE.product(values(x), W13, off, rows)
+    assert_within(values(h)[:n], OE.gated(C[:n]), rounded(dt, gated_bound(H, C[:n], mag[:n]), OE.gated(C[:n])), "up")
+    C, mag = OE.product(values(h), W2, off)
+    assert_within(values(y)[:n], C[:n], rounded(dt, sum_bound(F, mag[:n]), C[:n]), "down")
+    w = r.weights.double().cpu().numpy()
+    C = OE.combine(values(y), places, w, values(residual))
+    mag = OE.combine(np.abs(values(y)), places, np.abs(w), np.abs(values(residual)))
+    assert_within(values(out), C, rounded(dt, (k + 1) * 2.0 ** -23 * mag, C), "combine")
+
+    # replayed: other tokens and other experts every time, a row of no expert among them
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = layer(x, logits, residual, up, down, k)
+    for step in range(4):
+        x.copy_(to_dev(rng.standard_normal((T, H)).astype(np.float32), dev, dt))
+        logits.copy_(to_dev(rng.standard_normal((T, E)).astype(np.float32), dev, dt))
+        if step == 2:
+            logits[T // 2] = -float("inf")
+        eager = layer(x, logits, residual, up, down, k)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        n = int(eager[0].offsets[-1])
+        for a, b in zip(again[0], eager[0]):
+            if a.dim() == 1 and a.numel() == T * k:  # rows: only those of an expert are told
+                a, b = a[:n], b[:n]
+            assert torch.equal(a, b)
+        assert torch.equal(again[1][:n], eager[1][:n]) and torch.equal(again[2][:n], eager[2][:n])
+        assert torch.equal(again[3], eager[3])
+        if step == 2:
+            assert torch.equal(eager[3][T // 2], residual[T // 2])
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_adapters_beside_a_packed_projection(dt):
+    """The projection's output takes the adapters' update in place, eager and from a graph."""
+    import torch
+    import bit_weight_only_tq_amd as tq
+    log(f"projection with adapters {dt}")
+    T, K, N, L, r = 21, 256, 264, 5, 16
+    (x, _, A, B, ids, scale), h = make_lora(T, K, N, L, r, dt, 4)
+    packed, W = experts("ternary", 1, N, K, np.random.default_rng(1))
+    codes, s = to_dev(packed["w"][0], x.device), to_dev(packed["scale"][0], x.device)
+
+    def run():
+        out = tq.tq_gemm(x, codes, s)
+        plain = out.clone()
+        return plain, tq.tq_lora(x, out, A, B, ids, scale=scale, out=out)
+
+    base, got = run()
+    torch.cuda.synchronize()
+    want, bound = bound_of([h[0], values(base)] + h[2:], dt, K, r)
+    assert_within(values(got), want, bound, "projection")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _, again = run()
+    for shift in (1, 5):
+        ids.copy_(torch.roll(ids, shift))
+        x.mul_(-0.5)
+        _, eager = run()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(again, eager)
+
+
+@pytest.mark.parametrize("r", [8, 16, 32, 64, 128, 256])
+@pytest.mark.parametrize("T, N", [(1, 520), (9, 1031), (64, 520), (300, 520), (300, 523), (2055, 264), (2055, 131)])
+def test_adapters_give_the_same_bits_again(T, N, r):
+    """Calls one after another and two at once: no value depends on the waves' or the workgroups' order."""
+    import torch
+    import bit_weight_only_tq_amd as tq
+    log(f"lora again T={T} N={N} r={r}")
+    (x, base, A, B, ids, scale), _ = make_lora(T, 328, N, 3, r, "f16" if r % 16 else "bf16", T + r)
+    want = tq.tq_lora(x, base, A, B, ids, scale=scale)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(4):
+        with torch.cuda.stream(side):
+            other = tq.tq_lora(x, base, A, B, ids, scale=scale)
+        again = tq.tq_lora(x, base, A, B, ids, scale=scale)
+        torch.cuda.synchronize()
+        assert torch.equal(again, want) and torch.equal(other, want)
+
+
+@pytest.mark.parametrize("K, N", [(328, 1), (64, 9), (200, 31), (328, 265), (1096, 1030)])
+@pytest.mark.parametrize("T, r", [(3, 16), (40, 64), (300, 32), (300, 64), (2100, 16), (2100, 64)])
+@pytest.mark.parametrize("shift", [0, 1, 4])
+def test_adapters_of_rows_at_any_address(T, r, K, N, shift):
+    """Rows that begin at any value and end inside a vector, in place; what lies between the rows stays as it was."""
+    import torch
+    import bit_weight_only_tq_amd as tq
+    log(f"lora T={T} r={r} K={K} N={N} shift={shift}")
+    dt = "bf16" if shift else "f16"
+    (x, base, A, B, ids, scale), h = make_lora(T, K, N, 4, r, dt, N)
+    wide = torch.full((T, N + 11), 33.0, dtype=x.dtype, device=x.device)
+    view = wide[:, shift:shift + N]
+    view.copy_(base)
+    tq.tq_lora(x, view, A, B, ids, scale=scale, out=view)
+    torch.cuda.synchronize()
+    want, bound = bound_of(h, dt, K, r)
+    assert_within(values(view), want, bound, "rows")
+    assert (wide[:, :shift] == 33.0).all() and (wide[:, shift + N:] == 33.0).all()
+
+
+def test_calls_at_once():
+    """Routing with workspaces of their own and weighted sums on two streams at once."""
+    import torch
+    import bit_weight_only_tq_amd as tq
+    log("route and combine at once")
+    dev = require_gpu()
+    gen = torch.Generator().manual_seed(3)
+    logits = [torch.randn(1500, 60, generator=gen).to(dev) for _ in range(2)]
+    y = torch.randn(6000, 136, generator=gen).to(dev, torch.bfloat16)
+    want = [tq.tq_moe_route(v, 4) for v in logits]
+    sums = [tq.tq_moe_combine(y, w.places, w.weights) for w in want]
+    streams = [torch.cuda.Stream() for _ in logits]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for v, st in zip(logits, streams):
+            with torch.cuda.stream(st):
+                r = tq.tq_moe_route(v, 4)
+                got.append((r, tq.tq_moe_combine(y, r.places, r.weights)))
+        torch.cuda.synchronize()
+        for (r, s), w, t in zip(got, want, sums):
+            assert all(torch.equal(a, b) for a, b in zip(r, w)) and torch.equal(s, t)
