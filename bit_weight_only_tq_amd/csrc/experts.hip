@@ -64,10 +64,13 @@ __device__ __forceinline__ Blocks count_blocks(const ExpertArgs& a, int BM) {
     b.total = __builtin_amdgcn_readlane(b.sum, 63);
     return b;
 }
-// Block y < total.
+// Block y < total.  Offsets that no routing writes can make more blocks than an int
+// counts: what is then no block of an expert's rows has none.
 __device__ __forceinline__ Block find_block(const ExpertArgs& a, const Blocks& b, int BM, int y) {
     const int lane = threadIdx.x & 63;
-    const int l = __builtin_ctzll(__ballot(b.sum > y));
+    const uint64_t here = __ballot(b.sum > y);
+    if (here == 0) return Block{0, 0, 0};
+    const int l = __builtin_ctzll(here);
     int left = y - __builtin_amdgcn_readlane(b.sum - b.own, l);
     // the experts of lane l, 64 at a time (one where V is 1)
     for (int v0 = 0;; v0 += 64) {
@@ -78,8 +81,10 @@ __device__ __forceinline__ Block find_block(const ExpertArgs& a, const Blocks& b
         const uint64_t past = __ballot(sum > left);
         if (past) {
             const int w = __builtin_ctzll(past);
-            const int row = __builtin_amdgcn_readlane(r.lo, w) + (left - __builtin_amdgcn_readlane(sum - n, w)) * BM;
-            const int end = __builtin_amdgcn_readlane(r.hi, w);
+            const int lo = __builtin_amdgcn_readlane(r.lo, w), end = __builtin_amdgcn_readlane(r.hi, w);
+            const uint32_t from = (uint32_t)(left - __builtin_amdgcn_readlane(sum - n, w)) * (uint32_t)BM;
+            if (from >= (uint32_t)(end - lo)) return Block{0, 0, 0};
+            const int row = lo + (int)from;
             return Block{l * b.V + v0 + w, row, end - row < BM ? end - row : BM};
         }
         left -= __builtin_amdgcn_readlane(sum, 63);

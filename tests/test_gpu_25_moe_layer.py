@@ -203,3 +203,78 @@ def test_calls_at_once():
         torch.cuda.synchronize()
         for (r, s), w, t in zip(got, want, sums):
             assert all(torch.equal(a, b) for a, b in zip(r, w)) and torch.equal(s, t)
+
+
+LARGE = [("ternary", 16, 300, 144, 640), ("ternary", 8, 700, 272, 640), ("ternary", 8, 3000, 144, 640), ("w4", 8, 300, 272, 640),
+         ("w4", 8, 700, 272, 640), ("w4", 16, 3000, 144, 640), ("w4z", 8, 700, 144, 640), ("w4z", 16, 700, 144, 640),
+         ("w4z", 8, 3000, 144, 1024)]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("fmt, E, rows, N, K", LARGE)
+def test_many_rows_scales_and_values_that_are_not_finite(fmt, E, rows, N, K, dt):
+    """Blocks of 32 to 128 rows: groups whose scale is 0 (first, last, all of a row), scales from 2^-20 to 2^9 beside each
+    other, a NaN and an infinity in a row, rows of no expert at the end; 40 rows of each expert against the formula."""
+    import torch
+    log(f"experts {fmt} {dt} E={E} rows={rows} N={N} K={K} scales")
+    dev = require_gpu()
+    rng = np.random.default_rng(K + rows)
+    packed, W = experts("ternary" if fmt == "ternary" else "w4", E, N, K, rng, zeros=fmt == "w4z")
+    old = packed["scale"].astype(np.float64)
+    scale = (2.0 ** rng.integers(-20, 10, old.shape) * (1 + rng.integers(0, 4, old.shape) / 4)).astype(np.float16)
+    scale[:, 5:20:3] = 0.0
+    if fmt != "ternary":
+        scale[:, 30:60][rng.random(scale[:, 30:60].shape) < 0.5] = 0.0
+        scale[:, 60, 0] = scale[:, 61, -1] = 0.0
+    W = (W.reshape(E, N, old[0, 0].size, -1) / old.reshape(E, N, -1, 1) * scale.astype(np.float64).reshape(E, N, -1, 1)).reshape(E, N, K)
+    packed["scale"] = scale
+    counts = uneven(E, rows, 9)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    P = int(off[-1]) + 7
+    A = to_dev(rng.standard_normal((P, K)).astype(np.float32), dev, dt)
+    bad_nan, bad_inf = int(off[1]) + 3, int(off[2]) - 2
+    A[bad_nan, 5], A[bad_inf, K - 3] = float("nan"), float("inf")
+    d = {n: to_dev(v, dev) for n, v in packed.items()}
+    picked = np.unique(np.concatenate([np.r_[lo, hi - 1, rng.integers(lo, hi, 38)] for lo, hi in zip(off[:-1], off[1:])]))
+    picked = picked[(picked != bad_nan) & (picked != bad_inf)]
+    sub = np.searchsorted(picked, off).astype(np.int32)
+    C, mag = OE.product(values(A[torch.from_numpy(picked).to(dev)]), W, sub)
+    over = {"f16": 65520.0, "bf16": 3.3961775e38}[dt]
+    for gated in (False, True):
+        out = torch.full((P, N // 2 if gated else N), 123.0, dtype=A.dtype, device=dev)
+        call(A, d, to_dev(off, dev), gated=gated, out=out)
+        torch.cuda.synchronize()
+        assert (out[-7:] == 123.0).all()
+        assert out[bad_nan].isnan().all()
+        assert gated or not out[bad_inf].isfinite().any()
+        got = values(out)[picked]
+        want, bound = (OE.gated(C), gated_bound(K, C, mag)) if gated else (C, sum_bound(K, mag))
+        fine = np.abs(want) + bound < over
+        assert_within(got[fine], want[fine], rounded(dt, bound, want)[fine], "scales")
+        past = np.abs(want) - bound >= over
+        assert np.array_equal(got[past], np.sign(want[past]) * np.inf)
+
+
+@pytest.mark.parametrize("fmt, E, rows, N, K", LARGE)
+def test_many_rows_offsets_of_any_values(fmt, E, rows, N, K):
+    """Offsets and rows that no routing writes: memory around the output stays as it was."""
+    import torch
+    log(f"experts {fmt} E={E} rows={rows} wild offsets")
+    dev = require_gpu()
+    rng = np.random.default_rng(rows)
+    packed, _ = experts("ternary" if fmt == "ternary" else "w4", E, N, K, rng, zeros=fmt == "w4z")
+    d = {n: to_dev(v, dev) for n, v in packed.items()}
+    P = E * rows
+    A = to_dev(rng.standard_normal((P // 2, K)).astype(np.float32), dev, "f16")
+    pairs = rng.permutation(P).astype(np.int32)
+    pairs[:3] = -5, 2 ** 31 - 1, P
+    pairs = to_dev(pairs, dev)
+    big = torch.full((P + 64, N), 77.0, dtype=A.dtype, device=dev)
+    sound = np.arange(E + 1, dtype=np.int64) * rows
+    for change in ({1: 2 ** 30}, {0: -5, E: P + 99}, {0: 8, 1: 0, E - 1: -1}, {1: P, 2: 0, E: P}):
+        off = sound.copy()
+        for i, v in change.items():
+            off[i] = v
+        call(A, d, to_dev(off.astype(np.int32), dev), rows=pairs, out=big[32:-32])
+        torch.cuda.synchronize()
+        assert (big[:32] == 77.0).all() and (big[-32:] == 77.0).all()
