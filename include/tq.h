@@ -593,8 +593,9 @@ size_t tq_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t top_k);
  * Offsets are held to [0, P] and rows to [0, P); where they are not what
  * tq_moe_route writes, which rows of C are written is unspecified.
  * K % 64 == 0, K and N at most 2^22, N * K at most 2^32, E <= 65536, N even if
- * gated.  A and codes are
- * 16-byte aligned.  The sums' order depends on P, E and N alone.
+ * gated.  A and codes are 16-byte aligned.  How a row's sum is cut and in which
+ * order its parts are added depends on P, E, N, K, the weights' format and the
+ * device, not on the offsets and rows: the same call gives the same bits.
  */
 tq_status tq_moe_gemm(const void* A, tq_dtype dt, int64_t T, int64_t P, int64_t E, int64_t N, int64_t K,
                       const uint8_t* codes, const uint16_t* scale_f16, const int32_t* offsets, const int32_t* rows,

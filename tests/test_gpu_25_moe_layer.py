@@ -10,7 +10,7 @@ import oracle.experts as OE
 from gpu_common import log, require_gpu
 from moe_common import assert_within, experts, gated_bound, rounded, sum_bound, to_dev, values
 from test_gpu_23_experts import call, check
-from test_gpu_24_lora import bound_of, make as make_lora
+from test_gpu_24_lora import bound_of, make as make_lora, test_combine as combine_within
 
 pytestmark = pytest.mark.gpu
 
@@ -179,6 +179,14 @@ def test_adapters_of_rows_at_any_address(T, r, K, N, shift):
     want, bound = bound_of(h, dt, K, r)
     assert_within(values(view), want, bound, "rows")
     assert (wide[:, :shift] == 33.0).all() and (wide[:, shift + N:] == 33.0).all()
+
+
+@pytest.mark.parametrize("N", list(range(2, 17)) + [1054, 4101])
+def test_weighted_sums_of_rows_of_any_length(N):
+    """Rows that end inside a vector, and so begin at any address."""
+    for dt in ("f16", "bf16"):
+        combine_within(5, 3, N, dt)
+        combine_within(2, 9, N, dt)
 
 
 def test_calls_at_once():
