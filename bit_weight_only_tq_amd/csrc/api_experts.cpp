@@ -29,6 +29,14 @@ tq_status moe_gemm(const void* A, tq_dtype dt, int64_t T, int64_t P, int64_t E, 
     if (!aligned(A, 16) || !aligned(w, 16) || !aligned(scale, 2) || !aligned(offsets, 4) || !aligned(rows, 4) ||
         !aligned(bias, 2) || !aligned(C, 2))
         return TQ_ERR_ALIGN;
+    // rows of C are written while others of A are read
+    const int64_t units = fmt == 0 ? 1 : K / 128;  // scales of a weight row
+    const Span to{C, P * (gated ? N / 2 : N) * 2};
+    const Span from[] = {{A, T * K * 2}, {w, E * N * (K / (fmt == 0 ? 4 : 2))}, {scale, E * N * units * 2},
+                         {zeros, zeros ? E * N * units : 0}, {offsets, (E + 1) * 4}, {rows, rows ? P * 4 : 0},
+                         {bias, bias ? E * N * 2 : 0}};
+    for (const Span& s : from)
+        if (to.overlaps(s)) return TQ_ERR_VALUE;
     tq::ExpertArgs a{};
     a.A = static_cast<const uint16_t*>(A);
     a.bf16 = dt == TQ_BF16 ? 1 : 0;

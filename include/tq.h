@@ -589,7 +589,8 @@ size_t tq_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t top_k);
  *            C[p] = gate / (1 + exp(-gate)) * up, C is [P][N / 2]; gate and up
  *            stay in fp32.
  *   C        (written) rounded once from fp32; rows behind offsets[E] are left
- *            as they were.
+ *            as they were.  It must not overlap anything that is read
+ *            (TQ_ERR_VALUE).
  * Offsets are held to [0, P] and rows to [0, P); where they are not what
  * tq_moe_route writes, which rows of C are written is unspecified.
  * K % 64 == 0, K and N at most 2^22, N * K at most 2^32, E <= 65536, N even if

@@ -70,6 +70,18 @@ def test_products(w4, change, want):
     assert _gemm(w4, **change) == want
 
 
+@pytest.mark.parametrize("w4", [False, True])
+def test_products_over_their_inputs(w4):
+    last = dict(A=6 * 128 * 2 - 2, w=4 * 32 * 128 // (2 if w4 else 4) - 2, scale=4 * 32 * 2 - 2, offsets=5 * 4 - 2, rows=12 * 4 - 2,
+                bias=4 * 32 * 2 - 2)
+    for name, at in last.items():
+        assert _gemm(w4, **{name: P(7), "C": V((8 << 36) + at)}) == "TQ_ERR_VALUE", name
+    first = V((8 << 36) - 12 * 32 * 2 + 2)
+    assert _gemm(w4, A=P(7), C=first) == "TQ_ERR_VALUE" and _gemm(w4, rows=P(7), C=first) == "TQ_ERR_VALUE"
+    if w4:
+        assert _gemm(True, zeros=P(7), C=V((8 << 36) + 4 * 32 - 2)) == "TQ_ERR_VALUE"
+
+
 def test_products_nothing_to_do():
     assert _gemm(T=0, P=0) == "TQ_OK" and _gemm(True, T=0, P=0, rows=None, A=None, C=None) == "TQ_OK"
     assert _gemm(True, group=64) == "TQ_ERR_GROUP" and _gemm(True, K=192) == "TQ_ERR_SHAPE"
