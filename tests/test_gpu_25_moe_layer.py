@@ -286,3 +286,66 @@ def test_many_rows_offsets_of_any_values(fmt, E, rows, N, K):
         call(A, d, to_dev(off.astype(np.int32), dev), rows=pairs, out=big[32:-32])
         torch.cuda.synchronize()
         assert (big[:32] == 77.0).all() and (big[-32:] == 77.0).all()
+
+
+# --------------------------------------------------- offsets past 32 bits
+
+def test_experts_past_four_gigabytes():
+    """72 experts of 64 MB: the last ones' codes, scales and zero points lie past 2^32 bytes."""
+    import torch
+    log("experts past 2^32 bytes")
+    dev = require_gpu()
+    E, N, K = 72, 8192, 16384
+    gen = torch.Generator(device=dev).manual_seed(5)
+    q = torch.randint(-2 ** 31, 2 ** 31 - 1, (E, N, K // 8), generator=gen, device=dev, dtype=torch.int32)
+    scale = (torch.rand((E, N, K // 128), generator=gen, device=dev) * 0.01 + 0.001).half()
+    zeros = torch.randint(0, 16, (E, N, K // 128), generator=gen, device=dev, dtype=torch.uint8)
+    for counts in ({0: 2, 70: 1, 71: 3}, {3: 20, 71: 60}):
+        off = np.zeros(E + 1, np.int32)
+        for e, c in counts.items():
+            off[e + 1:] += c
+        A = torch.randn((int(off[-1]), K), generator=gen, device=dev).half()
+        got = values(call(A, {"w": q, "scale": scale, "zeros": zeros}, to_dev(off, dev)))
+        torch.cuda.synchronize()
+        picked = np.r_[0:8, 4000:4040, N - 8:N]
+        for e in counts:
+            words = q[e, picked].cpu().numpy().view(np.uint32)
+            W = ((words[..., None] >> (4 * np.arange(8, dtype=np.uint32))) & 15).reshape(len(picked), K // 128, 128).astype(np.float64)
+            W = (W - zeros[e, picked].cpu().numpy()[..., None]) * scale[e, picked].double().cpu().numpy()[..., None]
+            a = values(A[off[e]:off[e + 1]])
+            want, mag = a @ W.reshape(len(picked), K).T, np.abs(a) @ np.abs(W).reshape(len(picked), K).T
+            assert_within(got[off[e]:off[e + 1]][:, picked], want, rounded("f16", sum_bound(K, mag), want), f"expert {e}")
+
+
+def test_rows_past_four_gigabytes():
+    """Rows of the weighted sum and of the adapters that lie past 2^32 bytes."""
+    import torch
+    import bit_weight_only_tq_amd as tq
+    log("rows past 2^32 bytes")
+    dev = require_gpu()
+    P, N = 560000, 4096
+    y = torch.zeros((P, N), dtype=torch.bfloat16, device=dev)
+    rows = torch.randn((4, N), generator=torch.Generator(device=dev).manual_seed(1), device=dev).bfloat16()
+    for i, p in enumerate((0, 524288, P - 2, P - 1)):
+        y[p] = rows[i]
+    places = torch.tensor([[0, P - 1], [524288, P - 2]], dtype=torch.int32, device=dev)
+    weights = torch.tensor([[0.5, 1.5], [-1.0, 0.25]], device=dev)
+    got = values(tq.tq_moe_combine(y, places, weights))
+    r, w = values(rows), values(weights)
+    want = np.stack([w[0, 0] * r[0] + w[0, 1] * r[3], w[1, 0] * r[1] + w[1, 1] * r[2]])
+    mag = np.stack([np.abs(w[0, 0] * r[0]) + np.abs(w[0, 1] * r[3]), np.abs(w[1, 0] * r[1]) + np.abs(w[1, 1] * r[2])])
+    assert_within(got, want, rounded("bf16", 3 * 2.0 ** -23 * mag, want), "sum")
+    del y
+
+    # 9000 rows of 64 columns, 2^18 values from one to the next
+    T, K, N, r = 9000, 64, 72, 16
+    (x, base, A, B, _, scale), h = make_lora(T, K, N, 2, r, "f16", 3, ids=np.arange(T) // 4500)
+    ids = to_dev(h[4], dev)
+    far_x = torch.empty((T, 1 << 18), dtype=torch.float16, device=dev)[:, :K]
+    far_out = torch.empty((T, 1 << 18), dtype=torch.float16, device=dev)[:, 8:8 + N]
+    far_x.copy_(x)
+    far_out.copy_(base)
+    tq.tq_lora(far_x, far_out, A, B, ids, scale=scale, out=far_out)
+    torch.cuda.synchronize()
+    want, bound = bound_of(h, "f16", K, r)
+    assert_within(values(far_out), want, bound, "rows")
