@@ -8,10 +8,14 @@
 // out, so one launch serves any mixture, prompts of one adapter as well as
 // decoding rows of many, without sorting.
 //
-// The first product's sums are fp32.  They enter the second one as two 16-bit
-// numbers each, the rounded value and the rounded rest, after a scaling of the
-// row by a power of two to at most 1: together they keep at least 16 bits of the
-// row's largest value, so that the adapter's update is rounded once, with the sum.
+// The first product's sums are fp32.  They enter the second one whole, as three
+// 16-bit numbers each after a scaling of the row by a power of two: the rounded
+// value, the rounded rest and the rest of that.  Each takes as many bits of the
+// sum's 24 as the type has (8 of bf16, 11 of fp16), so nothing is left but, in fp16,
+// what lies 2^-39 below the row's largest sum: its third number is a multiple of
+// 2^-24, of sums scaled to 2^15.  (Two numbers keep 16 bits in bf16 and are 1 to 3 %
+// faster, 75 instead of 77 us for 8191 rows of rank 64, but one output in 600 is then
+// not what the fp32 sum rounds to.)
 //
 // What bounds it: a decoding row's call two trips to memory (ids, then all else): 8.5
 // us for one row of rank 16, 4096 x 4096; 64 rows of 32 adapters, 6144 x 4096, the
@@ -49,17 +53,20 @@ struct Depth {
     static constexpr int S = RT <= 8 ? 2 : 1;
     static constexpr int D = RT == 1 ? (MB == 1 ? 4 : 3) : RT == 2 ? 3 : RT == 4 ? (MB == 1 ? 3 : 2) : 1;
     static constexpr int kAhead = RT <= 2 ? (W == 16 ? 2 : 4) : RT == 4 ? 2 : 1;
-    static constexpr bool kEarly = RT <= 8;  // the first columns of B and base are asked for before x
+    // the first columns of B and base are asked for before x, as far as registers go
+    static constexpr bool kEarly = MB * RT < 16;
     static constexpr int kLd = 16 * RT + 4;  // words of a row of sums in LDS
 };
 
 // Rows of sums [16 MB][kLd] in LDS as operands of the second product: lane
-// 16 g + i has row i, ranks 32 s + 8 g .. + 7, as the rounded value and the rounded
-// rest of the sum times 2^-e, and `scale` 2^e.
+// 16 g + i has row i, ranks 32 s + 8 g .. + 7, as three numbers whose sum is the sum
+// times 2^-e, and `scale` 2^e.
+constexpr int kParts = 3;
 template <class T, int MB, int RT>
-__device__ __forceinline__ void split_sums16(const float* lds, int ld, float scale, u32x4 (&hi)[MB][(RT + 1) / 2],
-                                             u32x4 (&lo)[MB][(RT + 1) / 2], float (&factor)[MB]) {
+__device__ __forceinline__ void split_sums16(const float* lds, int ld, float scale, u32x4 (&h16)[kParts][MB][(RT + 1) / 2],
+                                             float (&factor)[MB]) {
     constexpr int kKs = (RT + 1) / 2;
+    constexpr int kTop = std::is_same<T, F16>::value ? 15 : 0;  // the row's largest sum becomes 2^kTop at most
     const int g = (threadIdx.x & 63) >> 4, i16 = threadIdx.x & 15;
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
@@ -82,18 +89,21 @@ __device__ __forceinline__ void split_sums16(const float* lds, int ld, float sca
             }
         most = fmaxf(most, __shfl_xor(most, 16, kWave));
         most = fmaxf(most, __shfl_xor(most, 32, kWave));
-        int ex = most > 0.0f ? __builtin_amdgcn_frexp_expf(most) : 0;  // most = f 2^ex, 1/2 <= f < 1
-        ex = ex < -100 ? -100 : ex > 120 ? 120 : ex;                   // 2^ex is a normal number
+        int ex = most > 0.0f ? __builtin_amdgcn_frexp_expf(most) - kTop : 0;  // most = f 2^(ex + kTop), 1/2 <= f < 1
+        ex = ex < -100 ? -100 : ex > 120 ? 120 : ex;                          // 2^ex is a normal number
         factor[m] = ldexpf(scale, ex);
 #pragma unroll
         for (int s = 0; s < kKs; ++s)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float v0 = ldexpf(h[s][e / 2][2 * (e % 2)], -ex), v1 = ldexpf(h[s][e / 2][2 * (e % 2) + 1], -ex);
-                const uint32_t top = round_pair<T>(v0, v1);
-                const float r0 = v0 - T::to_f32((uint16_t)top), r1 = v1 - T::to_f32((uint16_t)(top >> 16));
-                hi[m][s][e] = top;
-                lo[m][s][e] = round_pair<T>(fabsf(v0) < __builtin_inff() ? r0 : 0.0f, fabsf(v1) < __builtin_inff() ? r1 : 0.0f);
+                float v0 = ldexpf(h[s][e / 2][2 * (e % 2)], -ex), v1 = ldexpf(h[s][e / 2][2 * (e % 2) + 1], -ex);
+#pragma unroll
+                for (int p = 0; p < kParts; ++p) {
+                    const uint32_t part = round_pair<T>(v0, v1);
+                    h16[p][m][s][e] = part;
+                    v0 = fabsf(v0) < __builtin_inff() ? v0 - T::to_f32((uint16_t)part) : 0.0f;
+                    v1 = fabsf(v1) < __builtin_inff() ? v1 - T::to_f32((uint16_t)(part >> 16)) : 0.0f;
+                }
             }
     }
 }
@@ -157,7 +167,7 @@ __device__ __forceinline__ void update(const LoraArgs& a, int64_t t0, uint32_t c
     Cols cols[kAhead];
     if constexpr (Q::kEarly) load_cols(at(0), cols[0]);
 
-    u32x4 hi[MB][kKs], lo[MB][kKs];  // operands of the second product: lane 16 g + i, row i, ranks 32 s + 8 g ..
+    u32x4 h16[kParts][MB][kKs];  // operands of the second product: lane 16 g + i, row i, ranks 32 s + 8 g ..
     float factor[MB];
     if (some) {
         const float* scale_at = a.scale ? a.scale + l : nullptr;
@@ -234,7 +244,7 @@ __device__ __forceinline__ void update(const LoraArgs& a, int64_t t0, uint32_t c
             *p = v;
         }
         __syncthreads();
-        split_sums16<T, MB, RT>(smem_lora, kLd, scale, hi, lo, factor);
+        split_sums16<T, MB, RT>(smem_lora, kLd, scale, h16, factor);
     }
 
     auto finish = [&](int n, const Cols& c) {
@@ -248,10 +258,9 @@ __device__ __forceinline__ void update(const LoraArgs& a, int64_t t0, uint32_t c
                 for (int st = 0; st < kKs; ++st) {
                     const vec bv = __builtin_bit_cast(vec, c.b[t][st]);
 #pragma unroll
-                    for (int m = 0; m < MB; ++m) {
-                        d[m][t] = Mfma<T>::mma(bv, __builtin_bit_cast(vec, hi[m][st]), d[m][t]);
-                        d[m][t] = Mfma<T>::mma(bv, __builtin_bit_cast(vec, lo[m][st]), d[m][t]);
-                    }
+                    for (int m = 0; m < MB; ++m)
+#pragma unroll
+                        for (int p = 0; p < kParts; ++p) d[m][t] = Mfma<T>::mma(bv, __builtin_bit_cast(vec, h16[p][m][st]), d[m][t]);
                 }
         }
 #pragma unroll
@@ -373,7 +382,7 @@ __device__ __forceinline__ void update_staged(const LoraArgs& a, int64_t t0, uin
     uint8_t* const ring = lds + wave * (S * Q::kBytes);
     const uint32_t ring_at = lds_base + (uint32_t)(wave * (S * Q::kBytes));
 
-    u32x4 hi[2][kKs], lo[2][kKs];  // operands of the second product: lane 16 g + i, row i, ranks 32 s + 8 g ..
+    u32x4 h16[kParts][2][kKs];  // operands of the second product: lane 16 g + i, row i, ranks 32 s + 8 g ..
     float factor[2];
     if (some) {
         f32x4 acc[2][RT];
@@ -472,7 +481,7 @@ __device__ __forceinline__ void update_staged(const LoraArgs& a, int64_t t0, uin
         }
         __syncthreads();
         const float scale = a.scale ? a.scale[l] : 1.0f;
-        split_sums16<T, 2, RT>(smem_lora, kLd, scale, hi, lo, factor);
+        split_sums16<T, 2, RT>(smem_lora, kLd, scale, h16, factor);
         __syncthreads();  // the sums have been read: the rings again
     }
 
@@ -551,10 +560,10 @@ __device__ __forceinline__ void update_staged(const LoraArgs& a, int64_t t0, uin
                         const uint32_t keep = j < r ? ~0u : 0u;
                         b &= keep;
 #pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            d[m][t] = Mfma<T>::mma(__builtin_bit_cast(vec, b), __builtin_bit_cast(vec, hi[m][st]), d[m][t]);
-                            d[m][t] = Mfma<T>::mma(__builtin_bit_cast(vec, b), __builtin_bit_cast(vec, lo[m][st]), d[m][t]);
-                        }
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int p = 0; p < kParts; ++p)
+                                d[m][t] = Mfma<T>::mma(__builtin_bit_cast(vec, b), __builtin_bit_cast(vec, h16[p][m][st]), d[m][t]);
                     }
                 }
 #pragma unroll

@@ -640,7 +640,7 @@ tq_status tq_moe_combine(const void* y, tq_dtype dt, int64_t T, int64_t P, int64
  *            adapter.  It may be `base` itself (rows without an adapter are then
  *            left alone) and must not overlap anything else (TQ_ERR_VALUE).
  * Sums are fp32, and the result is rounded once: x A^T enters the second product
- * with at least 16 bits of the row's largest value.
+ * with all bits of its sums (in fp16, to 2^-39 of the row's largest one).
  * rank % 8 == 0, rank <= 256; K % 8 == 0; K, N <= 2^22, rank * K and rank * N
  * <= 2^29; T <= 2^27; strides <= 2^25 (TQ_ERR_VALUE; not looked at for one row).
  * x, A and B are 16-byte aligned and x_stride is a multiple of 8.
