@@ -32,6 +32,7 @@
 
 #include "tq_device.h"
 #include "tq_internal.h"
+#include "tq_lora_index.h"
 #include "tq_tiles.h"
 
 namespace tq {
@@ -40,8 +41,7 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// A buffer of fewer than 2^31 bytes, and an offset that lies past any of them.
-constexpr uint32_t kNowhere = 0x80000000u;
+// A buffer of fewer than 2^31 bytes (kNowhere lies past any of them).
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* p, int64_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
 }
@@ -141,9 +141,7 @@ __device__ __forceinline__ void update(const LoraArgs& a, int64_t t0, uint32_t c
         from_row[m] = live ? (uint32_t)((16 * m + i16) * a.base_stride + 8 * g) * 2u : kNowhere;
         to_row[m] = live ? (uint32_t)((16 * m + i16) * a.out_stride + 8 * g) * 2u : kNowhere;
     }
-    // Output columns n .. n + 31: matrix row 4 g' + e of tile c is column
-    // n + 8 g' + 4 c + e, so that a lane ends with 8 columns in a row of one row.
-    const uint32_t b_row = (uint32_t)((8 * (i16 >> 2) + (i16 & 3)) * a.r + 8 * g) * 2u;
+    // Output columns n .. n + 31
     struct Cols {
         u32x4 b[2][kKs], base[MB];
     };
@@ -153,19 +151,15 @@ __device__ __forceinline__ void update(const LoraArgs& a, int64_t t0, uint32_t c
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int st = 0; st < kKs; ++st)
-                    c.b[t][st] = __builtin_amdgcn_raw_buffer_load_b128(
-                        bbuf, 32 * st + 8 * g < a.r ? b_row + 8u * t * a.r + 64u * st : kNowhere, n * a.r * 2, 0);
+                    c.b[t][st] = __builtin_amdgcn_raw_buffer_load_b128(bbuf, lora_b_offset(n, a.r, i16, g, t, st), 0, 0);
         }
 #pragma unroll
         for (int m = 0; m < MB; ++m)
             c.base[m] = __builtin_amdgcn_raw_buffer_load_b128(from, n + 8 * g + 8 <= n_hi ? from_row[m] : kNowhere, n * 2, 0);
     };
-    // Step i of a wave: two in a row where there are enough columns for every wave,
-    // so that a wave's stores fill the cache lines that they begin.
-    const bool pairs = a.cols >= 64 * W;
-    auto at = [&](int i) { return n_lo + (pairs ? 64 * wave + 32 * (i & 1) + (i >> 1) * (64 * W) : 32 * wave + i * (32 * W)); };
+    auto at = [&](int i) { return lora_step(n_lo, (int)a.cols, W, wave, i); };
     Cols cols[kAhead];
-    if constexpr (Q::kEarly) load_cols(at(0), cols[0]);
+    if (Q::kEarly && at(0) < n_hi) load_cols(at(0), cols[0]);
 
     u32x4 h16[kParts][MB][kKs];  // operands of the second product: lane 16 g + i, row i, ranks 32 s + 8 g ..
     float factor[MB];
