@@ -229,13 +229,15 @@ __device__ __forceinline__ void update(const LoraArgs& a, int64_t t0, uint32_t c
 #pragma unroll
                 for (int e = 0; e < 4; ++e) smem_lora[(wave * kRows + 16 * m + 4 * g + e) * kLd + 16 * r + i16] = acc[m][r][e];
         __syncthreads();
-        // the waves' sums, in their order
+        // the waves' sums, in their order; ranks past r count as 0 (an infinite x has
+        // NaN there, times the zeros of A)
         for (int i = threadIdx.x; i < kRows * 4 * RT; i += kThreads) {
-            f32x4* p = reinterpret_cast<f32x4*>(smem_lora + (i / (4 * RT)) * kLd + 4 * (i % (4 * RT)));
+            const int j = 4 * (i % (4 * RT));
+            f32x4* p = reinterpret_cast<f32x4*>(smem_lora + (i / (4 * RT)) * kLd + j);
             f32x4 v = *p;
 #pragma unroll
             for (int w = 1; w < W; ++w) v += p[w * kRows * kLd / 4];
-            *p = v;
+            *p = j < a.r ? v : f32x4{0.f, 0.f, 0.f, 0.f};  // r is a multiple of 8
         }
         __syncthreads();
         split_sums16<T, MB, RT>(smem_lora, kLd, scale, h16, factor);
