@@ -108,6 +108,32 @@ __device__ __forceinline__ void split_sums16(const float* lds, int ld, float sca
     }
 }
 
+// The second product may be NaN because an infinite B met a sum's rest, which is 0 or
+// of the other sign: there the product of the sums' first numbers alone, first(m, t),
+// decides.  The test is an instruction for two values; what follows it is run by
+// waves with a NaN only.
+template <int MB>
+__device__ __forceinline__ bool any_nan(const f32x4 (&d)[MB][2]) {
+    bool odd = false;
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            odd |= (bool)__builtin_isunordered(d[m][t][0], d[m][t][1]) | (bool)__builtin_isunordered(d[m][t][2], d[m][t][3]);
+    return odd;
+}
+template <int MB, class First>
+__device__ __forceinline__ void take_first(f32x4 (&d)[MB][2], First first) {
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const f32x4 f = first(m, t);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[m][t][e] = d[m][t][e] != d[m][t][e] ? f[e] : d[m][t][e];
+        }
+}
+
 // The rows `mine` of the block at t0, all of adapter l (-1: none), and the columns
 // of the chunk.  W waves deal the columns of x in steps of 32 S (whole cache lines
 // of a row), then those of the output in steps of 32.  Both loops have the next
@@ -258,6 +284,14 @@ __device__ __forceinline__ void update(const LoraArgs& a, int64_t t0, uint32_t c
 #pragma unroll
                         for (int p = 0; p < kParts; ++p) d[m][t] = Mfma<T>::mma(bv, __builtin_bit_cast(vec, h16[p][m][st]), d[m][t]);
                 }
+            if (__builtin_expect(__ballot(any_nan<MB>(d)) != 0, 0))
+                take_first<MB>(d, [&](int m, int t) {
+                    f32x4 f = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int st = 0; st < kKs; ++st)
+                        f = Mfma<T>::mma(__builtin_bit_cast(vec, c.b[t][st]), __builtin_bit_cast(vec, h16[0][m][st]), f);
+                    return f;
+                });
         }
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
@@ -498,13 +532,16 @@ __device__ __forceinline__ void update_staged(const LoraArgs& a, int64_t t0, uin
     }
     auto row_swizzle = [&](int n) { return ((n >> 1) & 1) | (((n >> 3) & 3) << 1); };
     const uint32_t b_end = (uint32_t)N * (uint32_t)r * 2u - 16u;
-    auto issue = [&](int n, int stage) {
-        const uint32_t to = ring_at + (uint32_t)(stage * Q::kBytes);
+    auto issue_base = [&](int n, uint32_t to) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int col = n + base_col[u] < N ? n + base_col[u] : N - 8;
             dma16s(base, base_off[u] + 2u * col, to + 1024u * u);
         }
+    };
+    auto issue = [&](int n, int stage) {
+        const uint32_t to = ring_at + (uint32_t)(stage * Q::kBytes);
+        issue_base(n, to);
 #pragma unroll
         for (int u = 0; u < 2 * RT; ++u)
             if (u < b_count) {
@@ -512,6 +549,16 @@ __device__ __forceinline__ void update_staged(const LoraArgs& a, int64_t t0, uin
                 if (r == 64) off ^= 16u * row_swizzle(8 * u + (lane >> 3));
                 dma16s(B, off < b_end ? off : b_end, to + 4096u + 1024u * u);
             }
+    };
+    // ranks 32 st + 8 g .. of the row of tile t and a half of the columns; past r: zeros
+    auto read_b = [&](const uint8_t* p, int half, int t, int st) {
+        const int row = 32 * half + 8 * (i16 >> 2) + 4 * t + (i16 & 3), j = 32 * st + 8 * g;
+        uint32_t off = (uint32_t)row * r * 2u + (j < r ? 2u * j : 0u);
+        if (r == 64) off ^= 16u * row_swizzle(row);
+        u32x4 b = *reinterpret_cast<const u32x4*>(p + 4096 + off);
+        const uint32_t keep = j < r ? ~0u : 0u;
+        b &= keep;
+        return b;
     };
     auto at = [&](int i) { return n_lo + 64 * (wave + W * i); };
     int own = 0;
@@ -536,44 +583,56 @@ __device__ __forceinline__ void update_staged(const LoraArgs& a, int64_t t0, uin
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         }
         uint8_t* p = ring + stage * Q::kBytes;
+        const uint32_t p_at = ring_at + (uint32_t)(stage * Q::kBytes);
         stage = stage == S - 1 ? 0 : stage + 1;
         const int n = at(i);
-        if (some) {
+        // 32 columns of the sum, in base's place; -> whether there is a NaN before base
+        auto add_half = [&](auto mend, int half) {
+            f32x4 d[2][2];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                f32x4 d[2][2];
+            for (int m = 0; m < 2; ++m) d[m][0] = d[m][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int m = 0; m < 2; ++m) d[m][0] = d[m][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const int row = 32 * half + 8 * (i16 >> 2) + 4 * t + (i16 & 3);
+                for (int st = 0; st < kKs; ++st) {
+                    const u32x4 b = read_b(p, half, t, st);
 #pragma unroll
-                    for (int st = 0; st < kKs; ++st) {
-                        const int j = 32 * st + 8 * g;
-                        uint32_t off = (uint32_t)row * r * 2u + (j < r ? 2u * j : 0u);
-                        if (r == 64) off ^= 16u * row_swizzle(row);
-                        u32x4 b = *reinterpret_cast<const u32x4*>(p + 4096 + off);
-                        const uint32_t keep = j < r ? ~0u : 0u;
-                        b &= keep;
+                    for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int m = 0; m < 2; ++m)
-#pragma unroll
-                            for (int p = 0; p < kParts; ++p)
-                                d[m][t] = Mfma<T>::mma(__builtin_bit_cast(vec, b), __builtin_bit_cast(vec, h16[p][m][st]), d[m][t]);
-                    }
+                        for (int q = 0; q < kParts; ++q)
+                            d[m][t] = Mfma<T>::mma(__builtin_bit_cast(vec, b), __builtin_bit_cast(vec, h16[q][m][st]), d[m][t]);
                 }
+            const bool odd = any_nan<2>(d);
+            if constexpr (decltype(mend)::value)
+                take_first<2>(d, [&](int m, int t) {
+                    f32x4 f = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    u32x4* q = reinterpret_cast<u32x4*>(p + (16 * m + i16) * 128 + 16 * ((4 * half + g) ^ line_swizzle(i16)));
-                    u32x4 v = *q;
+                    for (int st = 0; st < kKs; ++st)
+                        f = Mfma<T>::mma(__builtin_bit_cast(vec, read_b(p, half, t, st)), __builtin_bit_cast(vec, h16[0][m][st]), f);
+                    return f;
+                });
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[e] = round_pair<T>(fmaf(factor[m], d[m][e / 2][2 * (e % 2)], T::to_f32((uint16_t)v[e])),
-                                             fmaf(factor[m], d[m][e / 2][2 * (e % 2) + 1], T::to_f32((uint16_t)(v[e] >> 16))));
-                    *q = v;
-                }
+            for (int m = 0; m < 2; ++m) {
+                u32x4* q = reinterpret_cast<u32x4*>(p + (16 * m + i16) * 128 + 16 * ((4 * half + g) ^ line_swizzle(i16)));
+                u32x4 v = *q;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = round_pair<T>(fmaf(factor[m], d[m][e / 2][2 * (e % 2)], T::to_f32((uint16_t)v[e])),
+                                         fmaf(factor[m], d[m][e / 2][2 * (e % 2) + 1], T::to_f32((uint16_t)(v[e] >> 16))));
+                *q = v;
             }
+            return odd;
+        };
+        if (some) {
+            const bool odd0 = add_half(std::false_type{}, 0), odd1 = add_half(std::false_type{}, 1);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            if (__builtin_expect(__ballot(odd0 || odd1) != 0, 0)) {  // once more, from base as it was
+                issue_base(n, p_at);
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                add_half(std::true_type{}, 0);
+                add_half(std::true_type{}, 1);
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            }
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {

@@ -1,4 +1,4 @@
-"""Rows of infinite activations in tq_lora: with A of one sign and each row of B of one sign, the result is +inf or -inf.
+"""Infinite activations and weights in tq_lora: with A of one sign and each row of B of one sign, the result is +inf or -inf.
 
 Ranks that fill the matrix tiles and ranks that do not must agree, and so must few rows and prompts: no rank that is not
 there may bring a NaN into the sums.
@@ -54,3 +54,32 @@ def test_infinite_activations(T, N, r, dt):
         h = [h[0][keep], h[1][keep], h[2], h[3], ids[keep], h[5]]
         want, bound = bound_of(h, dt, K, r)
         assert_within(values(got)[keep], want, bound, "rows beside them")
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T, N", [(1, 40), (40, 41), (300, 72), (2100, 72), (2100, 41)])
+@pytest.mark.parametrize("r", [8, 16, 24, 64, 104, 256])
+def test_infinite_weights(T, N, r, dt):
+    """Infinities in columns of B, and in a rank of one adapter's A, reach their columns and rows and no others."""
+    import torch
+    import bit_weight_only_tq_amd as tq
+    log(f"lora infinite weights T={T} N={N} r={r} {dt}")
+    K = 136
+    (x, base, A, B), ids, scale = signed(T, K, N, 3, r, dt, T + N + r)
+    x = x.abs() + 0.125
+    ids[0] = 0
+    for n, j in ((0, 0), (5, r - 1), (N - 1, 3)):
+        B[:2, n, j] = torch.sign(B[:2, n, j]) * float("inf")
+    A[1, 4, 9] = float("inf")
+    dev = x.device
+    got = tq.tq_lora(x, base, A, B, to_dev(ids, dev), scale=to_dev(scale, dev))
+    torch.cuda.synchronize()
+    h = [values(x), values(base), values(A), values(B), ids, scale.astype(np.float64)]
+    want = OE.lora(*h)[0]
+    assert np.isinf(want[ids == 0][:, [0, 5, N - 1]]).all() and np.isinf(want[ids == 1]).all() and np.isfinite(want[ids == 2]).all()
+    assert np.isfinite(np.delete(want[ids == 0], [0, 5, N - 1], 1)).all()
+    wide = np.isinf(want)
+    assert np.array_equal(values(got)[wide], want[wide])
+    h[2], h[3] = (np.where(np.isinf(v), 0.0, v) for v in h[2:4])  # finite results take no infinite value
+    rest, bound = bound_of(h, dt, K, r)
+    assert_within(values(got)[~wide], rest[~wide], bound[~wide], "the others")
