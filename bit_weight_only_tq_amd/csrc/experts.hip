@@ -103,8 +103,8 @@ __device__ __forceinline__ int64_t source_row(const ExpertArgs& a, int64_t p) {
 
 __device__ __forceinline__ float gate(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
-// Eight columns of a code word as exact operands.  fp16: q - z (add: the packed
-// constants of z).  bf16: (q - z) / 16, two nibbles' signed values by the
+// Eight columns of a code word as exact operands, for every z of 0 to 255.  fp16: q -
+// z (add: -(1024 + z) and -(64 + z), whole numbers below 2^11).  bf16: (q - z) / 16, two nibbles' signed values by the
 // converter of offset 4-bit numbers, (n ^ 8) / 16 - 1/2; `add` is (8 - z) / 16.
 // keep is 0 where the group's scale is 0 (all ones elsewhere): its words then
 // become those of zero weights.
@@ -117,7 +117,10 @@ struct W4Unpack<F16, ASYM> {
     f16x2 add = w4_nat_sub(8u);
     __device__ __forceinline__ void set(uint32_t z, bool zero) {
         keep = zero ? 0u : ~0u;
-        if constexpr (ASYM) add = w4_nat_sub(zero ? 0u : z);
+        if constexpr (ASYM) {
+            const _Float16 v = (_Float16)(uint16_t)(zero ? 0u : z);
+            add = f16x2{(_Float16)-1024.0f, (_Float16)-64.0f} - f16x2{v, v};
+        }
     }
     __device__ __forceinline__ uint4 quad(uint32_t x, uint32_t mask_v, uint32_t magic_v) const {
         const uint32_t y = ASYM ? x & keep : (x & keep) | (0x88888888u & ~keep);

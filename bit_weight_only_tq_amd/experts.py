@@ -63,7 +63,7 @@ def tq_moe_gemm(A, codes, scale, offsets, rows=None, bias=None, gated: bool = Fa
 def w4a16_moe_gemm(A, qweight, scales, offsets, rows=None, zeros=None, bias=None, group_size: int = 128,
                    gated: bool = False, out=None):
     """tq_moe_gemm with W4A16 experts: qweight int32 [E, N, K / 8], scales fp16 [E, N, K / 128], zeros uint8
-    [E, N, K / 128] or None for 8."""
+    [E, N, K / 128] (any values) or None for 8."""
     if group_size != 128:
         _lib._check("w4a16_moe_gemm", 5)  # TQ_ERR_GROUP
     return _result("w4a16_moe_gemm", _entry().moe_gemm(A, qweight, scales, zeros, offsets, rows, bias, gated, out))

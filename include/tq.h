@@ -604,7 +604,8 @@ tq_status tq_moe_gemm(const void* A, tq_dtype dt, int64_t T, int64_t P, int64_t 
 
 /*
  * w4a16_moe_gemm - the same with W4A16 experts: qweight [E][N][K / 8], scales_f16
- * and zeros [E][N][K / 128] (zeros may be NULL: 8).  K % 128 == 0.  Sums may be
+ * and zeros [E][N][K / 128] (zeros may be NULL: 8; any value of 8 bits: a weight
+ * is (q - zero) * scale).  K % 128 == 0.  Sums may be
  * held in units of a group's scale on the way, so bf16 activations of 2^60 and
  * more can overflow between groups whose scales differ by 2^40.
  */
