@@ -530,10 +530,10 @@ PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// (A, codes or qweight, scale, zeros, offsets, rows, bias, gated, out)
+// (A, codes or qweight, scale, zeros, offsets, rows, bias, gated, out, whether they are W4A16's)
 PyObject* moe_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    count(n, 9);
+    count(n, 10);
     const Tensor &A = tensor("A", a[0]), &w = tensor("weights", a[1]), &scale = tensor("scale", a[2]),
                  &offsets = tensor("offsets", a[4]);
     const Tensor *zeros = optional("zeros", a[3]), *rows = optional("rows", a[5]), *bias = optional("bias", a[6]),
@@ -544,18 +544,16 @@ PyObject* moe_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const tq_dtype dt = half_type("A", A);
     contiguous("A", A);
     const int64_t T = A.size(0), K = A.size(1);
-    if (w.dim() != 3 || (w.scalar_type() != at::kByte && w.scalar_type() != at::kInt))
-        type_error("the experts' weights must be 3-D uint8 codes [E, N, K / 4] or int32 words [E, N, K / 8], got " + kind_of(w));
-    const bool w4 = w.scalar_type() == at::kInt;
+    const bool w4 = a[9] == Py_True;
+    if (w.dim() != 3 || w.scalar_type() != (w4 ? at::kInt : at::kByte))
+        type_error((w4 ? "qweight must be a 3-D int32 tensor [E, N, K / 8], got " : "codes must be a 3-D uint8 tensor [E, N, K / 4], got ") +
+                   kind_of(w));
     const int64_t E = w.size(0), N = w.size(1), G = K / 128;
     if (K % (w4 ? 128 : 64) != 0) value_error("K must be a multiple of " + std::to_string(w4 ? 128 : 64) + ", got " + std::to_string(K));
     whole_of(w4 ? "qweight" : "codes", w, w.scalar_type(), {E, N, w4 ? K / 8 : K / 4});
     if (w4) whole_of("scales", scale, at::kHalf, {E, N, G});
     else whole_of("scale", scale, at::kHalf, {E, N});
-    if (zeros) {
-        if (!w4) value_error("ternary weights have no zeros");
-        whole_of("zeros", *zeros, at::kByte, {E, N, G});
-    }
+    if (zeros) whole_of("zeros", *zeros, at::kByte, {E, N, G});
     vector("offsets", offsets, at::kInt, E + 1);
     int64_t P = T;
     if (rows) {

@@ -57,7 +57,7 @@ def tq_moe_gemm(A, codes, scale, offsets, rows=None, bias=None, gated: bool = Fa
     None: row(p) is p.  bias [E, N].  gated: the first N / 2 weight rows are the
     gate g, the others u, and C[p] = g / (1 + exp(-g)) * u, [P, N / 2].  Rows
     behind offsets[E] are not written."""
-    return _result("tq_moe_gemm", _entry().moe_gemm(A, codes, scale, None, offsets, rows, bias, gated, out))
+    return _result("tq_moe_gemm", _entry().moe_gemm(A, codes, scale, None, offsets, rows, bias, gated, out, False))
 
 
 def w4a16_moe_gemm(A, qweight, scales, offsets, rows=None, zeros=None, bias=None, group_size: int = 128,
@@ -66,7 +66,7 @@ def w4a16_moe_gemm(A, qweight, scales, offsets, rows=None, zeros=None, bias=None
     [E, N, K / 128] (any values) or None for 8."""
     if group_size != 128:
         _lib._check("w4a16_moe_gemm", 5)  # TQ_ERR_GROUP
-    return _result("w4a16_moe_gemm", _entry().moe_gemm(A, qweight, scales, zeros, offsets, rows, bias, gated, out))
+    return _result("w4a16_moe_gemm", _entry().moe_gemm(A, qweight, scales, zeros, offsets, rows, bias, gated, out, True))
 
 
 def tq_moe_combine(y, places, weights, add=None, out=None):
