@@ -13,6 +13,7 @@
 
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -616,6 +617,12 @@ PyObject* moe_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// The call has no backward pass: a tensor that wants a gradient would lose it.
+void no_gradient(const char* name, const Tensor* t) {
+    if (t && t->requires_grad() && at::GradMode::is_enabled())
+        value_error(std::string(name) + " requires a gradient, but tq_lora goes forward only: detach it or call under torch.no_grad()");
+}
+
 // (x, base, A, B, ids, scale, out)
 PyObject* lora(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -623,6 +630,12 @@ PyObject* lora(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor &x = tensor("x", a[0]), &base = tensor("base", a[1]), &A = tensor("A", a[2]), &B = tensor("B", a[3]),
                  &ids = tensor("ids", a[4]);
     const Tensor *scale = optional("scale", a[5]), *given = optional("out", a[6]);
+    no_gradient("x", &x);
+    no_gradient("base", &base);
+    no_gradient("A", &A);
+    no_gradient("B", &B);
+    no_gradient("scale", scale);
+    no_gradient("out", given);
     if (x.dim() != 2) type_error("x must be 2-D [T, K], got " + std::to_string(x.dim()) + "-D");
     const tq_dtype dt = half_type("x", x);
     const at::ScalarType type = x.scalar_type();

@@ -6,7 +6,8 @@ requests beside a shared projection.  Like the calls of serving.py these go
 through _serving.so (csrc/binding.cpp), which checks tensors' types, shapes,
 strides and devices, allocates what is not given and calls the entry points of
 the same names in include/tq.h: TypeError and ValueError come from its checks,
-TQError from the library's.  There is no CPU fallback.
+TQError from the library's.  There is no CPU fallback, and no backward pass:
+results carry no gradient.
 
     r = tq_moe_route(logits, top_k)
     h = w4a16_moe_gemm(x, w13, s13, r.offsets, rows=r.rows, gated=True)
@@ -82,5 +83,6 @@ def tq_lora(x, base, A, B, ids, scale=None, out=None):
 
     x [T, K] and base [T, N] fp16/bf16 (rows may be strided); A [L, r, K], B
     [L, N, r], r a multiple of 8 up to 256; ids int32 [T]; scale fp32 [L].  out may
-    be base: the update is then made in place."""
+    be base: the update is then made in place.  Forward only: a tensor that requires
+    a gradient is refused, unless gradients are off (torch.no_grad())."""
     return _result("tq_lora", _entry().lora(x, base, A, B, ids, scale, out))

@@ -17,3 +17,16 @@ def test_weights_of_the_other_format():
         tq.w4a16_moe_gemm(H(4, 128), U(2, 8, 32), H(2, 8), I(3))
     with pytest.raises(TypeError, match="qweight must be a 3-D int32 tensor"):
         tq.w4a16_moe_gemm(H(4, 128), U(2, 8, 32), H(2, 8), I(3), zeros=U(2, 8, 1))
+
+
+@pytest.mark.parametrize("i, name", [(0, "x"), (1, "base"), (2, "A"), (3, "B"), (5, "scale"), (6, "out")])
+def test_adapters_that_want_a_gradient(i, name):
+    """No gradient is lost in silence; without gradients the same tensors go on to the next check."""
+    args = [H(4, 64), H(4, 32), H(3, 16, 64), H(3, 32, 16), I(4), torch.zeros(3), H(4, 32)]
+    args[i].requires_grad_(True)
+    call = lambda: tq.tq_lora(*args[:5], scale=args[5], out=args[6])  # noqa: E731
+    with pytest.raises(ValueError, match=f"{name} requires a gradient"):
+        call()
+    for off in (torch.no_grad, torch.inference_mode):
+        with off(), pytest.raises(ValueError, match="device tensors"):
+            call()
