@@ -11,7 +11,7 @@ from ._lib import (TQ_WORKSPACE_FLAG_BYTES, TQError, load, new_workspace, tq_abi
                    tq_select_path, tq_unpack, w4a16_gemm, w4a16_gemm_asym_workspace_bytes,
                    w4a16_gemm_workspace_bytes, w4a16_pack, w4a16_pack_asym, w4a16_unpack, w4a16_unpack_asym)
 from .experts import (MoeRoute, tq_lora, tq_moe_combine, tq_moe_gemm, tq_moe_route, tq_moe_route_workspace_bytes,  # noqa: F401
-                      w4a16_moe_gemm)
+                      tq_moe_select_cut, w4a16_moe_gemm)
 from .layout import TernaryLayout, W4Layout  # noqa: F401
 from .serving import (PagedPlan, tq_kv_append, tq_paged_attention, tq_paged_attention_workspace_bytes,  # noqa: F401
                       tq_paged_plan, tq_sample)
@@ -25,5 +25,6 @@ __all__ = [
     "w4a16_pack_asym", "w4a16_unpack", "w4a16_unpack_asym", "TernaryLayout", "W4Layout",
     "PagedPlan", "tq_kv_append", "tq_paged_attention", "tq_paged_attention_workspace_bytes", "tq_paged_plan",
     "tq_sample",
-    "MoeRoute", "tq_lora", "tq_moe_combine", "tq_moe_gemm", "tq_moe_route", "tq_moe_route_workspace_bytes", "w4a16_moe_gemm",
+    "MoeRoute", "tq_lora", "tq_moe_combine", "tq_moe_gemm", "tq_moe_route", "tq_moe_route_workspace_bytes",
+    "tq_moe_select_cut", "w4a16_moe_gemm",
 ]

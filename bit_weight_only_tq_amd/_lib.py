@@ -60,6 +60,7 @@ SIGNATURES = {
     "tq_moe_gemm": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp]),
     "w4a16_moe_gemm": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _i32, _vp,
                               _vp]),
+    "tq_moe_select_cut": (_i32, [_i32, _i32, _i64, _i64, _i64, _i64]),
     "tq_moe_combine": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp]),
     "tq_lora": (_i32, [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
     "tq_diag_stream_read": (_i32, [_vp, _sz, _vp, _i64, _vp]),

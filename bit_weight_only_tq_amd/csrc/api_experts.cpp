@@ -15,14 +15,17 @@ bool route_sizes_ok(int64_t T, int64_t E, int64_t top_k) {
            T <= kInt32Max / top_k;
 }
 
+bool expert_sizes_ok(int fmt, int64_t P, int64_t E, int64_t N, int64_t K) {
+    return P >= 0 && P <= kInt32Max && E > 0 && E <= 65536 && N > 0 && N <= tq::kMaxK && K > 0 && K <= tq::kMaxK &&
+           K % (fmt == 0 ? 64 : 128) == 0 && N * K <= (int64_t)1 << 32;
+}
+
 // The checks and the launch of both formats' products.
 tq_status moe_gemm(const void* A, tq_dtype dt, int64_t T, int64_t P, int64_t E, int64_t N, int64_t K, int fmt,
                    const void* w, const uint16_t* scale, const uint8_t* zeros, const int32_t* offsets,
                    const int32_t* rows, const void* bias, int gated, void* C, hipStream_t stream) {
     if (dt != TQ_F16 && dt != TQ_BF16) return TQ_ERR_DTYPE;
-    if (T < 0 || T > kInt32Max || P < 0 || P > kInt32Max || E <= 0 || E > 65536 || N <= 0 || N > tq::kMaxK || K <= 0 ||
-        K > tq::kMaxK || K % (fmt == 0 ? 64 : 128) != 0 || (gated && N % 2 != 0) || N * K > (int64_t)1 << 32)
-        return TQ_ERR_SHAPE;
+    if (T < 0 || T > kInt32Max || !expert_sizes_ok(fmt, P, E, N, K) || (gated && N % 2 != 0)) return TQ_ERR_SHAPE;
     if (rows ? (T == 0 ? P != 0 : P % T != 0) : P != T) return TQ_ERR_SHAPE;
     if (P == 0) return TQ_OK;
     if (!A || !w || !scale || !offsets || !C) return TQ_ERR_NULL;
@@ -116,6 +119,11 @@ tq_status w4a16_moe_gemm(const void* A, tq_dtype dt, int64_t T, int64_t P, int64
                          hipStream_t stream) {
     if (group_size != 128) return TQ_ERR_GROUP;
     return moe_gemm(A, dt, T, P, E, N, K, 1, qweight, scales_f16, zeros, offsets, rows, bias, gated, C, stream);
+}
+
+int tq_moe_select_cut(int format, int zeros, int64_t P, int64_t E, int64_t N, int64_t K) {
+    if ((format != 0 && format != 1) || (format == 0 && zeros) || P < 1 || !expert_sizes_ok(format, P, E, N, K)) return -1;
+    return tq::select_cut(format, zeros != 0, P, E, N, K);
 }
 
 tq_status tq_moe_combine(const void* y, tq_dtype dt, int64_t T, int64_t P, int64_t N, int64_t top_k,

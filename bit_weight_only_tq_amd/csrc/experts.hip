@@ -5,6 +5,7 @@
 // for as many blocks of rows as P rows of E experts can make at most; each finds
 // its expert and rows by a scan over the offsets and leaves if there are none.
 
+#include "tq.h"
 #include "tq_device.h"
 #include "tq_internal.h"
 #include "tq_tiles.h"
@@ -851,6 +852,7 @@ constexpr Cut kCuts[] = {
     {64, 128, 1, 64, {1.35f, 0.93f, 1.28f}, {1.10f, 0.76f, 0.96f}},
     {tile::BM, tile::BN, 1, 0, {0.71f, 1.02f, 1.11f}, {0.85f, 1.13f, 1.09f}},
 };
+static_assert(sizeof(kCuts) / sizeof(kCuts[0]) == TQ_MOE_CUTS, "tq.h names the number");
 
 // The cut of the shortest estimated time: few rows waste the rows of a large
 // block, few blocks leave compute units idle, and a long row takes one workgroup
@@ -859,20 +861,20 @@ constexpr Cut kCuts[] = {
 // slower than the best of the nine in the mean and 38 % at worst; by rows an expert
 // alone it is 28 % and fivefold.  Without any one of them some call is 11 to 85 %
 // slower at best.
-int choose_cut(const ExpertArgs& a) {
-    const int kind = a.fmt == 0 ? 0 : a.zeros ? 2 : 1;
-    const int64_t used = a.P < a.E ? a.P : a.E;
-    const int first = a.fmt == 0 ? 0 : 1;
+int choose_cut(int fmt, bool zeros, int64_t P, int64_t E, int64_t N, int64_t K) {
+    const int kind = fmt == 0 ? 0 : zeros ? 2 : 1;
+    const int64_t used = P < E ? P : E;
+    const int first = fmt == 0 ? 0 : 1;
     int best = first;
     double best_time = 0;
-    for (int i = first; i < (int)(sizeof(kCuts) / sizeof(kCuts[0])); ++i) {
+    for (int i = first; i < TQ_MOE_CUTS; ++i) {
         const Cut& c = kCuts[i];
         const bool tiled = c.rows == tile::BM;
-        const int64_t bk = tiled ? tile::BK : c.bytes * (a.fmt == 0 ? 4 : 2);
-        const int64_t steps = ((a.K + bk - 1) / bk + c.parts - 1) / c.parts;
+        const int64_t bk = tiled ? tile::BK : c.bytes * (fmt == 0 ? 4 : 2);
+        const int64_t steps = ((K + bk - 1) / bk + c.parts - 1) / c.parts;
         // an expert's last block is half full; experts of fewer rows than that have one
-        const double full = (double)a.P / (double)(used * c.rows) + 0.5;
-        const double share = (full > 1.0 ? full : 1.0) * (double)(used * ((a.N + c.weights - 1) / c.weights)) / compute_units();
+        const double full = (double)P / (double)(used * c.rows) + 0.5;
+        const double share = (full > 1.0 ? full : 1.0) * (double)(used * ((N + c.weights - 1) / c.weights)) / compute_units();
         const double step = share * c.shared[kind] > c.alone[kind] ? share * c.shared[kind] : c.alone[kind];
         // steps' worth of filling the ring and of the results, and the start
         const double time = (double)(steps + (tiled ? 6 : 2)) * step + (tiled ? 5.5 : 2.5);
@@ -892,7 +894,7 @@ hipError_t launch_cut(const ExpertArgs& a, hipStream_t s) {
 
 template <class T, int FMT, bool ASYM, bool GATED>
 hipError_t launch_rows(const ExpertArgs& a, hipStream_t s) {
-    const int cut = choose_cut(a);
+    const int cut = choose_cut(a.fmt, a.zeros != nullptr, a.P, a.E, a.N, a.K);
     if constexpr (FMT == 0) {
         if (cut == 0) return launch_cut<T, FMT, ASYM, GATED, 0>(a, s);
     }
@@ -916,6 +918,8 @@ hipError_t launch_type(const ExpertArgs& a, hipStream_t s) {
 }
 
 }  // namespace
+
+int select_cut(int fmt, bool zeros, int64_t P, int64_t E, int64_t N, int64_t K) { return choose_cut(fmt, zeros, P, E, N, K); }
 
 hipError_t launch_experts(const ExpertArgs& a, hipStream_t s) {
     return a.bf16 ? launch_type<BF16>(a, s) : launch_type<F16>(a, s);

@@ -306,6 +306,7 @@ struct ExpertArgs {
     int64_t first = 0;      // workgroup that this launch begins with (set by the launcher)
 };
 hipError_t launch_experts(const ExpertArgs& a, hipStream_t s);
+int select_cut(int fmt, bool zeros, int64_t P, int64_t E, int64_t N, int64_t K);
 
 // lora.hip: arguments as tq_lora.  A block's rows and an adapter's matrices are
 // addressed with 31 bits.

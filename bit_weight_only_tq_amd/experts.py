@@ -70,6 +70,11 @@ def w4a16_moe_gemm(A, qweight, scales, offsets, rows=None, zeros=None, bias=None
     return _result("w4a16_moe_gemm", _entry().moe_gemm(A, qweight, scales, zeros, offsets, rows, bias, gated, out, True))
 
 
+def tq_moe_select_cut(fmt: str, P: int, E: int, N: int, K: int, zeros: bool = False) -> int:
+    """Which of the library's cuts into workgroups a product of these sizes takes ("ternary", "w4a16"); -1: refused."""
+    return int(_lib.load().tq_moe_select_cut({"ternary": 0, "w4a16": 1}[fmt], int(zeros), P, E, N, K))
+
+
 def tq_moe_combine(y, places, weights, add=None, out=None):
     """out[t] = add[t] + sum over j of weights[t, j] * y[places[t, j]]; -> [T, N].
 

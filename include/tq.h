@@ -696,6 +696,16 @@ tq_status tq_diag_gemv(const void* A, tq_dtype dt, int64_t M, int64_t N, int64_t
  */
 tq_path tq_select_path(int format, int64_t M, int64_t N, int64_t K, tq_dtype dt);
 
+/*
+ * tq_moe_select_cut - how tq_moe_gemm (format 0) and w4a16_moe_gemm (format 1,
+ * with zero points or without) cut P rows of E experts into workgroups: 0 ..
+ * TQ_MOE_CUTS - 1 in the order of the library's table, by rows of a block; -1 for
+ * sizes that the calls refuse.  The choice also goes by the device's compute
+ * units, not by the activations' type, the rows' order or the gate.
+ */
+#define TQ_MOE_CUTS 9
+int tq_moe_select_cut(int format, int zeros, int64_t P, int64_t E, int64_t N, int64_t K);
+
 /* Static string for a status code (never NULL). */
 const char* tq_status_str(tq_status s);
 
