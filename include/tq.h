@@ -591,8 +591,9 @@ size_t tq_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t top_k);
  *   C        (written) rounded once from fp32; rows behind offsets[E] are left
  *            as they were.  It must not overlap anything that is read
  *            (TQ_ERR_VALUE).
- * Offsets are held to [0, P] and rows to [0, P); where they are not what
- * tq_moe_route writes, which rows of C are written is unspecified.
+ * Offsets are held to [0, P] and rows to [0, P).  Where the rows of two experts
+ * overlap, theirs are unspecified, and where the offsets name more than P rows in
+ * all, any value of C may be left as it was.
  * K % 64 == 0, K and N at most 2^22, N * K at most 2^32, E <= 65536, N even if
  * gated.  A and codes are 16-byte aligned.  How a row's sum is cut and in which
  * order its parts are added depends on P, E, N, K, the weights' format and the
