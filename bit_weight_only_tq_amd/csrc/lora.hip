@@ -167,6 +167,11 @@ __device__ __forceinline__ void update(const LoraArgs& a, int64_t t0, uint32_t c
         from_row[m] = live ? (uint32_t)((16 * m + i16) * a.base_stride + 8 * g) * 2u : kNowhere;
         to_row[m] = live ? (uint32_t)((16 * m + i16) * a.out_stride + 8 * g) * 2u : kNowhere;
     }
+    uint32_t b_lane[2][kKs];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int st = 0; st < kKs; ++st) b_lane[t][st] = lora_b_lane(a.r, i16, g, t, st);
     // Output columns n .. n + 31
     struct Cols {
         u32x4 b[2][kKs], base[MB];
@@ -177,7 +182,7 @@ __device__ __forceinline__ void update(const LoraArgs& a, int64_t t0, uint32_t c
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int st = 0; st < kKs; ++st)
-                    c.b[t][st] = __builtin_amdgcn_raw_buffer_load_b128(bbuf, lora_b_offset(n, a.r, i16, g, t, st), 0, 0);
+                    c.b[t][st] = __builtin_amdgcn_raw_buffer_load_b128(bbuf, b_lane[t][st] + lora_b_step(a.r, n), 0, 0);
         }
 #pragma unroll
         for (int m = 0; m < MB; ++m)

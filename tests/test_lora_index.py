@@ -16,6 +16,7 @@ SOURCE = r"""
 #include "tq_lora_index.h"
 #include <vector>
 // 0, or the number of the rule that a read breaks.  seen[n]: how many lanes took column n's ranks 0 .. 7.
+extern "C" uint32_t offset(int r, int n, int i16, int g, int t, int st) { return tq::lora_b_lane(r, i16, g, t, st) + tq::lora_b_step(r, n); }
 extern "C" int walk(int N, int r, int RT, int W, int cols, int* seen) {
     const int kKs = (RT + 1) / 2;
     const uint32_t bytes = (uint32_t)N * (uint32_t)r * 2u;
@@ -28,7 +29,7 @@ extern "C" int walk(int N, int r, int RT, int W, int cols, int* seen) {
                     for (int t = 0; t < 2; ++t)
                         for (int st = 0; st < kKs; ++st) {
                             const int g = lane >> 4, i16 = lane & 15, row = n + 8 * (i16 >> 2) + 4 * t + (i16 & 3);
-                            const uint32_t off = tq::lora_b_offset(n, r, i16, g, t, st);
+                            const uint32_t off = offset(r, n, i16, g, t, st);
                             const bool wanted = row < N && 32 * st + 8 * g < r;
                             if (wanted && off != ((uint32_t)row * r + 32 * st + 8 * g) * 2u) return 1;
                             if (wanted && off + 16 > bytes) return 2;
@@ -43,7 +44,7 @@ extern "C" int walk(int N, int r, int RT, int W, int cols, int* seen) {
 
 
 @pytest.fixture(scope="module")
-def walk(tmp_path_factory):
+def library(tmp_path_factory):
     cxx = shutil.which("g++") or shutil.which("c++")
     if not cxx:
         pytest.skip("no C++ compiler")
@@ -51,17 +52,19 @@ def walk(tmp_path_factory):
     source, lib = folder / "walk.cpp", folder / "walk.so"
     source.write_text(SOURCE)
     subprocess.run([cxx, "-O1", "-std=c++17", "-shared", "-fPIC", "-I", build.CSRC, str(source), "-o", str(lib)], check=True)
-    return ctypes.CDLL(str(lib)).walk
+    loaded = ctypes.CDLL(str(lib))
+    loaded.offset.restype = ctypes.c_uint32
+    return loaded
 
 
 @pytest.mark.parametrize("RT, W, ranks", [(1, 16, (8, 16)), (1, 8, (8, 16)), (2, 8, (24, 32)), (4, 8, (40, 48, 64)), (8, 8, (72, 128)),
                                           (16, 8, (136, 256))])
 @pytest.mark.parametrize("N", [1, 7, 8, 31, 33, 100, 513, 1025, 4096, 4101])
-def test_reads_of_b(walk, RT, W, ranks, N):
+def test_reads_of_b(library, RT, W, ranks, N):
     for r in ranks:
         for passes in (1, 2, 3, 9):
             seen = (ctypes.c_int * N)()
-            assert walk(N, r, RT, W, 32 * W * passes, seen) == 0
+            assert library.walk(N, r, RT, W, 32 * W * passes, seen) == 0
             assert all(s == 1 for s in seen)  # each column by one lane
 
 
@@ -69,4 +72,18 @@ def test_the_kernel_reads_b_through_it():
     """No scalar offset on the loads of B: that is not part of the bounds check."""
     text = open(os.path.join(build.CSRC, "lora.hip")).read()
     assert text.count("raw_buffer_load_b128(bbuf") == 1
-    assert "raw_buffer_load_b128(bbuf, lora_b_offset(n, a.r, i16, g, t, st), 0, 0)" in text
+    assert "raw_buffer_load_b128(bbuf, b_lane[t][st] + lora_b_step(a.r, n), 0, 0)" in text
+    assert "b_lane[t][st] = lora_b_lane(a.r, i16, g, t, st)" in text
+
+
+def test_the_largest_matrix(library):
+    """2^29 values: the last row is read, rows and ranks that are not there lie past the end, without wrapping."""
+    end = 1 << 30
+    for r, N in ((128, 1 << 22), (256, 1 << 21)):
+        for n in range(N - 32, N + 512, 32):
+            for i16 in range(16):
+                for t in (0, 1):
+                    row = n + 8 * (i16 >> 2) + 4 * t + (i16 & 3)
+                    off = library.offset(r, n, i16, 3, t, r // 32 - 1)
+                    assert off == (row * r + r - 8) * 2 and (off < end) == (row < N)
+        assert all(library.offset(r - 8, n, 15, 3, 1, r // 32 - 1) >= end for n in (0, N - 32, N + 480))
