@@ -186,9 +186,10 @@ __device__ __forceinline__ Place find_tile(const ExpertArgs& a, int BM, uint32_t
 // rows x 64 bytes an instruction, a compute unit gets 37 GB/s from its L2, in lines
 // of 128 bytes 119 GB/s.  So codes and activations go to LDS by DMA, a step of RB
 // code bytes a row (128, or 64 where 16 rows of activations and more need the room:
-// two workgroups a compute unit instead of one hide more than half lines cost, 53
-// instead of 55 us for 48 tokens of 64 experts and 67 instead of 87 for 1010 of 87),
-// into a ring of two steps (three: 65 instead of 58 us, for half the workgroups):
+// more workgroups a compute unit hide more than half lines cost, 52.4 instead of 55.2
+// us for 48 tokens of 64 experts in blocks of 16 and 57 instead of 67 in blocks of 32),
+// into a ring of two steps (three gain nothing where they halve the workgroups, 52.0
+// and 52.2 us, nor for one ternary token, 20.9 and 19.6, where as many fit):
 //  - codes: [32 rows a wave][RB / 16 chunks of 16 bytes], chunk c of row r at
 //    c ^ (r / 2 % 8), or c ^ (r / 4 % 4) of 64 bytes;
 //  - activations: [BM rows][BK columns], chunk c of row r at c ^ (r % 16).
@@ -858,9 +859,8 @@ static_assert(sizeof(kCuts) / sizeof(kCuts[0]) == TQ_MOE_CUTS, "tq.h names the n
 // block, few blocks leave compute units idle, and a long row takes one workgroup
 // many steps.  kCuts was fitted to every cut's time for 253 calls (1 to 4096
 // tokens, 1 to 120 experts, 512 to 14336 columns): the one taken here is 3 %
-// slower than the best of the nine in the mean and 38 % at worst; by rows an expert
-// alone it is 28 % and fivefold.  Without any one of them some call is 11 to 85 %
-// slower at best.
+// slower than the best of the nine in the mean and 38 % at worst (80 other calls: 3 %
+// and 35 %); by rows an expert alone it is 28 % and fivefold.
 int choose_cut(int fmt, bool zeros, int64_t P, int64_t E, int64_t N, int64_t K) {
     const int kind = fmt == 0 ? 0 : zeros ? 2 : 1;
     const int64_t used = P < E ? P : E;

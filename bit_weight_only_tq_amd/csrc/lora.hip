@@ -17,9 +17,9 @@
 // faster, 75 instead of 77 us for 8191 rows of rank 64, but one output in 600 is then
 // not what the fp32 sum rounds to.)
 //
-// What bounds it: a decoding row's call two trips to memory (ids, then all else): 8.5
+// What bounds it: a decoding row's call two trips to memory (ids, then all else): 8.9
 // us for one row of rank 16, 4096 x 4096; 64 rows of 32 adapters, 6144 x 4096, the
-// adapters' reads through L2, 11 us; a prompt the rows' loads, see below.
+// adapters' reads through L2, 11.5 us; a prompt the rows' loads, see below.
 //
 // Rows of any alignment are read and written in 16-byte vectors (the memory mode of
 // this platform allows any address), but for the last columns of a row.
@@ -384,7 +384,7 @@ __global__ __launch_bounds__(W * kWave) void lora_kernel(LoraArgs a) {
 // takes the place of base in LDS and leaves from there, in lines again.
 // Rows and ranks past the end are the last one again (ranks past it count as 0).
 // Needs N % 8 == 0 and 16-byte aligned rows.  Measured: 8191 rows of 5 prompts, 4096
-// x 4096, rank 64, 79 us (direct loads 123), 2.5 TB/s of rows; of one prompt 56: a
+// x 4096, rank 64, 81 us (direct loads 109), 2.4 TB/s of rows; of one prompt 55: a
 // block in which a prompt ends has two adapters and takes twice as long as the
 // others, one a compute unit, that wait for it.
 template <int RT>
@@ -671,6 +671,10 @@ __global__ __launch_bounds__(Stage<RT>::W * kWave) void staged_kernel(LoraArgs a
     } while (left);
 }
 
+// Up to so many rows a block's adapters are spread over workgroups; beyond, the rows
+// are taken for prompts, few adapters a block, and one workgroup takes them in turn.
+// For rows that each have another adapter that is slow: 256 rows of 32 adapters, rank
+// 16, 4096 x 4096, 17 us and 257 rows 104; sorted by adapter, 512 rows take 14.
 constexpr int64_t kLoraDecodeRows = 256;
 
 // Columns of a workgroup, in whole passes of its waves.  Each workgroup makes the
@@ -679,8 +683,8 @@ constexpr int64_t kLoraDecodeRows = 256;
 // one.  How many of a block's slots have an adapter is known on the device alone:
 // the sum of the times for one and for all of them is what is made small.  (Two
 // workgroups a compute unit in any case: 64 rows of 32 adapters, 6144 x 4096, rank
-// 16, 18.7 us instead of 11.5; one in any case: 229 rows of 10 prompts, 8840 x 704,
-// 22 instead of 14.)
+// 16, 19.4 us instead of 11.6; one in any case: 229 rows of 10 prompts, 8840 x 704,
+// 22.3 instead of 11.2.)
 int64_t chunk_columns(const LoraArgs& a, int64_t pass) {
     const int64_t passes = (a.N + pass - 1) / pass, units = compute_units();
     int64_t best = 0;
@@ -764,8 +768,8 @@ hipError_t launch_staged(const LoraArgs& args, hipStream_t s) {
 }
 
 // Rows of whole 16-byte vectors go through LDS where a block of 32 has few
-// adapters (300 rows of 3 prompts, 4096 x 4096, rank 64: 24 us instead of 42; rank
-// 16 from 2048 rows on, 1200 rows 24 and 22).  Else, for many rows, blocks of 32
+// adapters (300 rows of 3 prompts, 4096 x 4096, rank 64: 25 us instead of 43; rank
+// 16 from 2048 rows on, 1200 rows 25 and 22.5).  Else, for many rows, blocks of 32
 // read an adapter half as often as those of 16.  Few rows of a small rank: 16 waves,
 // so that one pass of loads covers 4096 columns.
 template <class T>

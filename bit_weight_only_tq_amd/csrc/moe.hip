@@ -14,8 +14,8 @@
 // tokens are routed and sorted by one workgroup; beyond, a first launch routes
 // chunks of tokens and leaves each chunk's counts in the workspace, and a second
 // one, a workgroup a chunk again, sums the counts before its own.  Bound by latency:
-// 1 token of 8 experts 4.5 us, 64 tokens of 64 experts, 8 chosen, 6.3 us and 65 tokens
-// 8.8, 16383 of 128 14 us (a launch 2.5).
+// 1 token of 8 experts 5.5 us (the kernel 4.1), 64 tokens of 64 experts, 8 chosen, 6.3
+// and 65 tokens 9.9, 16383 of 128 14 us (a launch 2.5).
 
 #include "tq_device.h"
 #include "tq_internal.h"
@@ -425,7 +425,7 @@ hipError_t route_variant(const RouteArgs& a, hipStream_t s) {
 }
 
 // 16 lanes a token as long as they hold its logits and its choices: 2048 tokens of
-// 64 experts, 8 chosen, 9.6 us with 16 lanes and 28 with 64; 16383 of 200, 20 and 36.
+// 64 experts, 8 chosen, 10.5 us with 16 lanes and 28 with 64; 16383 of 200, 21 and 36.
 template <class L>
 hipError_t route_type(const RouteArgs& a, hipStream_t s) {
     if (a.E > 256 || a.k > 16) return route_variant<L, 64, 16>(a, s);

@@ -41,7 +41,7 @@ def tq_moe_route_workspace_bytes(T: int, E: int, top_k: int) -> int:
 def tq_moe_route(logits, top_k: int, renormalize: bool = True, out: MoeRoute = None, workspace="auto") -> MoeRoute:
     """The top_k experts of each token, their weights, and the pairs sorted by expert.
 
-    logits [T, E] fp16, bf16 or fp32 (rows may be strided), E <= 1024, top_k <= 64;
+    logits [T, E] fp16, bf16 or fp32 (rows may be strided), T >= 1, E <= 1024, top_k <= 64;
     weights: softmax over the chosen experts, or over all with renormalize=False.
     out: a MoeRoute to write into.  workspace: "auto", or a contiguous device
     tensor of tq_moe_route_workspace_bytes bytes, of any contents (None where
